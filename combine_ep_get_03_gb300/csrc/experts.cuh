@@ -1,0 +1,223 @@
+// What the experts' kernels share: groups of rows as dispatch leaves them,
+// e4m3 rows with a scale for every 128 channels, and waits that end.
+#pragma once
+
+#include "device_common.cuh"
+
+namespace ep {
+
+constexpr int kMaxGroups = 4096;
+
+// Groups of rows: group g holds count[g] rows from offset[g], or from
+// g * rows_per_group where offset is null.
+struct GroupArgs {
+  const int* count;
+  const int* offset;
+  int G;
+  long long rows;            // rows of every row buffer
+  long long rows_per_group;  // with offset null
+  int* err;                  // status word or null
+};
+
+// e4m3 rows: the scale of row r, channels [128 g, 128 g + 128) is
+// scales[r * row_stride + g * group_stride].
+struct Fp8Rows {
+  unsigned char* data;
+  float* scales;
+  long long row_stride, group_stride;
+  __device__ __forceinline__ float* scale(long long r, int g) const {
+    return scales + r * row_stride + g * group_stride;
+  }
+};
+
+__device__ __forceinline__ void latch_status(int* err, int code) {
+  if (err) latch_error(err, code);
+}
+
+// First row and row count of group g.  A group that does not fit its slots or
+// the row buffer is cut to what does (EP_ERR_CAPACITY, latched by `report`).
+__device__ __forceinline__ int group_span(const GroupArgs& a, int g, long long* start, bool report) {
+  const long long first = a.offset ? static_cast<long long>(a.offset[g]) : g * a.rows_per_group;
+  long long n = a.count[g];
+  long long most = a.offset ? a.rows - first : a.rows_per_group;
+  if (first < 0 || most < 0) most = 0;
+  if (n < 0) n = 0;
+  if (n > most) {
+    n = most;
+    if (report) latch_status(a.err, kErrCapacity);
+  }
+  *start = first;
+  return static_cast<int>(n);
+}
+
+// prefix[g] = tiles of `tile_rows` rows in the groups before g, prefix[G] =
+// all of them (saturating), for the whole block; `sums` holds 32 words.
+__device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows, unsigned* prefix, unsigned* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int per = (a.G + blockDim.x - 1) / blockDim.x;
+  const int g0 = tid * per;
+  auto add = [](unsigned x, unsigned y) {
+    const unsigned s = x + y;
+    return s < x || s > 0x7fffffffu ? 0x7fffffffu : s;
+  };
+  unsigned mine = 0;
+  for (int g = g0; g < g0 + per && g < a.G; ++g) {
+    long long first;
+    const int n = group_span(a, g, &first, blockIdx.x == 0);
+    const unsigned t = static_cast<unsigned>((static_cast<long long>(n) + tile_rows - 1) / tile_rows);
+    prefix[g] = t;
+    mine = add(mine, t);
+  }
+  unsigned incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned v = __shfl_up_sync(kFullMask, incl, d);
+    if (lane >= d) incl = add(incl, v);
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  unsigned base = 0, all = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) base = add(base, sums[w]);
+    all = add(all, sums[w]);
+  }
+  unsigned before = __shfl_up_sync(kFullMask, incl, 1);
+  before = add(base, lane ? before : 0u);
+  for (int g = g0; g < g0 + per && g < a.G; ++g) {
+    const unsigned t = prefix[g];
+    prefix[g] = before;
+    before = add(before, t);
+  }
+  if (tid == 0) prefix[a.G] = all;
+  __syncthreads();
+}
+
+// The group that item i (< prefix[G]) belongs to.
+__device__ __forceinline__ int find_group(const unsigned* prefix, int G, unsigned i) {
+  int lo = 0, hi = G;  // prefix[lo] <= i < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Bounded wait on an mbarrier phase for kernels whose warps wait on one
+// another: one that gives up latches EP_ERR_TIMEOUT and raises `quit`, which
+// ends every other warp's wait too.
+__device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, volatile int* quit, int* err) {
+  const uint32_t addr = smem_u32(bar);
+  for (int it = 0; it < kSpinLimit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (it >= 64) {
+      if (*quit) return false;
+      __nanosleep(32);
+    }
+  }
+  *quit = 1;
+  latch_status(err, kErrTimeout);
+  return false;
+}
+
+// 32 bytes from registers, as one store where the address allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :
+                 : "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Four e4m3 codes of one word as fp32 (exact).
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
+  uint32_t lo, hi;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n" : "=f"(f[0]), "=f"(f[1]) : "r"(lo));
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n" : "=f"(f[2]), "=f"(f[3]) : "r"(hi));
+}
+
+// Four fp32 -> four e4m3 codes, each the saturating nearest-even image of x * inv.
+__device__ __forceinline__ uint32_t quant4(const float* x, float inv) {
+  return pack_e4m3x2(x[0] * inv, x[1] * inv) | (pack_e4m3x2(x[2] * inv, x[3] * inv) << 16);
+}
+
+// A 128-channel group's scale and inverse from its largest magnitude, as
+// dispatch quantises: a = max(amax, 1e-4), scale = a / 448, inv = 448 / a.
+__device__ __forceinline__ float group_scale(float amax, float* inv) {
+  const float a = fmaxf(amax, 1e-4f);
+  *inv = __fdiv_rn(448.0f, a);
+  return __fdiv_rn(a, 448.0f);
+}
+
+// ------------------------------------------------------------------ launches
+
+struct GateArgs {
+  const void* logits;  // [T][ld] fp32 or bf16
+  long long ld;
+  const uint8_t* mask;  // [T] or null: 0 = padding token
+  int T, E, k, groups, keep, sigmoid, ids32, vec;
+  float coef;
+  void* idx;       // [T][k]
+  float* weights;  // [T][k]
+  int* count;      // [E + 1]
+  float* prob;     // [E]
+  float* loss;     // [1]
+  unsigned* work;  // zeroed; left zeroed
+  // backward
+  const float* grad_weights;  // [T][k] or null
+  const float* grad_loss;     // [1] or null
+  void* grad_logits;          // [T][grad_ld], the logits' type
+  long long grad_ld;
+};
+
+struct SwigluBackwardArgs {
+  GroupArgs groups;
+  const uint16_t* grad_act;  // bf16 [rows][F]
+  Fp8Rows pre;               // [rows][2F]
+  const float* row_weights;  // [rows] or null
+  Fp8Rows grad_pre;          // [rows][2F]
+  float* grad_row_weights;   // [rows] or null
+  int F;
+};
+
+// One grouped product; act.data selects the SwiGLU epilogue (N = 2F then).
+struct MatmulArgs {
+  GroupArgs groups;
+  Fp8Rows x;             // [rows][K]
+  const void* w;         // e4m3 [G][N][K]
+  const float* w_scales; // [G][ceil(N/128)][K/128]
+  int N, K;
+  uint16_t* out;            // bf16 [rows][N], or null
+  Fp8Rows act;              // [rows][F]
+  Fp8Rows pre;              // [rows][2F], data null if not kept
+  const float* row_weights; // [rows] or null
+};
+
+// dw[g] = sum over the group's rows of dy^T x.
+struct WeightGradArgs {
+  GroupArgs groups;
+  Fp8Rows dy;  // [rows][N]
+  Fp8Rows x;   // [rows][K]
+  int N, K;
+  uint16_t* dw;  // bf16 [G][N][K]
+};
+
+cudaError_t launch_gate(const GateArgs& p, bool bf16, bool backward, int sms, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& p, int sms, cudaStream_t stream);
+cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream);
+cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream);
+size_t gate_work_bytes(int E);
+
+}  // namespace ep

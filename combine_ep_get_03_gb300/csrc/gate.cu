@@ -1,0 +1,400 @@
+// The gate: top-k choice of experts, their weights, per-expert counts and the
+// balance loss; and the gradient of both with respect to the logits.
+//
+// Per token t with logits l (fp32 arithmetic whatever their type):
+//   choice   the k largest logits (of the topk_groups groups with the largest
+//            maxima), ties to the lower index; -inf and NaN are never chosen
+//   softmax  w_j = exp(l_j) / sum_chosen exp(l),  p_e = exp(l_e) / sum_E exp(l)
+//   sigmoid  s = 1/(1+exp(-l)), w_j = s_j / sum_chosen s, p_e = s_e / sum_E s
+// and over the V unmasked tokens, with c_e entries of expert e:
+//   P_e = sum_t p_te / V,   loss = coef E / (k V) sum_e c_e P_e.
+// Backward (r_e = 1 for softmax, 1 - s_e for sigmoid):
+//   dl_e  = dloss coef E / (k V^2) p_e r_e (c_e - sum_j p_j c_j)
+//         + [e chosen] w_e r_e (dw_e - sum_chosen w dw).
+//
+// A warp owns a token and a lane VPL consecutive experts in registers, so a
+// lane's experts are the same for every token and the column sums P stay in
+// registers until the block ends; lane order is index order, which settles
+// ties by the first lane of a ballot.  Blocks join their sums as 64-bit fixed
+// point (2^-36), which makes the result independent of their order, and the
+// last block to finish writes counts, P and the loss: one launch.
+#include <math_constants.h>
+
+#include "ep_internal.h"
+#include "experts.cuh"
+
+namespace ep {
+
+constexpr int kGateWarps = 8;
+constexpr double kFixed = 68719476736.0;  // 2^36
+
+// work: [0] finished blocks, [1] set if a row had no finite sum, [2] unmasked
+// tokens, [3] unused, then E u64 sums, then E counts
+__device__ __forceinline__ unsigned long long* work_sums(unsigned* w) {
+  return reinterpret_cast<unsigned long long*>(w + 4);
+}
+__device__ __forceinline__ int* work_counts(unsigned* w, int E) { return reinterpret_cast<int*>(w + 4 + 2 * E); }
+
+// Order-preserving image of a float; 0 for what is never chosen.
+__device__ __forceinline__ unsigned order_key(float v) {
+  if (!(v > -CUDART_INF_F)) return 0u;
+  const unsigned b = __float_as_uint(v + 0.0f);  // -0 and +0 tie
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p);
+template <>
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// The lane's VPL logits of a row, -inf past E.
+template <typename T, int VPL>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec, float* v) {
+  constexpr int kChunk = 16 / sizeof(T);
+  const int e0 = lane * VPL;
+  if constexpr (VPL % kChunk == 0) {
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += kChunk) {
+        if (e0 + j < E) {
+          const uint4 q = *reinterpret_cast<const uint4*>(row + e0 + j);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i)
+            v[j + i] = sizeof(T) == 4 ? __uint_as_float(w[i & 3]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) v[j + i] = -CUDART_INF_F;
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) v[j] = e0 + j < E ? load_logit(row + e0 + j) : -CUDART_INF_F;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kFullMask, x, d);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, d));
+  return x;
+}
+
+// Unnormalised score of a logit: exp(v - m) for softmax with m the largest
+// logit; for sigmoid exp(min(v,0) - m) / (1 + exp(-|v|)) with m the largest
+// min(v,0), which stays away from 0/0 when every sigmoid underflows.
+__device__ __forceinline__ float score_of(float v, float m, int sigmoid) {
+  if (!sigmoid) return expf(v - m);
+  return expf(fminf(v, 0.0f) - m) / (1.0f + expf(-fabsf(v)));
+}
+__device__ __forceinline__ float score_base(float vmax, int sigmoid) {
+  const float m = sigmoid ? fminf(vmax, 0.0f) : vmax;
+  return m == -CUDART_INF_F ? 0.0f : m;
+}
+// 1 for softmax, 1 - sigmoid(v) for sigmoid
+__device__ __forceinline__ float slope_of(float v, int sigmoid) { return sigmoid ? 1.0f / (1.0f + expf(v)) : 1.0f; }
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs p) {
+  extern __shared__ float sm[];  // [E] sums, then [E] counts, then [warps][groups] keys
+  float* s_sum = sm;
+  int* s_count = reinterpret_cast<int*>(sm + p.E);
+  unsigned* s_group = reinterpret_cast<unsigned*>(sm + 2 * p.E) + (threadIdx.x >> 5) * p.groups;
+  __shared__ int s_live, s_bad, s_last;
+  __shared__ float s_part[kGateWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.E, k = p.k;
+  for (int e = tid; e < E; e += blockDim.x) s_sum[e] = 0.0f, s_count[e] = 0;
+  if (tid == 0) s_live = 0, s_bad = 0;
+  __syncthreads();
+
+  float acc[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) acc[j] = 0.0f;
+  int live = 0;
+  bool bad = false;
+  const int gs = E / p.groups;
+  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+    int my_id = -1;
+    float my_w = 0.0f;
+    if (!p.mask || p.mask[t]) {
+      ++live;
+      float v[VPL], c[VPL];
+      load_row<T, VPL>(static_cast<const T*>(p.logits) + t * p.ld, E, lane, p.vec, v);
+      // probabilities over all experts
+      float m = -CUDART_INF_F;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+      m = score_base(warp_max(m), p.sigmoid);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        c[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+        sum += c[j];
+      }
+      sum = warp_sum(sum);
+      bad |= !(sum < CUDART_INF_F);
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // a row of -inf has no probability
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) acc[j] = fmaf(c[j], inv, acc[j]);
+
+      // candidates
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) c[j] = v[j];
+      if (p.groups > 1) {
+        for (int g = lane; g < p.groups; g += 32) s_group[g] = 0u;
+        __syncwarp();
+        {
+          int g = min(lane * VPL, E - 1) / gs, left = (g + 1) * gs - lane * VPL;
+          unsigned best = 0u;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) {
+            if (lane * VPL + j < E) {
+              if (left == 0) {
+                atomicMax(&s_group[g], best);
+                best = 0u, ++g, left = gs;
+              }
+              best = max(best, order_key(v[j]));
+              --left;
+            }
+          }
+          if (lane * VPL < E) atomicMax(&s_group[g], best);
+        }
+        __syncwarp();
+        // lane l ranks groups 2l and 2l + 1; a group's key + 1 keeps 0 for "taken or absent"
+        unsigned long long kept = 0ull;
+        unsigned g0 = 2 * lane < p.groups ? max(s_group[2 * lane], 1u) : 0u;
+        unsigned g1 = 2 * lane + 1 < p.groups ? max(s_group[2 * lane + 1], 1u) : 0u;
+        for (int i = 0; i < p.keep; ++i) {
+          const unsigned best = __reduce_max_sync(kFullMask, max(g0, g1));
+          const unsigned who = __ballot_sync(kFullMask, max(g0, g1) == best);
+          const int src = __ffs(who) - 1;
+          const int g = __shfl_sync(kFullMask, 2 * lane + (g0 == best ? 0 : 1), src);
+          kept |= 1ull << g;
+          if (lane == src) {
+            if (g0 == best) g0 = 0u; else g1 = 0u;
+          }
+        }
+        int g = min(lane * VPL, E - 1) / gs, left = (g + 1) * gs - lane * VPL;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          if (left == 0) ++g, left = gs;
+          if (!((kept >> (g & 63)) & 1ull)) c[j] = -CUDART_INF_F;
+          --left;
+        }
+        __syncwarp();
+      }
+      // the k largest, one after another
+      unsigned best = 0u;
+      int at = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const unsigned key = order_key(c[j]);
+        if (key > best) best = key, at = j;
+      }
+      float my_v = -CUDART_INF_F;
+      for (int i = 0; i < k; ++i) {
+        const unsigned top = __reduce_max_sync(kFullMask, best);
+        if (top == 0u) break;
+        const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        const int id = __shfl_sync(kFullMask, lane * VPL + at, src);
+        if (lane == i) {
+          my_id = id;
+          my_v = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
+        }
+        if (lane == src) {
+          const int gone = at;
+          best = 0u;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) {
+            if (j == gone) c[j] = -CUDART_INF_F;
+            const unsigned key = order_key(c[j]);
+            if (key > best) best = key, at = j;
+          }
+        }
+      }
+      const float top_v = __shfl_sync(kFullMask, my_v, 0);
+      const float s = my_id >= 0 ? score_of(my_v, score_base(top_v, p.sigmoid), p.sigmoid) : 0.0f;
+      const float s_all = warp_sum(s);
+      my_w = my_id >= 0 ? s / s_all : 0.0f;
+      if (my_id >= 0) atomicAdd(&s_count[my_id], 1);
+    }
+    if (lane < k) {
+      const long long o = static_cast<long long>(t) * k + lane;
+      if (p.ids32) static_cast<int*>(p.idx)[o] = my_id; else static_cast<long long*>(p.idx)[o] = my_id;
+      p.weights[o] = my_w;
+    }
+  }
+  // the block's sums, warp after warp so that their order is fixed
+  for (int w = 0; w < kGateWarps; ++w) {
+    if (w == warp) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (lane * VPL + j < E) s_sum[lane * VPL + j] += acc[j];
+      if (lane == 0) s_live += live;
+      if (bad) s_bad = 1;
+    }
+    __syncthreads();
+  }
+  unsigned long long* sums = work_sums(p.work);
+  int* counts = work_counts(p.work, E);
+  for (int e = tid; e < E; e += blockDim.x) {
+    if (s_sum[e] > 0.0f) atomicAdd(&sums[e], static_cast<unsigned long long>(__double2ull_rn(static_cast<double>(s_sum[e]) * kFixed)));
+    if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
+  }
+  if (tid == 0) {
+    if (s_live) atomicAdd(&p.work[2], static_cast<unsigned>(s_live));
+    if (s_bad) atomicOr(&p.work[1], 1u);
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(&p.work[0], 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  // every block's sums are in: results, and the work space back to zero
+  __threadfence();
+  const int tokens = static_cast<int>(__ldcg(&p.work[2]));
+  const bool any_bad = __ldcg(&p.work[1]) != 0u;
+  float part = 0.0f;
+  for (int e = tid; e < E; e += blockDim.x) {
+    const int n = __ldcg(&counts[e]);
+    float pe = tokens ? static_cast<float>(static_cast<double>(__ldcg(&sums[e])) * (1.0 / kFixed) / tokens) : 0.0f;
+    if (any_bad) pe = CUDART_NAN_F;
+    p.count[e] = n;
+    p.prob[e] = pe;
+    part = fmaf(static_cast<float>(n), pe, part);
+    sums[e] = 0ull;
+    counts[e] = 0;
+  }
+  part = warp_sum(part);
+  if (lane == 0) s_part[warp] = part;
+  __syncthreads();
+  if (tid == 0) {
+    float sum = 0.0f;
+    for (int w = 0; w < kGateWarps; ++w) sum += s_part[w];
+    p.count[E] = tokens;
+    *p.loss = tokens ? p.coef * E / (static_cast<float>(k) * tokens) * sum : 0.0f;
+    p.work[0] = 0u;
+    p.work[1] = 0u;
+    p.work[2] = 0u;
+  }
+}
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kGateWarps * 32) k_gate_backward(const GateArgs p) {
+  extern __shared__ float sm[];  // [E] counts less their mean
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.E, k = p.k;
+  const int tokens = p.count[E];
+  // sum_e p_e = 1, so c_e may be counted from any common value; from the mean
+  // the difference c_e - sum p c loses fewer digits
+  const float mean = static_cast<float>(k) * tokens / E;
+  for (int e = tid; e < E; e += blockDim.x) sm[e] = p.count[e] - mean;
+  __syncthreads();
+  const float coef =
+      p.grad_loss && tokens ? *p.grad_loss * p.coef * E / (static_cast<float>(k) * tokens * tokens) : 0.0f;
+  const bool balance = p.grad_loss && tokens;
+  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+    float d[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
+    if (!p.mask || p.mask[t]) {
+      const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+      if (balance) {
+        float v[VPL], c[VPL];
+        load_row<T, VPL>(row, E, lane, p.vec, v);
+        float m = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+        m = score_base(warp_max(m), p.sigmoid);
+        float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          const int e = lane * VPL + j;
+          c[j] = e < E ? sm[e] : 0.0f;
+          d[j] = e < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+          sum += d[j];
+          dot = fmaf(d[j], c[j], dot);
+        }
+        sum = warp_sum(sum);
+        dot = warp_sum(dot);
+        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : CUDART_NAN_F);
+        dot *= inv;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) d[j] = coef * (d[j] * inv) * slope_of(v[j], p.sigmoid) * (c[j] - dot);
+      }
+      if (p.grad_weights) {
+        int id = -1;
+        float dw = 0.0f, v = -CUDART_INF_F;
+        if (lane < k) {
+          const long long o = static_cast<long long>(t) * k + lane;
+          const long long wide = load_topk_id(p.idx, o, p.ids32);
+          id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
+          if (id >= 0) {
+            dw = p.grad_weights[o];
+            v = load_logit(row + id);
+          }
+        }
+        const float m = score_base(warp_max(v), p.sigmoid);
+        const float s = id >= 0 ? score_of(v, m, p.sigmoid) : 0.0f;
+        const float all = warp_sum(s);
+        const float w = id >= 0 ? s / all : 0.0f;
+        const float mean_dw = warp_sum(w * dw);
+        const float g = id >= 0 ? w * slope_of(v, p.sigmoid) * (dw - mean_dw) : 0.0f;
+        for (int i = 0; i < k; ++i) {
+          const int at = __shfl_sync(kFullMask, id, i) - lane * VPL;
+          const float x = __shfl_sync(kFullMask, g, i);
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (at == j) d[j] += x;
+        }
+      }
+    }
+    T* out = static_cast<T*>(p.grad_logits) + t * p.grad_ld;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int e = lane * VPL + j;
+      if (e < E) out[e] = static_cast<T>(d[j]);
+    }
+  }
+}
+
+namespace {
+
+template <typename T, int VPL>
+cudaError_t launch_vpl(const GateArgs& p, bool backward, int blocks, cudaStream_t s) {
+  const size_t smem = sizeof(float) * (backward ? p.E : 2 * p.E + (p.groups > 1 ? kGateWarps * p.groups : 0));
+  const dim3 grid(blocks), block(kGateWarps * 32);
+  return backward ? launch_kernel(k_gate_backward<T, VPL>, grid, block, smem, s, p)
+                  : launch_kernel(k_gate_forward<T, VPL>, grid, block, smem, s, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const GateArgs& p, bool backward, int blocks, cudaStream_t s) {
+  if (p.E <= 32) return launch_vpl<T, 1>(p, backward, blocks, s);
+  if (p.E <= 64) return launch_vpl<T, 2>(p, backward, blocks, s);
+  if (p.E <= 128) return launch_vpl<T, 4>(p, backward, blocks, s);
+  if (p.E <= 256) return launch_vpl<T, 8>(p, backward, blocks, s);
+  if (p.E <= 512) return launch_vpl<T, 16>(p, backward, blocks, s);
+  if (p.E <= 1024) return launch_vpl<T, 32>(p, backward, blocks, s);
+  return launch_vpl<T, 128>(p, backward, blocks, s);
+}
+
+}  // namespace
+
+size_t gate_work_bytes(int E) { return sizeof(unsigned) * (4 + 3 * static_cast<size_t>(E)); }
+
+cudaError_t launch_gate(const GateArgs& p, bool bf16, bool backward, int sms, cudaStream_t stream) {
+  const int need = (p.T + kGateWarps - 1) / kGateWarps, most = 4 * sms;
+  const int blocks = need < 1 ? 1 : need < most ? need : most;
+  return bf16 ? launch_type<__nv_bfloat16>(p, backward, blocks, stream) : launch_type<float>(p, backward, blocks, stream);
+}
+
+}  // namespace ep

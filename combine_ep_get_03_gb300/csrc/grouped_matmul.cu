@@ -1,0 +1,355 @@
+// The experts' product on e4m3 rows: for a row r of group e
+//   y[r, n] = sum_kb sx[r, kb] sw[e, n / 128, kb] sum_{k in block kb} x[r, k] w[e, n, k]
+// with a scale for every 128 channels of a row and for every 128 x 128 block
+// of the weights.  Stored as bf16, or (SwiGLU) taken through
+//   a = row_weight silu(gate) up
+// and stored as e4m3 with scales, the pre-activations kept as e4m3 if asked.
+//
+// Tile 128 rows x 256 columns, a block per SM that walks over tiles.  One
+// thread loads 48 KB stages by TMA (128 channels of both operands, 128-byte
+// swizzle), one issues the MMAs: four per stage into a fresh TMEM accumulator,
+// since every 128 channels carry their own scale.  Two accumulators of 256
+// columns alternate, so while the tensor cores fill one, eight warps read the
+// other (a thread owns a row, so its factor sx * sw is one number) and add it,
+// scaled, to fp32 registers: 128 a thread.
+//
+// SwiGLU takes its 256 columns as gate 64, up 64, gate 64, up 64 so that a
+// thread holds gate and up of the same channel and the row's 128-channel
+// maximum needs one exchange between two threads.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "ep_internal.h"
+#include "experts.cuh"
+#include "tcgen05.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
+constexpr int kStages = 4;
+constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr uint32_t kTmemColumns = 512;
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], amax_full;
+  uint32_t tmem;
+  int quit;
+  unsigned sums[32];
+  float amax[2][2][3][kTileM];  // [tile parity][half][gate, up, act][row]
+};
+
+struct Tile {
+  int group, n;     // group and column tile
+  long long row;    // first row
+  int rows;         // live rows of the tile
+};
+
+__device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* prefix, int tiles_n, long long t) {
+  // tiles of a group are ordered column tile by column tile, row tiles inside
+  const int g = find_group(prefix, a.G, static_cast<unsigned>(t / tiles_n));
+  Tile r;
+  long long start;
+  const int count = group_span(a, g, &start, false);
+  const int tiles_m = (count + kTileM - 1) / kTileM;
+  const long long local = t - static_cast<long long>(prefix[g]) * tiles_n;
+  r.group = g;
+  r.n = tiles_m ? static_cast<int>(local / tiles_m) : 0;
+  const int m = tiles_m ? static_cast<int>(local % tiles_m) : 0;
+  r.row = start + static_cast<long long>(m) * kTileM;
+  r.rows = tiles_m ? min(kTileM, count - m * kTileM) : 0;
+  return r;
+}
+
+}  // namespace
+
+template <bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_grouped_matmul(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                     const MatmulArgs p) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* stages = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Shared& s = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  unsigned* prefix = reinterpret_cast<unsigned*>(&s + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* quit = &s.quit;
+  int* err = p.groups.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kEpilogueWarps);
+    mbar_init(&s.amax_full, kEpilogueWarps);
+    s.quit = 0;
+    mbar_init_fence();
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+  }
+  if (warp == kEpilogueWarps + 1) tmem_alloc(&s.tmem, kTmemColumns);
+  groups_prefix(p.groups, kTileM, prefix, s.sums);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  const int F = p.N >> 1;
+  const int tiles_n = kSwiglu ? (F + kTileN / 2 - 1) / (kTileN / 2) : (p.N + kTileN - 1) / kTileN;
+  const int blocks_k = p.K / kBlockK;
+  const long long tiles = static_cast<long long>(prefix[p.groups.G]) * tiles_n;
+
+  if (warp == kEpilogueWarps) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const Tile c = tile_at(p.groups, prefix, tiles_n, t);
+        bool ok = true;
+        for (int kb = 0; kb < blocks_k; ++kb, ++it) {
+          const int st = it % kStages;
+          if (it >= kStages && !(ok = wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err))) break;
+          unsigned char* a = stages + st * kStageBytes;
+          unsigned char* b = a + kTileM * kBlockK;
+          mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+          tma_load_2d(a, &map_x, kb * kBlockK, static_cast<int>(c.row), &s.full[st]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = kSwiglu ? c.n * 128 + (q >> 1) * 64 + (q & 1) * F : c.n * kTileN + q * 64;
+            tma_load_3d(b + q * 64 * kBlockK, &map_w, kb * kBlockK, n, c.group, &s.full[st]);
+          }
+        }
+        if (!ok) break;
+      }
+      // no load may outlive the block: wait for the last fill of every stage
+      const uint32_t last = it < kStages ? it : kStages;
+      for (uint32_t i = it - last; i < it; ++i) {
+        const uint32_t parity = (i / kStages) & 1;
+        int none = 0;
+        wait_or_quit(&s.full[i % kStages], parity, &none, err);
+      }
+    }
+  } else if (warp == kEpilogueWarps + 1) {
+    if (lane == 0) {
+      constexpr uint32_t desc = mma_desc(kTileM, kTileN, false);
+      uint32_t it = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int kb = 0; kb < blocks_k; ++kb, ++it) {
+          const int st = it % kStages, ac = it & 1;
+          if (it >= 2 && !(ok = wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err))) break;
+          if (!(ok = wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err))) break;
+          tmem_fence_after();
+          const uint32_t a = smem_u32(stages + st * kStageBytes), b = a + kTileM * kBlockK;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f8(tmem + ac * kTileN, smem_desc(a + j * 32, 16, 1024), smem_desc(b + j * 32, 16, 1024), desc, j > 0);
+          mma_commit(&s.empty[st]);
+          mma_commit(&s.acc_full[ac]);
+        }
+      }
+      // nor may an MMA: its last accumulator is complete before TMEM goes back
+      for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) {
+        int none = 0;
+        wait_or_quit(&s.acc_full[i & 1], (i >> 1) & 1, &none, err);
+      }
+    }
+  } else {
+    const int half = warp >> 2, quarter = warp & 3;
+    const int in_tile = quarter * 32 + lane;  // the thread's row in the tile
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (kTileN / 2);
+    const int Gk = blocks_k, Gn = (p.N + 127) >> 7;
+    const bool wide = kSwiglu ? false : ((reinterpret_cast<uintptr_t>(p.out) | (static_cast<uintptr_t>(p.N) * 2)) & 31) == 0;
+    uint32_t it = 0;
+    int turn = 0;
+    bool ok = true;
+    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, turn ^= 1) {
+      const Tile c = tile_at(p.groups, prefix, tiles_n, t);
+      const long long row = c.row + in_tile;
+      const bool live = in_tile < c.rows;
+      // the columns' scale blocks: one for plain tiles, gate and up for SwiGLU
+      const int n0 = kSwiglu ? c.n : c.n * 2 + half;
+      const float* sw0 = p.w_scales + (static_cast<long long>(c.group) * Gn + min(n0, Gn - 1)) * Gk;
+      const float* sw1 = kSwiglu ? sw0 + static_cast<long long>(F >> 7) * Gk : sw0;
+      const float* sx = p.x.scales + (live ? row * p.x.row_stride : 0);
+      uint64_t acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+      float nx = live ? sx[0] : 0.0f, nw0 = sw0[0], nw1 = kSwiglu ? sw1[0] : 0.0f;
+      for (int kb = 0; kb < blocks_k; ++kb, ++it) {
+        const int ac = it & 1;
+        const float f0 = nx * nw0, f1 = kSwiglu ? nx * nw1 : f0;
+        if (kb + 1 < blocks_k) {
+          nx = live ? sx[(kb + 1) * p.x.group_stride] : 0.0f;
+          nw0 = sw0[kb + 1];
+          if (kSwiglu) nw1 = sw1[kb + 1];
+        }
+        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it >> 1) & 1, quit, err));
+        if (!ok) break;
+        tmem_fence_after();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_load32(lanes + ac * kTileN + q * 32, v);
+          tmem_load_wait();
+          if (q == 3) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
+          }
+          const float f = kSwiglu && q >= 2 ? f1 : f0;
+          const uint64_t ff = pack2(f, f);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], pack2u(v[2 * j], v[2 * j + 1]), ff);
+        }
+      }
+      if (!ok) break;
+      if constexpr (!kSwiglu) {
+        const int col = c.n * kTileN + half * 128;
+        if (live) {
+          uint16_t* o = p.out + row * p.N + col;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float lo, hi;
+              unpack2(acc[q * 8 + j], &lo, &hi);
+              v[j] = pack_bf16x2(lo, hi);
+            }
+            if (col + q * 16 + 16 <= p.N)
+              store32(o + q * 16, v, wide);
+            else if (col + q * 16 + 8 <= p.N)
+              *reinterpret_cast<uint4*>(o + q * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      } else {
+        const int f = c.n * 128 + half * 64;
+        const float w = live && p.row_weights ? p.row_weights[row] : 1.0f;
+        const bool keep = p.pre.data != nullptr;
+        float (*amax)[3][kTileM] = s.amax[turn];
+        float ag = 0.0f, au = 0.0f, aa = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          float g, u;
+          {
+            float lo, hi;
+            unpack2(acc[j >> 1], &lo, &hi);
+            g = (j & 1) ? hi : lo;
+            unpack2(acc[32 + (j >> 1)], &lo, &hi);
+            u = (j & 1) ? hi : lo;
+          }
+          ag = fmaxf(ag, fabsf(g));
+          au = fmaxf(au, fabsf(u));
+          aa = fmaxf(aa, fabsf(__fdividef(g, 1.0f + __expf(-g)) * u * w));
+        }
+        amax[half][0][in_tile] = ag;
+        amax[half][1][in_tile] = au;
+        amax[half][2][in_tile] = aa;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.amax_full);
+        ok = __all_sync(kFullMask, wait_or_quit(&s.amax_full, turn, quit, err));
+        if (!ok) break;
+        if (live) {
+          float inv;
+          uint32_t q[16];
+          if (keep) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const float sc = group_scale(fmaxf(amax[0][part][in_tile], amax[1][part][in_tile]), &inv);
+              if (half == 0) *p.pre.scale(row, c.n + part * (F >> 7)) = sc;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float x[4];
+                unpack2(acc[part * 32 + 2 * j], x, x + 1);
+                unpack2(acc[part * 32 + 2 * j + 1], x + 2, x + 3);
+                q[j] = quant4(x, inv);
+              }
+              unsigned char* o = p.pre.data + row * p.N + part * F + f;
+              const bool w32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+              store32(o, q, w32);
+              store32(o + 32, q + 8, w32);
+            }
+          }
+          const float sc = group_scale(fmaxf(amax[0][2][in_tile], amax[1][2][in_tile]), &inv);
+          if (half == 0) *p.act.scale(row, c.n) = sc;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float g[4], u[4];
+            unpack2(acc[2 * j], g, g + 1);
+            unpack2(acc[2 * j + 1], g + 2, g + 3);
+            unpack2(acc[32 + 2 * j], u, u + 1);
+            unpack2(acc[32 + 2 * j + 1], u + 2, u + 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i] * w;
+            q[j] = quant4(g, inv);
+          }
+          unsigned char* o = p.act.data + row * F + f;
+          const bool w32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+          store32(o, q, w32);
+          store32(o + 32, q + 8, w32);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kEpilogueWarps + 1) {
+    tmem_fence_after();
+    tmem_free(tmem, kTmemColumns);
+  }
+}
+
+namespace {
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+}  // namespace
+
+// A tensor map over e4m3 bytes [planes][rows][width], box 128 x box_rows.
+cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t rank = planes > 0 ? 3 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes > 0 ? planes : 1)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(width) * rows};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream) {
+  CUtensorMap map_x, map_w;
+  cudaError_t e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, kTileM);
+  if (e == cudaSuccess) e = make_byte_map(&map_w, p.w, p.K, p.N, p.groups.G, 64);
+  if (e != cudaSuccess) return e;
+  const bool swiglu = p.act.data != nullptr;
+  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared) + sizeof(unsigned) * (p.groups.G + 1);
+  auto kernel = swiglu ? k_grouped_matmul<true> : k_grouped_matmul<false>;
+  int device = 0, optin = 0;
+  if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess) return e;
+  if ((e = set_dynamic_smem_limit(reinterpret_cast<const void*>(kernel), smem, optin)) != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p);
+}
+
+}  // namespace ep

@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libep_gb300.so")
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CUDA, EP_ERR_CAPACITY, EP_ERR_BAD_EXPERT, EP_ERR_TIMEOUT, EP_ERR_STATE = range(7)
 EP_BF16, EP_FP8_E4M3 = 0, 1
 EP_LAYOUT_RANK_MAJOR, EP_LAYOUT_LOW_LATENCY, EP_LAYOUT_EXPERT_MAJOR = 0, 1, 2
+EP_LOGITS_FP32, EP_LOGITS_BF16 = 0, 1
+EP_GATE_SOFTMAX, EP_GATE_SIGMOID = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -30,6 +32,16 @@ class EPError(RuntimeError):
     def __init__(self, status: int, call: str):
         super().__init__(f"{call}: {status_str(status)} ({status})")
         self.status = status
+
+
+class _Groups(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_void_p), ("offset", ctypes.c_void_p), ("num_groups", ctypes.c_int),
+                ("rows", ctypes.c_int64), ("rows_per_group", ctypes.c_int64), ("status", ctypes.c_void_p)]
+
+
+class _Fp8Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("group_stride", ctypes.c_int64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -66,13 +78,24 @@ def lib() -> ctypes.CDLL:
             L.ep_get_device_status.argtypes = [P, P]
             L.ep_check_wait_timeout.argtypes = [P, P]
             L.ep_get_dispatch_layout_noalloc.argtypes = [I, I, I, P, I, P, P, P, P, P, P, P, P, P, P]
+            F32 = ctypes.c_float
+            GP, RP = ctypes.POINTER(_Groups), ctypes.POINTER(_Fp8Rows)
+            L.ep_gate_workspace_bytes.argtypes = [I, P]
+            L.ep_gate_forward.argtypes = [P, I, I64, P, I, I, I, I, I, I, F32, P, I, P, P, P, P, P, I, P]
+            L.ep_gate_backward.argtypes = [P, I, I64, P, I, I, I, I, F32, P, I, P, P, P, P, I64, I, P]
+            L.ep_grouped_matmul.argtypes = [GP, RP, P, P, I, I, P, I, P]
+            L.ep_grouped_matmul_swiglu.argtypes = [GP, RP, P, P, I, I, P, RP, RP, I, P]
+            L.ep_grouped_swiglu_backward.argtypes = [GP, P, RP, P, I, RP, P, I, P]
+            L.ep_grouped_weight_grad.argtypes = [GP, RP, I, RP, I, P, I, P]
             L.ep_status_str.argtypes = [I]
             L.ep_status_str.restype = ctypes.c_char_p
             for n in ("ep_handle_create", "ep_handle_destroy", "ep_get_dispatch_layout", "ep_get_num_recv",
                       "ep_dispatch", "ep_combine", "ep_layout_and_dispatch", "ep_low_latency_dispatch",
                       "ep_low_latency_combine", "ep_combine_ex", "ep_handle_set_topk_idx_bits",
                       "ep_em_layout_and_dispatch", "ep_em_dispatch", "ep_em_get_layout", "ep_em_combine",
-                      "ep_get_buffer_size_hint",
+                      "ep_get_buffer_size_hint", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
+                      "ep_grouped_matmul", "ep_grouped_matmul_swiglu", "ep_grouped_swiglu_backward",
+                      "ep_grouped_weight_grad",
                       "ep_get_device_status", "ep_check_wait_timeout", "ep_get_dispatch_layout_noalloc"):
                 getattr(L, n).restype = I
             _lib = L
@@ -332,6 +355,221 @@ def ep_get_dispatch_layout_noalloc(num_ranks, num_experts, num_topk, topk_idx, n
         _ptr(rank_offset, (torch.int32,), "rank_offset"), _ptr(token_dest, (torch.int32,), "token_dest"),
         _ptr(topk_idx32, (torch.int32,), "topk_idx32"), _ptr(device_status, (torch.int32,), "device_status"),
         _stream(stream)), "ep_get_dispatch_layout_noalloc")
+
+
+# ------------------------------------------------------- gate and experts
+#
+# Row buffers are either expert-major ([rows, width], with group_offset) or
+# low latency ([E, M, width], group_offset None); FP8 scales follow as the
+# dispatches leave them: [width/128, ld >= rows] or [E, M, width/128].
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _one_device(*tensors) -> None:
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _rows_ptr(t, dtypes, name):
+    """A row buffer's pointer and its (rows, width); 2-D expert-major or 3-D low latency."""
+    p = _ptr(t, dtypes, name)
+    _need(t is not None and t.dim() in (2, 3), f"{name} must be [rows, width] or [E, M, width]")
+    width = t.shape[-1]
+    return p, t.numel() // width if width else 0, width
+
+
+def _fp8_rows(data, scales, name):
+    p, rows, width = _rows_ptr(data, _FP8_BYTES, name)
+    _need(width > 0 and width % 128 == 0, f"{name}'s width must be a positive multiple of 128")
+    sp = _ptr(scales, (torch.float32,), f"{name}_scales")
+    g = width // 128
+    if data.dim() == 2:
+        _need(scales is not None and scales.dim() == 2 and scales.shape[0] == g and scales.shape[1] >= rows,
+              f"{name}_scales must be [{g}, ld >= {rows}] for expert-major rows")
+        r = _Fp8Rows(p, sp, 1, scales.shape[1])
+    else:
+        _need(scales is not None and tuple(scales.shape) == tuple(data.shape[:2]) + (g,),
+              f"{name}_scales must be {list(data.shape[:2]) + [g]} for low-latency rows")
+        r = _Fp8Rows(p, sp, g, 1)
+    return r, rows, width
+
+
+def _groups(rows_like, group_count, group_offset, device_status):
+    cp = _ptr(group_count, (torch.int32,), "group_count")
+    _need(group_count is not None and group_count.dim() == 1, "group_count must be an int32 [E] tensor")
+    E = group_count.numel()
+    if rows_like.dim() == 2:
+        _need(group_offset is not None and group_offset.numel() >= E,
+              "expert-major rows need group_offset: the first row of each of the E groups")
+        rows, per = rows_like.shape[0], 0
+    else:
+        _need(group_offset is None, "low-latency rows [E, M, width] take no group_offset")
+        _need(rows_like.shape[0] == E, f"rows hold {rows_like.shape[0]} groups, group_count {E}")
+        rows, per = rows_like.shape[0] * rows_like.shape[1], rows_like.shape[1]
+    op = _ptr(group_offset, (torch.int32,), "group_offset")
+    _need(device_status is None or device_status.numel() >= 1, "device_status must hold one int32")
+    return _Groups(cp, op, E, rows, per, _ptr(device_status, (torch.int32,), "device_status")), E, rows
+
+
+def _same_rows(a, b, name):
+    _need(b.dim() == a.dim() and b.shape[:-1] == a.shape[:-1], f"{name} must have the rows {list(a.shape[:-1])}")
+
+
+def _weights_ptr(w, w_scales, E, N, K):
+    wp, sp = _ptr(w, _FP8_BYTES, "w"), _ptr(w_scales, (torch.float32,), "w_scales")
+    _need(w is not None and tuple(w.shape) == (E, N, K), f"w must be [{E}, {N}, {K}]")
+    shape = (E, (N + 127) // 128, K // 128)
+    _need(w_scales is not None and tuple(w_scales.shape) == shape, f"w_scales must be {list(shape)}")
+    return wp, sp
+
+
+def _row_vector(t, rows, name):
+    p = _ptr(t, (torch.float32,), name)
+    _need(t is None or t.numel() >= rows, f"{name} needs one value for each of the {rows} rows")
+    return p
+
+
+def ep_gate_workspace_bytes(num_experts: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().ep_gate_workspace_bytes(num_experts, ctypes.byref(n)), "ep_gate_workspace_bytes")
+    return n.value
+
+
+def _logits(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _need(t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16), f"{name} must be [T, E] fp32 or bf16")
+    T, E = t.shape
+    _need(T == 0 or E == 1 or t.stride(1) == 1, f"{name} must have contiguous rows")
+    ld = t.stride(0) if T > 1 else max(E, 1)
+    _need(ld >= E, f"{name}'s rows must not overlap")
+    return t.data_ptr(), EP_LOGITS_FP32 if t.dtype == torch.float32 else EP_LOGITS_BF16, ld, T, E
+
+
+def _gate_common(T, topk_idx, token_mask):
+    ip = _ptr(topk_idx, (torch.int64, torch.int32), "topk_idx")
+    _need(topk_idx is not None and topk_idx.dim() == 2 and topk_idx.shape[0] == T, f"topk_idx must be [{T}, k]")
+    mp = _ptr(token_mask, (torch.bool, torch.uint8), "token_mask")
+    _need(token_mask is None or token_mask.numel() >= T, "token_mask needs one value per token")
+    return ip, 64 if topk_idx.dtype == torch.int64 else 32, topk_idx.shape[1], mp
+
+
+def ep_gate_forward(logits, topk_idx, topk_weights, expert_count, expert_prob, loss, workspace,
+                    score: int = EP_GATE_SOFTMAX, num_groups: int = 1, topk_groups: int = 1, loss_coef: float = 0.0,
+                    token_mask=None, num_sms: int = 0, stream=None) -> None:
+    """Top-k routing of logits [T, E] (rows may be strided): fills topk_idx
+    [T, k], topk_weights [T, k], expert_count [E + 1], expert_prob [E] and
+    loss [1].  workspace: ep_gate_workspace_bytes(E) zeroed bytes, reusable."""
+    lp, lt, ld, T, E = _logits(logits, "logits")
+    ip, bits, k, mp = _gate_common(T, topk_idx, token_mask)
+    for t, n, name in ((topk_weights, T * k, "topk_weights"), (expert_count, E + 1, "expert_count"),
+                       (expert_prob, E, "expert_prob"), (loss, 1, "loss")):
+        _need(isinstance(t, torch.Tensor) and t.numel() >= n, f"{name} must hold {n} elements")
+    _need(isinstance(workspace, torch.Tensor) and workspace.numel() * workspace.element_size() >= 16 + 12 * E,
+          f"workspace must hold {16 + 12 * E} bytes")
+    _one_device(logits, topk_idx, topk_weights, expert_count, expert_prob, loss, workspace, token_mask)
+    _check(lib().ep_gate_forward(
+        lp, lt, ld, mp, T, E, k, int(num_groups), int(topk_groups), int(score), float(loss_coef), ip, bits,
+        _ptr(topk_weights, (torch.float32,), "topk_weights"), _ptr(expert_count, (torch.int32,), "expert_count"),
+        _ptr(expert_prob, (torch.float32,), "expert_prob"), _ptr(loss, (torch.float32,), "loss"),
+        _ptr(workspace, None, "workspace"), int(num_sms), _stream(stream)), "ep_gate_forward")
+
+
+def ep_gate_backward(logits, topk_idx, expert_count, grad_topk_weights, grad_loss, grad_logits,
+                     score: int = EP_GATE_SOFTMAX, loss_coef: float = 0.0, token_mask=None, num_sms: int = 0,
+                     stream=None) -> None:
+    """Gradient with respect to the logits from those of topk_weights [T, k]
+    and loss [1] (either may be None)."""
+    lp, lt, ld, T, E = _logits(logits, "logits")
+    ip, bits, k, mp = _gate_common(T, topk_idx, token_mask)
+    gp, gt, gld, gT, gE = _logits(grad_logits, "grad_logits")
+    _need((gt, gT, gE) == (lt, T, E), "grad_logits must have the logits' shape and dtype")
+    _need(isinstance(expert_count, torch.Tensor) and expert_count.numel() >= E + 1, "expert_count must be [E + 1]")
+    _need(grad_topk_weights is None or tuple(grad_topk_weights.shape) == (T, k), f"grad_topk_weights must be [{T}, {k}]")
+    _need(grad_loss is None or grad_loss.numel() >= 1, "grad_loss must hold one value")
+    _one_device(logits, topk_idx, expert_count, grad_topk_weights, grad_loss, grad_logits, token_mask)
+    _check(lib().ep_gate_backward(
+        lp, lt, ld, mp, T, E, k, int(score), float(loss_coef), ip, bits,
+        _ptr(expert_count, (torch.int32,), "expert_count"),
+        _ptr(grad_topk_weights, (torch.float32,), "grad_topk_weights"), _ptr(grad_loss, (torch.float32,), "grad_loss"),
+        gp, gld, int(num_sms), _stream(stream)), "ep_gate_backward")
+
+
+def ep_grouped_matmul(x, x_scales, w, w_scales, out, group_count, group_offset=None, device_status=None,
+                      num_sms: int = 0, stream=None) -> None:
+    """out = x @ w[e].T for the rows of every group: e4m3 x and w [E, N, K]
+    with 128-channel and 128 x 128 scales, bf16 out."""
+    g, E, rows = _groups(x, group_count, group_offset, device_status)
+    xr, _, K = _fp8_rows(x, x_scales, "x")
+    op, _, N = _rows_ptr(out, (torch.bfloat16,), "out")
+    _same_rows(x, out, "out")
+    wp, sp = _weights_ptr(w, w_scales, E, N, K)
+    _one_device(x, x_scales, w, w_scales, out, group_count, group_offset, device_status)
+    _check(lib().ep_grouped_matmul(ctypes.byref(g), ctypes.byref(xr), wp, sp, N, K, op, int(num_sms),
+                                   _stream(stream)), "ep_grouped_matmul")
+
+
+def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_count, group_offset=None,
+                             row_weights=None, pre=None, pre_scales=None, device_status=None, num_sms: int = 0,
+                             stream=None) -> None:
+    """act = row_weights * silu(gate) * up in e4m3 with scales, where (gate, up)
+    = x @ w[e].T, w [E, 2F, K]; pre (optional) keeps (gate, up) in e4m3."""
+    g, E, rows = _groups(x, group_count, group_offset, device_status)
+    xr, _, K = _fp8_rows(x, x_scales, "x")
+    ar, _, F = _fp8_rows(act, act_scales, "act")
+    _same_rows(x, act, "act")
+    pr = None
+    if pre is not None:
+        pr, _, two = _fp8_rows(pre, pre_scales, "pre")
+        _same_rows(x, pre, "pre")
+        _need(two == 2 * F, f"pre must be {2 * F} wide")
+    wp, sp = _weights_ptr(w, w_scales, E, 2 * F, K)
+    _one_device(x, x_scales, w, w_scales, act, act_scales, row_weights, pre, pre_scales, group_count, group_offset,
+                device_status)
+    _check(lib().ep_grouped_matmul_swiglu(
+        ctypes.byref(g), ctypes.byref(xr), wp, sp, F, K, _row_vector(row_weights, rows, "row_weights"),
+        ctypes.byref(ar), ctypes.byref(pr) if pr is not None else None, int(num_sms), _stream(stream)),
+        "ep_grouped_matmul_swiglu")
+
+
+def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, group_count, group_offset=None,
+                               row_weights=None, grad_row_weights=None, device_status=None, num_sms: int = 0,
+                               stream=None) -> None:
+    """Gradient of the pre-activations (e4m3 with scales) and of the row
+    weights, from grad_act (bf16) and the 8-bit pre-activations."""
+    g, E, rows = _groups(grad_act, group_count, group_offset, device_status)
+    dp, _, F = _rows_ptr(grad_act, (torch.bfloat16,), "grad_act")
+    pr, _, two = _fp8_rows(pre, pre_scales, "pre")
+    gr, _, two_out = _fp8_rows(grad_pre, grad_pre_scales, "grad_pre")
+    _same_rows(grad_act, pre, "pre")
+    _same_rows(grad_act, grad_pre, "grad_pre")
+    _need(two == 2 * F and two_out == 2 * F, f"pre and grad_pre must be {2 * F} wide")
+    _one_device(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, row_weights, grad_row_weights, group_count,
+                group_offset, device_status)
+    _check(lib().ep_grouped_swiglu_backward(
+        ctypes.byref(g), dp, ctypes.byref(pr), _row_vector(row_weights, rows, "row_weights"), F, ctypes.byref(gr),
+        _row_vector(grad_row_weights, rows, "grad_row_weights"), int(num_sms), _stream(stream)),
+        "ep_grouped_swiglu_backward")
+
+
+def ep_grouped_weight_grad(grad_out, grad_out_scales, x, x_scales, grad_w, group_count, group_offset=None,
+                           device_status=None, num_sms: int = 0, stream=None) -> None:
+    """grad_w[e] = grad_out.T @ x over the rows of group e, both e4m3 with
+    scales; bf16 [E, N, K]."""
+    g, E, rows = _groups(x, group_count, group_offset, device_status)
+    yr, _, N = _fp8_rows(grad_out, grad_out_scales, "grad_out")
+    xr, _, K = _fp8_rows(x, x_scales, "x")
+    _same_rows(x, grad_out, "grad_out")
+    gp = _ptr(grad_w, (torch.bfloat16,), "grad_w")
+    _need(grad_w is not None and tuple(grad_w.shape) == (E, N, K), f"grad_w must be [{E}, {N}, {K}]")
+    _one_device(grad_out, grad_out_scales, x, x_scales, grad_w, group_count, group_offset, device_status)
+    _check(lib().ep_grouped_weight_grad(ctypes.byref(g), ctypes.byref(yr), N, ctypes.byref(xr), K, gp, int(num_sms),
+                                        _stream(stream)), "ep_grouped_weight_grad")
 
 
 class Handle:

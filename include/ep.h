@@ -393,6 +393,132 @@ ep_status_t ep_get_device_status(ep_handle_t h, ep_stream_t stream);
  * fails. */
 ep_status_t ep_check_wait_timeout(ep_handle_t h, ep_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * The experts' side: the gate that decides the routing, and the experts'
+ * computation on the rows that dispatch leaves.  These calls need no handle
+ * and allocate nothing; they run on the current device and work on whatever
+ * layout the groups describe.  Sums, softmax statistics and norms are held
+ * in fp32.
+ * --------------------------------------------------------------------- */
+
+/* Groups of rows, one group per expert.
+ *  - expert-major: offset = the dispatch's expert_offset, count = its rows per
+ *    expert (ep_em_get_groups copies both to device buffers);
+ *  - low latency: offset NULL, rows_per_group = M, count = recv_count.
+ * Rows outside every group are neither read into a result nor written.  A
+ * group that does not fit its rows_per_group slots or the `rows` of the
+ * buffers is cut to what does, and EP_ERR_CAPACITY is latched in *status.
+ * Groups must not overlap. */
+typedef struct {
+  const int* count;       /* dev int32 [num_groups]                                  */
+  const int* offset;      /* dev int32 [num_groups]: first row of a group, or NULL   */
+  int num_groups;         /* 1..4096                                                 */
+  int64_t rows;           /* rows of every row buffer, < 2^31                        */
+  int64_t rows_per_group; /* offset NULL: group g starts at row g * rows_per_group   */
+  int* status;            /* dev int32 [1] zeroed by the caller, or NULL: the first
+                             EP_ERR_CAPACITY or EP_ERR_TIMEOUT found on the device   */
+} ep_groups_t;
+
+/* e4m3 rows with one fp32 scale per 128 channels: the scale of row r, channels
+ * [128 g, 128 g + 128) is scales[r * row_stride + g * group_stride].
+ *  - expert-major dispatch: row_stride 1, group_stride scales_ld;
+ *  - low-latency dispatch: row_stride width/128, group_stride 1. */
+typedef struct {
+  void* data;    /* dev [rows][width] bytes, 16-byte aligned */
+  float* scales; /* dev fp32                                 */
+  int64_t row_stride, group_stride;
+} ep_fp8_rows_t;
+
+typedef enum { EP_LOGITS_FP32 = 0, EP_LOGITS_BF16 = 1 } ep_logits_t;
+typedef enum { EP_GATE_SOFTMAX = 0, EP_GATE_SIGMOID = 1 } ep_gate_score_t;
+
+/* Bytes of the gate's workspace for a number of experts (1..4096). */
+ep_status_t ep_gate_workspace_bytes(int num_experts, int64_t* bytes);
+
+/* The gate: top-k experts, their weights, per-expert counts and the balance
+ * loss of T tokens.
+ * In:  logits      dev [T][logits_ld] fp32 or bf16, E of each row used.
+ *      token_mask  dev uint8 [T] or NULL: 0 marks a padding token, whose
+ *                  logits are not read.
+ *      num_groups, topk_groups  the k experts come from the topk_groups groups
+ *                  of E/num_groups consecutive experts with the largest
+ *                  maximal logit (num_groups <= 64; 1, 1: no group limit).
+ *      score       EP_GATE_SOFTMAX: weights = softmax of the chosen logits,
+ *                  p = softmax over all experts;  EP_GATE_SIGMOID: weights =
+ *                  sigmoid of the chosen logits over their sum, p = sigmoid
+ *                  over the sum of all.
+ * Out: topk_idx     dev [T][k] int64 or int32 (topk_idx_bits), by descending
+ *                   logit, ties to the lower index; -1 for padding tokens and
+ *                   where fewer than k logits are above -inf (a NaN logit is
+ *                   never chosen).
+ *      topk_weights dev fp32 [T][k], 0 where topk_idx is -1.
+ *      expert_count dev int32 [E + 1]: entries per expert; [E] = unmasked tokens V.
+ *      expert_prob  dev fp32 [E]: mean of p over the unmasked tokens (0 if none).
+ *      loss         dev fp32 [1]: loss_coef * E / (k V) * sum_e expert_count[e]
+ *                   expert_prob[e] (0 if V = 0); NaN, as expert_prob, if a
+ *                   row's probabilities are not finite.
+ * workspace: dev, ep_gate_workspace_bytes, 16-byte aligned, zeroed before its
+ * first use and left zeroed; one call at a time may use it.
+ * k <= 32, k <= E <= 4096, T <= 2^26.  One launch. */
+ep_status_t ep_gate_forward(const void* logits, ep_logits_t logits_type, int64_t logits_ld,
+                            const uint8_t* token_mask, int num_tokens, int num_experts, int num_topk,
+                            int num_groups, int topk_groups, ep_gate_score_t score, float loss_coef,
+                            void* topk_idx, int topk_idx_bits, float* topk_weights, int* expert_count,
+                            float* expert_prob, float* loss, void* workspace, int num_sms,
+                            ep_stream_t stream);
+
+/* Gradient of the gate with respect to its logits, from the gradients of
+ * topk_weights (dev fp32 [T][k], or NULL) and of the loss (dev fp32 [1], or
+ * NULL); logits, token_mask, topk_idx and expert_count as ep_gate_forward had
+ * and left them.  The choice and the counts are constants.
+ * Out: grad_logits dev [T][grad_logits_ld], the logits' type; 0 on padding
+ * tokens. */
+ep_status_t ep_gate_backward(const void* logits, ep_logits_t logits_type, int64_t logits_ld,
+                             const uint8_t* token_mask, int num_tokens, int num_experts, int num_topk,
+                             ep_gate_score_t score, float loss_coef, const void* topk_idx, int topk_idx_bits,
+                             const int* expert_count, const float* grad_topk_weights, const float* grad_loss,
+                             void* grad_logits, int64_t grad_logits_ld, int num_sms, ep_stream_t stream);
+
+/* The experts' product: out[r][n] = sum_k x[r][k] w[e][n][k] for every live
+ * row r of group e, dequantised, rounded once to bf16.
+ * In:  x         e4m3 rows of width K (a multiple of 128).
+ *      w         dev e4m3 [num_groups][N][K], 16-byte aligned; N a multiple of 8.
+ *      w_scales  dev fp32 [num_groups][ceil(N/128)][K/128]: one scale per 128 x
+ *                128 block.
+ * Out: out       dev bf16 [rows][N].
+ * The gradient with respect to x is the same call on grad_out rows of width N
+ * with the weights and their scales transposed. */
+ep_status_t ep_grouped_matmul(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                              const float* w_scales, int N, int K, void* out, int num_sms, ep_stream_t stream);
+
+/* The experts' first product with the activation in its epilogue.  w holds the
+ * gate's F rows, then the up projection's (dev e4m3 [num_groups][2F][K], scales
+ * [num_groups][2F/128][K/128]; F, K multiples of 128).
+ *   act = row_weights[r] * silu(gate) * up   (row_weights dev fp32 [rows] or NULL: 1)
+ * Out: act  e4m3 rows of width F, quantised from fp32 as dispatch quantises.
+ *      pre  e4m3 rows of width 2F (gate, then up), or NULL: the activations
+ *           that the backward pass needs, kept in 8 bits. */
+ep_status_t ep_grouped_matmul_swiglu(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                                     const float* w_scales, int F, int K, const float* row_weights,
+                                     const ep_fp8_rows_t* act, const ep_fp8_rows_t* pre, int num_sms,
+                                     ep_stream_t stream);
+
+/* Backward of that activation from its 8-bit checkpoint.
+ * In:  grad_act  dev bf16 [rows][F], the gradient of act;  pre and row_weights as
+ *                ep_grouped_matmul_swiglu left and had them.
+ * Out: grad_pre  e4m3 rows of width 2F: the gradient of the pre-activations.
+ *      grad_row_weights  dev fp32 [rows] or NULL. */
+ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* grad_act, const ep_fp8_rows_t* pre,
+                                       const float* row_weights, int F, const ep_fp8_rows_t* grad_pre,
+                                       float* grad_row_weights, int num_sms, ep_stream_t stream);
+
+/* Gradient of the experts' weights from 8-bit rows: grad_w[e][n][k] = sum over
+ * the rows r of group e of grad_out[r][n] x[r][k], dequantised, rounded once to
+ * bf16 (dev [num_groups][N][K], 16-byte aligned; 0 for an empty group).
+ * N and K are multiples of 128. */
+ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_t* grad_out, int N,
+                                   const ep_fp8_rows_t* x, int K, void* grad_w, int num_sms, ep_stream_t stream);
+
 /* Static, NUL-terminated name of a status. */
 const char* ep_status_str(ep_status_t s);
 
