@@ -74,9 +74,9 @@ __device__ __forceinline__ void sts128(unsigned char* p, uint32_t a, uint32_t b,
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" : : "r"(smem_u32(p)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 codes of row r, 16-channel chunk c of an operand, to its f16 tile.  The
-// two halves of a 128-byte line's lanes write their pairs of 16-byte units in
-// opposite order, which keeps the eight lanes of a phase on different banks.
+// 16 codes of row r, 16-channel chunk c of an operand, to its f16 tile.  A
+// phase of a warp's 16-byte stores covers two rows of one 64-channel block,
+// whose swizzled units are the even and the odd ones: no bank conflict.
 __device__ __forceinline__ void store_chunk(unsigned char* tile, int r, int c, const uint4& q, uint32_t scale, bool scaled) {
   uint32_t h[8];
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -87,21 +87,15 @@ __device__ __forceinline__ void store_chunk(unsigned char* tile, int r, int c, c
   }
   unsigned char* line = tile + (c >> 2) * kChunkBytes + r * 128;
   const int u = (c & 3) * 2, x = r & 7;
-  unsigned char* p0 = line + ((u ^ x) << 4);
-  unsigned char* p1 = line + (((u + 1) ^ x) << 4);
-  if ((c >> 2) & 1) {
-    sts128(p1, h[4], h[5], h[6], h[7]);
-    sts128(p0, h[0], h[1], h[2], h[3]);
-  } else {
-    sts128(p0, h[0], h[1], h[2], h[3]);
-    sts128(p1, h[4], h[5], h[6], h[7]);
-  }
+  sts128(line + ((u ^ x) << 4), h[0], h[1], h[2], h[3]);
+  sts128(line + (((u + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
 }
 
-// One thread's part of 64 rows: two chunks of dy, four of x with their scales.
+// One thread's part of 64 rows, all of one row: chunks c, c + 4 of dy and
+// c, c + 4, c + 8, c + 12 of x (c = thread mod 4), and the row's scales.
 struct Fetched {
   uint4 dy[2], x[4];
-  float scale[4];
+  float y_scale, x_scale[2];
 };
 
 }  // namespace
@@ -130,8 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
 
   if (warp < kLoadWarps) {
     const int tid = threadIdx.x;
-    const int dy_row = tid >> 3, dy_chunk = tid & 7;  // rows dy_row + 32 j
-    const int x_row = tid >> 4, x_chunk = tid & 15;   // rows x_row + 16 j
+    const int my_row = tid >> 2, chunk = tid & 3;
     uint32_t it = 0, used = 0;                        // stages filled, tiles with rows
     bool ok = true;
     for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -139,6 +132,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       if (c.rows == 0) continue;
       const int group0 = c.k * 2, groups = p.K >> 7;
       const bool second = group0 + 1 < groups;
+      const unsigned char* dy0 = p.dy.data + (c.row + my_row) * p.N + c.n * kTileN + chunk * 16;
+      const unsigned char* x0 = p.x.data + (c.row + my_row) * p.K + c.k * kTileK + chunk * 16;
+      const float* dy_scale = p.dy.scale(c.row + my_row, c.n);
+      const float* x_scale = p.x.scale(c.row + my_row, group0);
+      const int blocks = (c.rows + kRows - 1) / kRows;
+      auto fetch = [&](int b, Fetched& f) {
+        const long long r = static_cast<long long>(b) * kRows;
+        const bool on = my_row + r < c.rows;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f.dy[j] = on ? ld_stream(dy0 + r * p.N + j * 64) : zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.x[j] = on && (j < 2 || second) ? ld_stream(x0 + r * p.K + j * 64) : zero;
+        f.y_scale = on ? dy_scale[r * p.dy.row_stride] : 0.0f;
+        f.x_scale[0] = on ? x_scale[r * p.x.row_stride] : 0.0f;
+        f.x_scale[1] = on && second ? x_scale[r * p.x.row_stride + p.x.group_stride] : 0.0f;
+      };
+      Fetched ahead[2];  // two blocks of rows are on their way
+      fetch(0, ahead[0]);
+      fetch(1, ahead[1]);
       // the largest scale of each half of the tile
       float m0 = 0.0f, m1 = 0.0f;
       for (int r = tid; r < c.rows; r += kLoadWarps * 32) {
@@ -158,58 +171,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       }
       ok = __all_sync(kFullMask, wait_or_quit(&s.max_full, used & 1, quit, err));
       if (!ok) break;
-      const int mine = x_chunk >> 3;
-      float m = 0.0f;
+      float down[2];
 #pragma unroll
-      for (int w = 0; w < kLoadWarps; ++w) m = fmaxf(m, s.max_part[used & 1][w][mine]);
-      // 2^e > m; a scale without a finite largest is used as it is
-      int e = m > 0.0f && m < 3.0e38f ? ilogbf(m) + 1 : 0;
-      e = max(-100, min(100, e));
-      if (lane == 0 || lane == 8) {
-        if (warp == 0) s.exponent[used % kExponents][mine] = e;
+      for (int h = 0; h < 2; ++h) {
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kLoadWarps; ++w) m = fmaxf(m, s.max_part[used & 1][w][h]);
+        // 2^e > m; a scale without a finite largest is used as it is
+        int e = m > 0.0f && m < 3.0e38f ? ilogbf(m) + 1 : 0;
+        e = max(-100, min(100, e));
+        if (tid == 0) s.exponent[used % kExponents][h] = e;
+        down[h] = power_of_two(-e);
       }
-      const float down = power_of_two(-e);
-      const bool in_k = c.k * kTileK + x_chunk * 16 < p.K;
-      const unsigned char* dy0 = p.dy.data + c.row * p.N + c.n * kTileN + dy_chunk * 16;
-      const unsigned char* x0 = p.x.data + c.row * p.K + c.k * kTileK + x_chunk * 16;
-      const int blocks = (c.rows + kRows - 1) / kRows;
-      auto fetch = [&](int b, Fetched& f) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = b * kRows + dy_row + 32 * j;
-          f.dy[j] = r < c.rows ? *reinterpret_cast<const uint4*>(dy0 + static_cast<long long>(r) * p.N) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = b * kRows + x_row + 16 * j;
-          const bool on = in_k && r < c.rows;
-          f.x[j] = on ? *reinterpret_cast<const uint4*>(x0 + static_cast<long long>(r) * p.K) : make_uint4(0, 0, 0, 0);
-          f.scale[j] = on ? *p.dy.scale(c.row + r, c.n) * *p.x.scale(c.row + r, group0 + mine) * down : 0.0f;
-        }
-      };
-      Fetched now;
-      fetch(0, now);
-      for (int b = 0; b < blocks; ++b, ++it) {
+      auto block = [&](int b, Fetched& f) {
         const int st = it % kStages;
         if (it >= kStages) {
           ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
-          if (!ok) break;
+          if (!ok) return;
         }
         unsigned char* dy_tile = stages + st * kStageBytes;
         unsigned char* x_tile = dy_tile + kTileN / 64 * kChunkBytes;
-        const Fetched f = now;
-        if (b + 1 < blocks) fetch(b + 1, now);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) store_chunk(dy_tile, dy_row + 32 * j, dy_chunk, f.dy[j], 0u, false);
+        for (int j = 0; j < 2; ++j) store_chunk(dy_tile, my_row, chunk + 4 * j, f.dy[j], 0u, false);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          const float sc = f.y_scale * f.x_scale[j >> 1] * down[j >> 1];
           uint32_t h;
-          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f.scale[j]));
-          store_chunk(x_tile, x_row + 16 * j, x_chunk, f.x[j], h, true);
+          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(sc));
+          store_chunk(x_tile, my_row, chunk + 4 * j, f.x[j], h, true);
         }
+        fetch(b + 2, f);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[st]);
+        ++it;
+      };
+      for (int b = 0; ok && b < blocks; b += 2) {
+        block(b, ahead[0]);
+        if (ok && b + 1 < blocks) block(b + 1, ahead[1]);
       }
       ++used;
     }
