@@ -167,7 +167,8 @@ struct GateArgs {
   const void* logits;  // [T][ld] fp32 or bf16
   long long ld;
   const uint8_t* mask;  // [T] or null: 0 = padding token
-  int T, E, k, groups, keep, sigmoid, ids32, vec;
+  int T, E, k, groups, keep, sigmoid, ids32;
+  int vec;  // rows readable as 16-byte words (grad_vec: writable)
   float coef;
   void* idx;       // [T][k]
   float* weights;  // [T][k]
@@ -180,6 +181,7 @@ struct GateArgs {
   const float* grad_loss;     // [1] or null
   void* grad_logits;          // [T][grad_ld], the logits' type
   long long grad_ld;
+  int grad_vec;
 };
 
 struct SwigluBackwardArgs {

@@ -57,6 +57,12 @@ bool gate_ok(const void* logits, ep_logits_t type, int64_t ld, int T, int E, int
   return T == 0 || (logits && aligned(logits, type == EP_LOGITS_FP32 ? 4 : 2));
 }
 
+// Whether rows of logits split into 16-byte words.
+bool words16(const void* p, ep_logits_t type, int64_t ld, int E) {
+  const int per = type == EP_LOGITS_FP32 ? 4 : 8;
+  return E % per == 0 && ld % per == 0 && aligned(p, 16);
+}
+
 ep::GateArgs gate_args(const void* logits, ep_logits_t type, int64_t ld, const uint8_t* mask, int T, int E, int k,
                        ep_gate_score_t score, float coef, int bits) {
   ep::GateArgs p{};
@@ -70,9 +76,7 @@ ep::GateArgs gate_args(const void* logits, ep_logits_t type, int64_t ld, const u
   p.sigmoid = score == EP_GATE_SIGMOID;
   p.ids32 = bits == 32;
   p.coef = coef;
-  // rows readable as 16-byte words
-  const int per = type == EP_LOGITS_FP32 ? 4 : 8;
-  p.vec = E % per == 0 && ld % per == 0 && aligned(logits, 16);
+  p.vec = words16(logits, type, ld, E);
   return p;
 }
 
@@ -139,6 +143,7 @@ ep_status_t ep_gate_backward(const void* logits, ep_logits_t logits_type, int64_
   p.grad_loss = grad_loss;
   p.grad_logits = grad_logits;
   p.grad_ld = grad_logits_ld;
+  p.grad_vec = words16(grad_logits, logits_type, grad_logits_ld, E);
   return status_of(ep::launch_gate(p, logits_type == EP_LOGITS_BF16, true, sms, reinterpret_cast<cudaStream_t>(stream)),
                    "ep_gate_backward launch");
 }

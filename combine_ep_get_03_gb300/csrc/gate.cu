@@ -25,7 +25,9 @@
 
 namespace ep {
 
-constexpr int kGateWarps = 8;
+// Warps of a block: as many as leave room for a row of floats each.
+__host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 2; }
+__host__ __device__ constexpr int index_bits(int vpl) { return vpl == 1 ? 5 : 1 + index_bits(vpl / 2); }
 constexpr double kFixed = 68719476736.0;  // 2^36
 
 // work: [0] finished blocks, [1] set if a row had no finite sum, [2] unmasked
@@ -92,23 +94,36 @@ __device__ __forceinline__ float warp_max(float x) {
 // min(v,0), which stays away from 0/0 when every sigmoid underflows.
 __device__ __forceinline__ float score_of(float v, float m, int sigmoid) {
   if (!sigmoid) return expf(v - m);
-  return expf(fminf(v, 0.0f) - m) / (1.0f + expf(-fabsf(v)));
+  return __fdividef(expf(fminf(v, 0.0f) - m), 1.0f + expf(-fabsf(v)));
 }
 __device__ __forceinline__ float score_base(float vmax, int sigmoid) {
   const float m = sigmoid ? fminf(vmax, 0.0f) : vmax;
   return m == -CUDART_INF_F ? 0.0f : m;
 }
 // 1 for softmax, 1 - sigmoid(v) for sigmoid
-__device__ __forceinline__ float slope_of(float v, int sigmoid) { return sigmoid ? 1.0f / (1.0f + expf(v)) : 1.0f; }
+__device__ __forceinline__ float slope_of(float v, int sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + expf(v)) : 1.0f; }
+
+// The lane's values sorted out of the keys c[] (order keys whose low bits are
+// replaced by the inverted index, 0 = never chosen): the largest of the warp.
+template <int VPL>
+__device__ __forceinline__ unsigned local_max(const unsigned* c) {
+  unsigned m = c[0];
+#pragma unroll
+  for (int j = 1; j < VPL; ++j) m = max(m, c[j]);
+  return m;
+}
 
 template <typename T, int VPL>
-__global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs p) {
+__global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const GateArgs p) {
+  constexpr int kWarps = gate_warps(VPL);
+  constexpr int kBits = index_bits(VPL);
+  constexpr unsigned kIndex = (1u << kBits) - 1u;
   extern __shared__ float sm[];  // [E] sums, then [E] counts, then [warps][groups] keys
   float* s_sum = sm;
   int* s_count = reinterpret_cast<int*>(sm + p.E);
   unsigned* s_group = reinterpret_cast<unsigned*>(sm + 2 * p.E) + (threadIdx.x >> 5) * p.groups;
   __shared__ int s_live, s_bad, s_last;
-  __shared__ float s_part[kGateWarps];
+  __shared__ float s_part[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.E, k = p.k;
   for (int e = tid; e < E; e += blockDim.x) s_sum[e] = 0.0f, s_count[e] = 0;
@@ -121,37 +136,53 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs
   int live = 0;
   bool bad = false;
   const int gs = E / p.groups;
-  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+  // lanes of a group, where every group is a power of two of whole lanes
+  const int span = gs % VPL == 0 && ((gs / VPL) & (gs / VPL - 1)) == 0 && gs / VPL <= 32 ? gs / VPL : 0;
+  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
     int my_id = -1;
     float my_w = 0.0f;
     if (!p.mask || p.mask[t]) {
       ++live;
-      float v[VPL], c[VPL];
+      float v[VPL];
       load_row<T, VPL>(static_cast<const T*>(p.logits) + t * p.ld, E, lane, p.vec, v);
       // probabilities over all experts
-      float m = -CUDART_INF_F;
+      float m = v[0];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+      for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
       m = score_base(warp_max(m), p.sigmoid);
-      float sum = 0.0f;
+      {
+        float x[VPL], sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        c[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
-        sum += c[j];
+        for (int j = 0; j < VPL; ++j) {
+          x[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+          sum += x[j];
+        }
+        sum = warp_sum(sum);
+        bad |= !(sum < CUDART_INF_F);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // a row of -inf has no probability
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) acc[j] = fmaf(x[j], inv, acc[j]);
       }
-      sum = warp_sum(sum);
-      bad |= !(sum < CUDART_INF_F);
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // a row of -inf has no probability
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) acc[j] = fmaf(c[j], inv, acc[j]);
-
-      // candidates
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) c[j] = v[j];
+      bool allowed = true;  // the lane's experts, where groups are whole lanes
+      unsigned long long kept = ~0ull;
       if (p.groups > 1) {
-        for (int g = lane; g < p.groups; g += 32) s_group[g] = 0u;
-        __syncwarp();
-        {
+        if (span) {
+          unsigned key = 0u;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) key = max(key, order_key(v[j]));
+          for (int d = 1; d < span; d <<= 1) key = max(key, __shfl_xor_sync(kFullMask, key, d));
+          // 0: taken, past the last expert, or not the group's first lane
+          unsigned mine = (lane & (span - 1)) == 0 && lane * VPL < E ? max(key, 1u) : 0u;
+          allowed = false;
+          for (int i = 0; i < p.keep; ++i) {
+            const unsigned top = __reduce_max_sync(kFullMask, mine);
+            const int src = __ffs(__ballot_sync(kFullMask, mine == top)) - 1;
+            if (lane == src) mine = 0u;
+            if ((lane & ~(span - 1)) == src) allowed = true;
+          }
+        } else {
+          for (int g = lane; g < p.groups; g += 32) s_group[g] = 0u;
+          __syncwarp();
           int g = min(lane * VPL, E - 1) / gs, left = (g + 1) * gs - lane * VPL;
           unsigned best = 0u;
 #pragma unroll
@@ -166,60 +197,75 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs
             }
           }
           if (lane * VPL < E) atomicMax(&s_group[g], best);
-        }
-        __syncwarp();
-        // lane l ranks groups 2l and 2l + 1; a group's key + 1 keeps 0 for "taken or absent"
-        unsigned long long kept = 0ull;
-        unsigned g0 = 2 * lane < p.groups ? max(s_group[2 * lane], 1u) : 0u;
-        unsigned g1 = 2 * lane + 1 < p.groups ? max(s_group[2 * lane + 1], 1u) : 0u;
-        for (int i = 0; i < p.keep; ++i) {
-          const unsigned best = __reduce_max_sync(kFullMask, max(g0, g1));
-          const unsigned who = __ballot_sync(kFullMask, max(g0, g1) == best);
-          const int src = __ffs(who) - 1;
-          const int g = __shfl_sync(kFullMask, 2 * lane + (g0 == best ? 0 : 1), src);
-          kept |= 1ull << g;
-          if (lane == src) {
-            if (g0 == best) g0 = 0u; else g1 = 0u;
+          __syncwarp();
+          // lane l ranks groups 2l and 2l + 1; 0: taken or absent
+          kept = 0ull;
+          unsigned g0 = 2 * lane < p.groups ? max(s_group[2 * lane], 1u) : 0u;
+          unsigned g1 = 2 * lane + 1 < p.groups ? max(s_group[2 * lane + 1], 1u) : 0u;
+          for (int i = 0; i < p.keep; ++i) {
+            const unsigned top = __reduce_max_sync(kFullMask, max(g0, g1));
+            const int src = __ffs(__ballot_sync(kFullMask, max(g0, g1) == top)) - 1;
+            const int id = __shfl_sync(kFullMask, 2 * lane + (g0 == top ? 0 : 1), src);
+            kept |= 1ull << id;
+            if (lane == src) {
+              if (g0 == top) g0 = 0u; else g1 = 0u;
+            }
           }
+          __syncwarp();
         }
-        int g = min(lane * VPL, E - 1) / gs, left = (g + 1) * gs - lane * VPL;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          if (left == 0) ++g, left = gs;
-          if (!((kept >> (g & 63)) & 1ull)) c[j] = -CUDART_INF_F;
-          --left;
-        }
-        __syncwarp();
       }
-      // the k largest, one after another
-      unsigned best = 0u;
-      int at = 0;
+      auto usable = [&](int j) {
+        return allowed && (span || p.groups == 1 || ((kept >> min((lane * VPL + j) / gs, 63)) & 1ull));
+      };
+      // The k largest, one after another.  A key's low bits give way to the
+      // inverted index, so one warp maximum names the expert and the owner
+      // drops it by comparing.  bf16 keys lose nothing; of fp32 keys 32 - kBits
+      // bits stay, and rows where two of the first k + 1 agree in them (about
+      // one in a hundred) are settled again below, on whole keys.
+      unsigned c[VPL];
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const unsigned key = order_key(c[j]);
-        if (key > best) best = key, at = j;
+        const unsigned key = order_key(v[j]);
+        c[j] = key && usable(j) ? (key & ~kIndex) | (kIndex - (lane * VPL + j)) : 0u;
       }
-      float my_v = -CUDART_INF_F;
-      for (int i = 0; i < k; ++i) {
+      unsigned best = local_max<VPL>(c), my_key = 0u;
+      constexpr int kMore = sizeof(T) == 4 ? 1 : 0;
+      for (int i = 0; i < k + kMore && i < 32; ++i) {
         const unsigned top = __reduce_max_sync(kFullMask, best);
         if (top == 0u) break;
-        const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
-        const int id = __shfl_sync(kFullMask, lane * VPL + at, src);
-        if (lane == i) {
-          my_id = id;
-          my_v = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
-        }
-        if (lane == src) {
-          const int gone = at;
-          best = 0u;
+        if (lane == i) my_key = top;
 #pragma unroll
-          for (int j = 0; j < VPL; ++j) {
-            if (j == gone) c[j] = -CUDART_INF_F;
-            const unsigned key = order_key(c[j]);
-            if (key > best) best = key, at = j;
-          }
+        for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
+        best = local_max<VPL>(c);
+      }
+      bool again = false;
+      if (kMore) {
+        const unsigned next = __shfl_down_sync(kFullMask, my_key, 1);
+        again = k >= 32 || __any_sync(kFullMask, lane < k && my_key && next && ((my_key ^ next) & ~kIndex) == 0u);
+      }
+      if (!again) {
+        if (lane < k && my_key) my_id = static_cast<int>(kIndex - (my_key & kIndex));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) c[j] = usable(j) ? order_key(v[j]) : 0u;
+        for (int i = 0; i < k; ++i) {
+          best = local_max<VPL>(c);
+          const unsigned top = __reduce_max_sync(kFullMask, best);
+          if (top == 0u) break;
+          const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+          int at = 0;
+#pragma unroll
+          for (int j = VPL - 1; j >= 0; --j)
+            if (c[j] == top) at = j;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (lane == src && j == at) c[j] = 0u;
+          const int id = __shfl_sync(kFullMask, lane * VPL + at, src);
+          if (lane == i) my_id = id;
         }
       }
+      // weights of the chosen: their logits once more, from the cache
+      const float my_v = my_id >= 0 ? load_logit(static_cast<const T*>(p.logits) + t * p.ld + my_id) : -CUDART_INF_F;
       const float top_v = __shfl_sync(kFullMask, my_v, 0);
       const float s = my_id >= 0 ? score_of(my_v, score_base(top_v, p.sigmoid), p.sigmoid) : 0.0f;
       const float s_all = warp_sum(s);
@@ -233,7 +279,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs
     }
   }
   // the block's sums, warp after warp so that their order is fixed
-  for (int w = 0; w < kGateWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w == warp) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
@@ -278,7 +324,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs
   __syncthreads();
   if (tid == 0) {
     float sum = 0.0f;
-    for (int w = 0; w < kGateWarps; ++w) sum += s_part[w];
+    for (int w = 0; w < kWarps; ++w) sum += s_part[w];
     p.count[E] = tokens;
     *p.loss = tokens ? p.coef * E / (static_cast<float>(k) * tokens) * sum : 0.0f;
     p.work[0] = 0u;
@@ -287,39 +333,84 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_forward(const GateArgs
   }
 }
 
+// The lane's VPL gradients of a row, rounded to the logits' type.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(kGateWarps * 32) k_gate_backward(const GateArgs p) {
-  extern __shared__ float sm[];  // [E] counts less their mean
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ void store_row(T* row, int E, int lane, bool vec, const float* d) {
+  constexpr int kChunk = 16 / sizeof(T);
+  const int e0 = lane * VPL;
+  if constexpr (VPL % kChunk == 0) {
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += kChunk) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = sizeof(T) == 4 ? __float_as_uint(d[j + i]) : pack_bf16x2(d[j + (2 * i) % kChunk], d[j + (2 * i + 1) % kChunk]);
+        if (e0 + j < E) *reinterpret_cast<uint4*>(row + e0 + j) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    if (e0 + j < E) row[e0 + j] = static_cast<T>(d[j]);
+}
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const GateArgs p) {
+  constexpr int kWarps = gate_warps(VPL);
+  extern __shared__ float sm[];  // [warps][E]: gradients of the chosen, 0 between tokens
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.k;
+  float* chosen = sm + warp * 32 * VPL;
   const int tokens = p.count[E];
   // sum_e p_e = 1, so c_e may be counted from any common value; from the mean
   // the difference c_e - sum p c loses fewer digits
   const float mean = static_cast<float>(k) * tokens / E;
-  for (int e = tid; e < E; e += blockDim.x) sm[e] = p.count[e] - mean;
-  __syncthreads();
-  const float coef =
-      p.grad_loss && tokens ? *p.grad_loss * p.coef * E / (static_cast<float>(k) * tokens * tokens) : 0.0f;
+  float c[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int e = lane * VPL + j;
+    c[j] = e < E ? p.count[e] - mean : 0.0f;
+    chosen[e] = 0.0f;
+  }
   const bool balance = p.grad_loss && tokens;
-  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+  const float coef = balance ? *p.grad_loss * p.coef * E / (static_cast<float>(k) * tokens * tokens) : 0.0f;
+  __syncwarp();
+  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
     float d[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
     if (!p.mask || p.mask[t]) {
       const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+      int id = -1;
+      if (p.grad_weights) {
+        float dw = 0.0f, v = -CUDART_INF_F;
+        if (lane < k) {
+          const long long o = static_cast<long long>(t) * k + lane;
+          const long long wide = load_topk_id(p.idx, o, p.ids32);
+          dw = p.grad_weights[o];
+          id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
+          if (id >= 0) v = load_logit(row + id);
+        }
+        const float m = score_base(warp_max(v), p.sigmoid);
+        const float s = id >= 0 ? score_of(v, m, p.sigmoid) : 0.0f;
+        const float all = warp_sum(s);
+        const float w = id >= 0 ? s / all : 0.0f;
+        const float mean_dw = warp_sum(id >= 0 ? w * dw : 0.0f);
+        if (id >= 0) atomicAdd(chosen + id, w * slope_of(v, p.sigmoid) * (dw - mean_dw));
+      }
       if (balance) {
-        float v[VPL], c[VPL];
+        float v[VPL];
         load_row<T, VPL>(row, E, lane, p.vec, v);
-        float m = -CUDART_INF_F;
+        float m = v[0];
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+        for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
         m = score_base(warp_max(m), p.sigmoid);
         float sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          const int e = lane * VPL + j;
-          c[j] = e < E ? sm[e] : 0.0f;
-          d[j] = e < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+          d[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
           sum += d[j];
           dot = fmaf(d[j], c[j], dot);
         }
@@ -327,64 +418,44 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_backward(const GateArg
         dot = warp_sum(dot);
         const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : CUDART_NAN_F);
         dot *= inv;
+        const float scale = coef * inv;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) d[j] = coef * (d[j] * inv) * slope_of(v[j], p.sigmoid) * (c[j] - dot);
+        for (int j = 0; j < VPL; ++j) d[j] = scale * d[j] * slope_of(v[j], p.sigmoid) * (c[j] - dot);
       }
       if (p.grad_weights) {
-        int id = -1;
-        float dw = 0.0f, v = -CUDART_INF_F;
-        if (lane < k) {
-          const long long o = static_cast<long long>(t) * k + lane;
-          const long long wide = load_topk_id(p.idx, o, p.ids32);
-          id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
-          if (id >= 0) {
-            dw = p.grad_weights[o];
-            v = load_logit(row + id);
-          }
-        }
-        const float m = score_base(warp_max(v), p.sigmoid);
-        const float s = id >= 0 ? score_of(v, m, p.sigmoid) : 0.0f;
-        const float all = warp_sum(s);
-        const float w = id >= 0 ? s / all : 0.0f;
-        const float mean_dw = warp_sum(w * dw);
-        const float g = id >= 0 ? w * slope_of(v, p.sigmoid) * (dw - mean_dw) : 0.0f;
-        for (int i = 0; i < k; ++i) {
-          const int at = __shfl_sync(kFullMask, id, i) - lane * VPL;
-          const float x = __shfl_sync(kFullMask, g, i);
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < VPL; ++j)
-            if (at == j) d[j] += x;
-        }
+        for (int j = 0; j < VPL; ++j) d[j] += chosen[lane * VPL + j];
+        __syncwarp();
+        if (id >= 0) chosen[id] = 0.0f;
+        __syncwarp();
       }
     }
-    T* out = static_cast<T*>(p.grad_logits) + t * p.grad_ld;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = lane * VPL + j;
-      if (e < E) out[e] = static_cast<T>(d[j]);
-    }
+    store_row<T, VPL>(static_cast<T*>(p.grad_logits) + t * p.grad_ld, E, lane, p.grad_vec, d);
   }
 }
 
 namespace {
 
 template <typename T, int VPL>
-cudaError_t launch_vpl(const GateArgs& p, bool backward, int blocks, cudaStream_t s) {
-  const size_t smem = sizeof(float) * (backward ? p.E : 2 * p.E + (p.groups > 1 ? kGateWarps * p.groups : 0));
-  const dim3 grid(blocks), block(kGateWarps * 32);
+cudaError_t launch_vpl(const GateArgs& p, bool backward, int sms, cudaStream_t s) {
+  constexpr int kWarps = gate_warps(VPL);
+  const int need = (p.T + kWarps - 1) / kWarps, most = sms * (32 / kWarps);
+  const dim3 grid(need < 1 ? 1 : need < most ? need : most), block(kWarps * 32);
+  const size_t smem = sizeof(float) * (backward ? kWarps * 32 * VPL : 2 * p.E + (p.groups > 1 ? kWarps * p.groups : 0));
   return backward ? launch_kernel(k_gate_backward<T, VPL>, grid, block, smem, s, p)
                   : launch_kernel(k_gate_forward<T, VPL>, grid, block, smem, s, p);
 }
 
 template <typename T>
-cudaError_t launch_type(const GateArgs& p, bool backward, int blocks, cudaStream_t s) {
-  if (p.E <= 32) return launch_vpl<T, 1>(p, backward, blocks, s);
-  if (p.E <= 64) return launch_vpl<T, 2>(p, backward, blocks, s);
-  if (p.E <= 128) return launch_vpl<T, 4>(p, backward, blocks, s);
-  if (p.E <= 256) return launch_vpl<T, 8>(p, backward, blocks, s);
-  if (p.E <= 512) return launch_vpl<T, 16>(p, backward, blocks, s);
-  if (p.E <= 1024) return launch_vpl<T, 32>(p, backward, blocks, s);
-  return launch_vpl<T, 128>(p, backward, blocks, s);
+cudaError_t launch_type(const GateArgs& p, bool backward, int sms, cudaStream_t s) {
+  if (p.E <= 32) return launch_vpl<T, 1>(p, backward, sms, s);
+  if (p.E <= 64) return launch_vpl<T, 2>(p, backward, sms, s);
+  if (p.E <= 128) return launch_vpl<T, 4>(p, backward, sms, s);
+  if (p.E <= 256) return launch_vpl<T, 8>(p, backward, sms, s);
+  if (p.E <= 512) return launch_vpl<T, 16>(p, backward, sms, s);
+  if (p.E <= 1024) return launch_vpl<T, 32>(p, backward, sms, s);
+  return launch_vpl<T, 128>(p, backward, sms, s);
 }
 
 }  // namespace
@@ -392,9 +463,7 @@ cudaError_t launch_type(const GateArgs& p, bool backward, int blocks, cudaStream
 size_t gate_work_bytes(int E) { return sizeof(unsigned) * (4 + 3 * static_cast<size_t>(E)); }
 
 cudaError_t launch_gate(const GateArgs& p, bool bf16, bool backward, int sms, cudaStream_t stream) {
-  const int need = (p.T + kGateWarps - 1) / kGateWarps, most = 4 * sms;
-  const int blocks = need < 1 ? 1 : need < most ? need : most;
-  return bf16 ? launch_type<__nv_bfloat16>(p, backward, blocks, stream) : launch_type<float>(p, backward, blocks, stream);
+  return bf16 ? launch_type<__nv_bfloat16>(p, backward, sms, stream) : launch_type<float>(p, backward, sms, stream);
 }
 
 }  // namespace ep
