@@ -2,7 +2,10 @@
 // e4m3 rows with a scale for every 128 channels, and waits that end.
 #pragma once
 
+#include <atomic>
+
 #include "device_common.cuh"
+#include "ep_internal.h"
 
 namespace ep {
 
@@ -162,6 +165,25 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
 }
 
 // ------------------------------------------------------------------ launches
+
+// Once per kernel and device: the whole shared memory for dynamic use, and the
+// register count that a kernel moving registers between warps relies on.
+inline cudaError_t set_up_kernel(const void* kernel, std::atomic<unsigned long long>& ready, int registers) {
+  int device = 0, optin = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device < 64 && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  if (registers) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if (fa.numRegs < registers) return cudaErrorInvalidValue;
+  }
+  if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess) return e;
+  if ((e = set_dynamic_smem_limit(kernel, 0, optin)) != cudaSuccess) return e;
+  if (device < 64) ready.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
 
 struct GateArgs {
   const void* logits;  // [T][ld] fp32 or bf16

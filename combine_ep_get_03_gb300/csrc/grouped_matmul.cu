@@ -32,7 +32,11 @@ constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
 constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // load, MMA and two idle warps fill the third warpgroup
+// Registers: launched with 168 a thread; the third warpgroup hands most of its
+// own to the two that hold accumulators.
+constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 216, kOtherRegisters = 72;
+static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegisters <= kThreads * kLaunchRegisters, "");
 constexpr uint32_t kTmemColumns = 512;
 
 struct Shared {
@@ -100,8 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int blocks_k = p.K / kBlockK;
   const long long tiles = static_cast<long long>(prefix[p.groups.G]) * tiles_n;
 
-  if (warp == kEpilogueWarps) {
-    if (lane == 0) {
+  if (warp >= kEpilogueWarps) {
+    registers_down<kOtherRegisters>();
+    if (warp == kEpilogueWarps && lane == 0) {
       uint32_t it = 0;
       for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
@@ -129,8 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_or_quit(&s.full[i % kStages], parity, &none, err);
       }
     }
-  } else if (warp == kEpilogueWarps + 1) {
-    if (lane == 0) {
+    if (warp == kEpilogueWarps + 1 && lane == 0) {
       constexpr uint32_t desc = mma_desc(kTileM, kTileN, false);
       uint32_t it = 0;
       bool ok = true;
@@ -155,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    registers_up<kEpilogueRegisters>();
     const int half = warp >> 2, quarter = warp & 3;
     const int in_tile = quarter * 32 + lane;  // the thread's row in the tile
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (kTileN / 2);
@@ -187,12 +192,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it >> 1) & 1, quit, err));
         if (!ok) break;
         tmem_fence_after();
+        // 32 columns are on their way while the 32 before them are added
+        uint32_t v[2][32];
+        tmem_load32(lanes + ac * kTileN, v[0]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_load32(lanes + ac * kTileN + q * 32, v);
-          tmem_load_wait();
-          if (q == 3) {
+          tmem_load_wait(v[q & 1]);
+          if (q < 3) {
+            tmem_load32(lanes + ac * kTileN + (q + 1) * 32, v[(q + 1) & 1]);
+          } else {
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = kSwiglu && q >= 2 ? f1 : f0;
           const uint64_t ff = pack2(f, f);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], pack2u(v[2 * j], v[2 * j + 1]), ff);
+          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], pack2u(v[q & 1][2 * j], v[q & 1][2 * j + 1]), ff);
         }
       }
       if (!ok) break;
@@ -345,10 +353,8 @@ cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t str
   const bool swiglu = p.act.data != nullptr;
   const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared) + sizeof(unsigned) * (p.groups.G + 1);
   auto kernel = swiglu ? k_grouped_matmul<true> : k_grouped_matmul<false>;
-  int device = 0, optin = 0;
-  if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess) return e;
-  if ((e = set_dynamic_smem_limit(reinterpret_cast<const void*>(kernel), smem, optin)) != cudaSuccess) return e;
+  static std::atomic<unsigned long long> ready[2];  // devices set up, a bit each
+  if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[swiglu], kLaunchRegisters)) != cudaSuccess) return e;
   return launch_kernel(kernel, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p);
 }
 

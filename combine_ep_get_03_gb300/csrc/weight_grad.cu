@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       for (int q = 0; q < kTileK / 32; ++q) {
         uint32_t v[32];
         tmem_load32(lanes + ac * kTileK + q * 32, v);
-        tmem_load_wait();
+        tmem_load_wait(v);
         if (q == kTileK / 32 - 1) {
           tmem_fence_before();
           __syncwarp();
@@ -296,10 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
 
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream) {
   const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
-  int device = 0, optin = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
-  if (e == cudaSuccess) e = set_dynamic_smem_limit(reinterpret_cast<const void*>(k_weight_grad), smem, optin);
+  static std::atomic<unsigned long long> ready;  // devices set up, a bit each
+  const cudaError_t e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
   if (e != cudaSuccess) return e;
   return launch_kernel(k_weight_grad, dim3(sms), dim3(kThreads), smem, stream, p);
 }

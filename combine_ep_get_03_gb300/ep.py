@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -34,14 +35,9 @@ class EPError(RuntimeError):
         self.status = status
 
 
-class _Groups(ctypes.Structure):
-    _fields_ = [("count", ctypes.c_void_p), ("offset", ctypes.c_void_p), ("num_groups", ctypes.c_int),
-                ("rows", ctypes.c_int64), ("rows_per_group", ctypes.c_int64), ("status", ctypes.c_void_p)]
-
-
-class _Fp8Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
-                ("group_stride", ctypes.c_int64)]
+# ep_groups_t and ep_fp8_rows_t of include/ep.h, as the bytes of one struct
+_GROUPS = struct.Struct("@PPiqqP")
+_FP8_ROWS = struct.Struct("@PPqq")
 
 
 def lib() -> ctypes.CDLL:
@@ -79,7 +75,7 @@ def lib() -> ctypes.CDLL:
             L.ep_check_wait_timeout.argtypes = [P, P]
             L.ep_get_dispatch_layout_noalloc.argtypes = [I, I, I, P, I, P, P, P, P, P, P, P, P, P, P]
             F32 = ctypes.c_float
-            GP, RP = ctypes.POINTER(_Groups), ctypes.POINTER(_Fp8Rows)
+            GP, RP = ctypes.c_char_p, ctypes.c_char_p
             L.ep_gate_workspace_bytes.argtypes = [I, P]
             L.ep_gate_forward.argtypes = [P, I, I64, P, I, I, I, I, I, I, F32, P, I, P, P, P, P, P, I, P]
             L.ep_gate_backward.argtypes = [P, I, I64, P, I, I, I, I, F32, P, I, P, P, P, P, I64, I, P]
@@ -363,75 +359,87 @@ def ep_get_dispatch_layout_noalloc(num_ranks, num_experts, num_topk, topk_idx, n
 # low latency ([E, M, width], group_offset None); FP8 scales follow as the
 # dispatches leave them: [width/128, ld >= rows] or [E, M, width/128].
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# These calls are short, so their checks are written for few attribute reads.
+
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_IDS, _MASK = (torch.int64, torch.int32), (torch.bool, torch.uint8)
 
 
-def _one_device(*tensors) -> None:
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
-
-
-def _rows_ptr(t, dtypes, name):
-    """A row buffer's pointer and its (rows, width); 2-D expert-major or 3-D low latency."""
+def _dev_ptr(t, dtypes, name, dev):
+    """Device pointer of a contiguous tensor on the current device."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and t.dtype in dtypes and t.is_contiguous():
+        return t.data_ptr()
     p = _ptr(t, dtypes, name)
-    _need(t is not None and t.dim() in (2, 3), f"{name} must be [rows, width] or [E, M, width]")
-    width = t.shape[-1]
-    return p, t.numel() // width if width else 0, width
+    if p is None:
+        raise ValueError(f"{name} is required")
+    raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
 
 
-def _fp8_rows(data, scales, name):
-    p, rows, width = _rows_ptr(data, _FP8_BYTES, name)
-    _need(width > 0 and width % 128 == 0, f"{name}'s width must be a positive multiple of 128")
-    sp = _ptr(scales, (torch.float32,), f"{name}_scales")
-    g = width // 128
-    if data.dim() == 2:
-        _need(scales is not None and scales.dim() == 2 and scales.shape[0] == g and scales.shape[1] >= rows,
-              f"{name}_scales must be [{g}, ld >= {rows}] for expert-major rows")
-        r = _Fp8Rows(p, sp, 1, scales.shape[1])
-    else:
-        _need(scales is not None and tuple(scales.shape) == tuple(data.shape[:2]) + (g,),
-              f"{name}_scales must be {list(data.shape[:2]) + [g]} for low-latency rows")
-        r = _Fp8Rows(p, sp, g, 1)
-    return r, rows, width
-
-
-def _groups(rows_like, group_count, group_offset, device_status):
-    cp = _ptr(group_count, (torch.int32,), "group_count")
-    _need(group_count is not None and group_count.dim() == 1, "group_count must be an int32 [E] tensor")
-    E = group_count.numel()
-    if rows_like.dim() == 2:
-        _need(group_offset is not None and group_offset.numel() >= E,
-              "expert-major rows need group_offset: the first row of each of the E groups")
-        rows, per = rows_like.shape[0], 0
-    else:
-        _need(group_offset is None, "low-latency rows [E, M, width] take no group_offset")
-        _need(rows_like.shape[0] == E, f"rows hold {rows_like.shape[0]} groups, group_count {E}")
-        rows, per = rows_like.shape[0] * rows_like.shape[1], rows_like.shape[1]
-    op = _ptr(group_offset, (torch.int32,), "group_offset")
-    _need(device_status is None or device_status.numel() >= 1, "device_status must hold one int32")
-    return _Groups(cp, op, E, rows, per, _ptr(device_status, (torch.int32,), "device_status")), E, rows
-
-
-def _same_rows(a, b, name):
-    _need(b.dim() == a.dim() and b.shape[:-1] == a.shape[:-1], f"{name} must have the rows {list(a.shape[:-1])}")
-
-
-def _weights_ptr(w, w_scales, E, N, K):
-    wp, sp = _ptr(w, _FP8_BYTES, "w"), _ptr(w_scales, (torch.float32,), "w_scales")
-    _need(w is not None and tuple(w.shape) == (E, N, K), f"w must be [{E}, {N}, {K}]")
-    shape = (E, (N + 127) // 128, K // 128)
-    _need(w_scales is not None and tuple(w_scales.shape) == shape, f"w_scales must be {list(shape)}")
-    return wp, sp
-
-
-def _row_vector(t, rows, name):
-    p = _ptr(t, (torch.float32,), name)
-    _need(t is None or t.numel() >= rows, f"{name} needs one value for each of the {rows} rows")
+def _vector(t, n, dtypes, name, dev):
+    p = _dev_ptr(t, dtypes, name, dev)
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, the call needs {n}")
     return p
+
+
+def _optional(t, n, dtypes, name, dev):
+    return None if t is None else _vector(t, n, dtypes, name, dev)
+
+
+def _fp8_rows(data, scales, lead, name, dev):
+    """ep_fp8_rows_t of a row buffer with the leading dimensions `lead`, and its width."""
+    p = _dev_ptr(data, _FP8_BYTES, name, dev)
+    shape = data.shape
+    width = shape[-1] if shape else 0
+    if shape[:-1] != lead or width == 0 or width % 128:
+        raise ValueError(f"{name} must be {list(lead)} rows of a positive multiple of 128, got {list(shape)}")
+    sp = _dev_ptr(scales, _F32, f"{name}_scales", dev)
+    g, have = width >> 7, scales.shape
+    if len(lead) == 1:
+        if len(have) != 2 or have[0] != g or have[1] < lead[0]:
+            raise ValueError(f"{name}_scales must be [{g}, ld >= {lead[0]}] for expert-major rows, got {list(have)}")
+        return _FP8_ROWS.pack(p, sp, 1, have[1]), width
+    if have != (lead[0], lead[1], g):
+        raise ValueError(f"{name}_scales must be {[*lead, g]} for low-latency rows, got {list(have)}")
+    return _FP8_ROWS.pack(p, sp, g, 1), width
+
+
+def _groups(rows_like, group_count, group_offset, device_status, name, dev):
+    """ep_groups_t of a row buffer, its number of groups, rows and leading dimensions."""
+    if not isinstance(rows_like, torch.Tensor) or rows_like.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a [rows, width] or [E, M, width] tensor")
+    lead = rows_like.shape[:-1]
+    cp = _dev_ptr(group_count, _I32, "group_count", dev)
+    E = group_count.numel()
+    if len(lead) == 1:
+        if group_offset is None:
+            raise ValueError("expert-major rows need group_offset: the first row of each group")
+        op, rows, per = _vector(group_offset, E, _I32, "group_offset", dev), lead[0], 0
+    else:
+        if group_offset is not None:
+            raise ValueError("low-latency rows [E, M, width] take no group_offset")
+        if lead[0] != E:
+            raise ValueError(f"{name} holds {lead[0]} groups, group_count {E}")
+        op, per = 0, lead[1]
+        rows = E * per
+    st = _optional(device_status, 1, _I32, "device_status", dev)
+    return _GROUPS.pack(cp, op, E, rows, per, st or 0), E, rows, lead
+
+
+def _bf16_rows(t, lead, name, dev):
+    p = _dev_ptr(t, _BF16, name, dev)
+    if t.shape[:-1] != lead or t.shape[-1] == 0:
+        raise ValueError(f"{name} must be {list(lead)} rows, got {list(t.shape)}")
+    return p, t.shape[-1]
+
+
+def _expert_weights(w, w_scales, E, N, K, dev):
+    wp, sp = _dev_ptr(w, _FP8_BYTES, "w", dev), _dev_ptr(w_scales, _F32, "w_scales", dev)
+    if w.shape != (E, N, K):
+        raise ValueError(f"w must be [{E}, {N}, {K}], got {list(w.shape)}")
+    if w_scales.shape != (E, (N + 127) >> 7, K >> 7):
+        raise ValueError(f"w_scales must be [{E}, {(N + 127) >> 7}, {K >> 7}], got {list(w_scales.shape)}")
+    return wp, sp
 
 
 def ep_gate_workspace_bytes(num_experts: int) -> int:
@@ -440,23 +448,26 @@ def ep_gate_workspace_bytes(num_experts: int) -> int:
     return n.value
 
 
-def _logits(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    _need(t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16), f"{name} must be [T, E] fp32 or bf16")
+def _logits(t, name, dev):
+    """Pointer, type, row stride and shape of [T, E] logits; rows may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be [T, E] fp32 or bf16")
     T, E = t.shape
-    _need(T == 0 or E == 1 or t.stride(1) == 1, f"{name} must have contiguous rows")
-    ld = t.stride(0) if T > 1 else max(E, 1)
-    _need(ld >= E, f"{name}'s rows must not overlap")
+    ld, step = t.stride()
+    if T <= 1:
+        ld = max(E, 1)
+    if (step != 1 and E > 1 and T > 0) or ld < E:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return t.data_ptr(), EP_LOGITS_FP32 if t.dtype == torch.float32 else EP_LOGITS_BF16, ld, T, E
 
 
-def _gate_common(T, topk_idx, token_mask):
-    ip = _ptr(topk_idx, (torch.int64, torch.int32), "topk_idx")
-    _need(topk_idx is not None and topk_idx.dim() == 2 and topk_idx.shape[0] == T, f"topk_idx must be [{T}, k]")
-    mp = _ptr(token_mask, (torch.bool, torch.uint8), "token_mask")
-    _need(token_mask is None or token_mask.numel() >= T, "token_mask needs one value per token")
-    return ip, 64 if topk_idx.dtype == torch.int64 else 32, topk_idx.shape[1], mp
+def _topk(topk_idx, T, dev):
+    p = _dev_ptr(topk_idx, _IDS, "topk_idx", dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k], got {list(topk_idx.shape)}")
+    return p, 64 if topk_idx.dtype == torch.int64 else 32, topk_idx.shape[1]
 
 
 def ep_gate_forward(logits, topk_idx, topk_weights, expert_count, expert_prob, loss, workspace,
@@ -465,19 +476,17 @@ def ep_gate_forward(logits, topk_idx, topk_weights, expert_count, expert_prob, l
     """Top-k routing of logits [T, E] (rows may be strided): fills topk_idx
     [T, k], topk_weights [T, k], expert_count [E + 1], expert_prob [E] and
     loss [1].  workspace: ep_gate_workspace_bytes(E) zeroed bytes, reusable."""
-    lp, lt, ld, T, E = _logits(logits, "logits")
-    ip, bits, k, mp = _gate_common(T, topk_idx, token_mask)
-    for t, n, name in ((topk_weights, T * k, "topk_weights"), (expert_count, E + 1, "expert_count"),
-                       (expert_prob, E, "expert_prob"), (loss, 1, "loss")):
-        _need(isinstance(t, torch.Tensor) and t.numel() >= n, f"{name} must hold {n} elements")
-    _need(isinstance(workspace, torch.Tensor) and workspace.numel() * workspace.element_size() >= 16 + 12 * E,
-          f"workspace must hold {16 + 12 * E} bytes")
-    _one_device(logits, topk_idx, topk_weights, expert_count, expert_prob, loss, workspace, token_mask)
+    dev = torch.cuda.current_device()
+    lp, lt, ld, T, E = _logits(logits, "logits", dev)
+    ip, bits, k = _topk(topk_idx, T, dev)
+    if not isinstance(workspace, torch.Tensor) or workspace.numel() * workspace.element_size() < 16 + 12 * E:
+        raise ValueError(f"workspace must be a tensor of at least {16 + 12 * E} zeroed bytes")
     _check(lib().ep_gate_forward(
-        lp, lt, ld, mp, T, E, k, int(num_groups), int(topk_groups), int(score), float(loss_coef), ip, bits,
-        _ptr(topk_weights, (torch.float32,), "topk_weights"), _ptr(expert_count, (torch.int32,), "expert_count"),
-        _ptr(expert_prob, (torch.float32,), "expert_prob"), _ptr(loss, (torch.float32,), "loss"),
-        _ptr(workspace, None, "workspace"), int(num_sms), _stream(stream)), "ep_gate_forward")
+        lp, lt, ld, _optional(token_mask, T, _MASK, "token_mask", dev), T, E, k, num_groups, topk_groups, score,
+        loss_coef, ip, bits, _vector(topk_weights, T * k, _F32, "topk_weights", dev),
+        _vector(expert_count, E + 1, _I32, "expert_count", dev), _vector(expert_prob, E, _F32, "expert_prob", dev),
+        _vector(loss, 1, _F32, "loss", dev), _dev_ptr(workspace, (workspace.dtype,), "workspace", dev), num_sms,
+        _stream(stream)), "ep_gate_forward")
 
 
 def ep_gate_backward(logits, topk_idx, expert_count, grad_topk_weights, grad_loss, grad_logits,
@@ -485,33 +494,29 @@ def ep_gate_backward(logits, topk_idx, expert_count, grad_topk_weights, grad_los
                      stream=None) -> None:
     """Gradient with respect to the logits from those of topk_weights [T, k]
     and loss [1] (either may be None)."""
-    lp, lt, ld, T, E = _logits(logits, "logits")
-    ip, bits, k, mp = _gate_common(T, topk_idx, token_mask)
-    gp, gt, gld, gT, gE = _logits(grad_logits, "grad_logits")
-    _need((gt, gT, gE) == (lt, T, E), "grad_logits must have the logits' shape and dtype")
-    _need(isinstance(expert_count, torch.Tensor) and expert_count.numel() >= E + 1, "expert_count must be [E + 1]")
-    _need(grad_topk_weights is None or tuple(grad_topk_weights.shape) == (T, k), f"grad_topk_weights must be [{T}, {k}]")
-    _need(grad_loss is None or grad_loss.numel() >= 1, "grad_loss must hold one value")
-    _one_device(logits, topk_idx, expert_count, grad_topk_weights, grad_loss, grad_logits, token_mask)
+    dev = torch.cuda.current_device()
+    lp, lt, ld, T, E = _logits(logits, "logits", dev)
+    ip, bits, k = _topk(topk_idx, T, dev)
+    gp, gt, gld, gT, gE = _logits(grad_logits, "grad_logits", dev)
+    if gt != lt or gT != T or gE != E:
+        raise ValueError("grad_logits must have the logits' shape and dtype")
     _check(lib().ep_gate_backward(
-        lp, lt, ld, mp, T, E, k, int(score), float(loss_coef), ip, bits,
-        _ptr(expert_count, (torch.int32,), "expert_count"),
-        _ptr(grad_topk_weights, (torch.float32,), "grad_topk_weights"), _ptr(grad_loss, (torch.float32,), "grad_loss"),
-        gp, gld, int(num_sms), _stream(stream)), "ep_gate_backward")
+        lp, lt, ld, _optional(token_mask, T, _MASK, "token_mask", dev), T, E, k, score, loss_coef, ip, bits,
+        _vector(expert_count, E + 1, _I32, "expert_count", dev),
+        _optional(grad_topk_weights, T * k, _F32, "grad_topk_weights", dev),
+        _optional(grad_loss, 1, _F32, "grad_loss", dev), gp, gld, num_sms, _stream(stream)), "ep_gate_backward")
 
 
 def ep_grouped_matmul(x, x_scales, w, w_scales, out, group_count, group_offset=None, device_status=None,
                       num_sms: int = 0, stream=None) -> None:
     """out = x @ w[e].T for the rows of every group: e4m3 x and w [E, N, K]
     with 128-channel and 128 x 128 scales, bf16 out."""
-    g, E, rows = _groups(x, group_count, group_offset, device_status)
-    xr, _, K = _fp8_rows(x, x_scales, "x")
-    op, _, N = _rows_ptr(out, (torch.bfloat16,), "out")
-    _same_rows(x, out, "out")
-    wp, sp = _weights_ptr(w, w_scales, E, N, K)
-    _one_device(x, x_scales, w, w_scales, out, group_count, group_offset, device_status)
-    _check(lib().ep_grouped_matmul(ctypes.byref(g), ctypes.byref(xr), wp, sp, N, K, op, int(num_sms),
-                                   _stream(stream)), "ep_grouped_matmul")
+    dev = torch.cuda.current_device()
+    g, E, _, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
+    op, N = _bf16_rows(out, lead, "out", dev)
+    wp, sp = _expert_weights(w, w_scales, E, N, K, dev)
+    _check(lib().ep_grouped_matmul(g, xr, wp, sp, N, K, op, num_sms, _stream(stream)), "ep_grouped_matmul")
 
 
 def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_count, group_offset=None,
@@ -519,22 +524,18 @@ def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_co
                              stream=None) -> None:
     """act = row_weights * silu(gate) * up in e4m3 with scales, where (gate, up)
     = x @ w[e].T, w [E, 2F, K]; pre (optional) keeps (gate, up) in e4m3."""
-    g, E, rows = _groups(x, group_count, group_offset, device_status)
-    xr, _, K = _fp8_rows(x, x_scales, "x")
-    ar, _, F = _fp8_rows(act, act_scales, "act")
-    _same_rows(x, act, "act")
+    dev = torch.cuda.current_device()
+    g, E, rows, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
+    ar, F = _fp8_rows(act, act_scales, lead, "act", dev)
     pr = None
     if pre is not None:
-        pr, _, two = _fp8_rows(pre, pre_scales, "pre")
-        _same_rows(x, pre, "pre")
-        _need(two == 2 * F, f"pre must be {2 * F} wide")
-    wp, sp = _weights_ptr(w, w_scales, E, 2 * F, K)
-    _one_device(x, x_scales, w, w_scales, act, act_scales, row_weights, pre, pre_scales, group_count, group_offset,
-                device_status)
-    _check(lib().ep_grouped_matmul_swiglu(
-        ctypes.byref(g), ctypes.byref(xr), wp, sp, F, K, _row_vector(row_weights, rows, "row_weights"),
-        ctypes.byref(ar), ctypes.byref(pr) if pr is not None else None, int(num_sms), _stream(stream)),
-        "ep_grouped_matmul_swiglu")
+        pr, two = _fp8_rows(pre, pre_scales, lead, "pre", dev)
+        if two != 2 * F:
+            raise ValueError(f"pre must be {2 * F} wide, got {two}")
+    wp, sp = _expert_weights(w, w_scales, E, 2 * F, K, dev)
+    _check(lib().ep_grouped_matmul_swiglu(g, xr, wp, sp, F, K, _optional(row_weights, rows, _F32, "row_weights", dev),
+                                          ar, pr, num_sms, _stream(stream)), "ep_grouped_matmul_swiglu")
 
 
 def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, group_count, group_offset=None,
@@ -542,18 +543,16 @@ def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_sca
                                stream=None) -> None:
     """Gradient of the pre-activations (e4m3 with scales) and of the row
     weights, from grad_act (bf16) and the 8-bit pre-activations."""
-    g, E, rows = _groups(grad_act, group_count, group_offset, device_status)
-    dp, _, F = _rows_ptr(grad_act, (torch.bfloat16,), "grad_act")
-    pr, _, two = _fp8_rows(pre, pre_scales, "pre")
-    gr, _, two_out = _fp8_rows(grad_pre, grad_pre_scales, "grad_pre")
-    _same_rows(grad_act, pre, "pre")
-    _same_rows(grad_act, grad_pre, "grad_pre")
-    _need(two == 2 * F and two_out == 2 * F, f"pre and grad_pre must be {2 * F} wide")
-    _one_device(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, row_weights, grad_row_weights, group_count,
-                group_offset, device_status)
+    dev = torch.cuda.current_device()
+    g, _, rows, lead = _groups(grad_act, group_count, group_offset, device_status, "grad_act", dev)
+    dp, F = _bf16_rows(grad_act, lead, "grad_act", dev)
+    pr, two = _fp8_rows(pre, pre_scales, lead, "pre", dev)
+    gr, two_out = _fp8_rows(grad_pre, grad_pre_scales, lead, "grad_pre", dev)
+    if two != 2 * F or two_out != 2 * F:
+        raise ValueError(f"pre and grad_pre must be {2 * F} wide, got {two} and {two_out}")
     _check(lib().ep_grouped_swiglu_backward(
-        ctypes.byref(g), dp, ctypes.byref(pr), _row_vector(row_weights, rows, "row_weights"), F, ctypes.byref(gr),
-        _row_vector(grad_row_weights, rows, "grad_row_weights"), int(num_sms), _stream(stream)),
+        g, dp, pr, _optional(row_weights, rows, _F32, "row_weights", dev), F, gr,
+        _optional(grad_row_weights, rows, _F32, "grad_row_weights", dev), num_sms, _stream(stream)),
         "ep_grouped_swiglu_backward")
 
 
@@ -561,15 +560,14 @@ def ep_grouped_weight_grad(grad_out, grad_out_scales, x, x_scales, grad_w, group
                            device_status=None, num_sms: int = 0, stream=None) -> None:
     """grad_w[e] = grad_out.T @ x over the rows of group e, both e4m3 with
     scales; bf16 [E, N, K]."""
-    g, E, rows = _groups(x, group_count, group_offset, device_status)
-    yr, _, N = _fp8_rows(grad_out, grad_out_scales, "grad_out")
-    xr, _, K = _fp8_rows(x, x_scales, "x")
-    _same_rows(x, grad_out, "grad_out")
-    gp = _ptr(grad_w, (torch.bfloat16,), "grad_w")
-    _need(grad_w is not None and tuple(grad_w.shape) == (E, N, K), f"grad_w must be [{E}, {N}, {K}]")
-    _one_device(grad_out, grad_out_scales, x, x_scales, grad_w, group_count, group_offset, device_status)
-    _check(lib().ep_grouped_weight_grad(ctypes.byref(g), ctypes.byref(yr), N, ctypes.byref(xr), K, gp, int(num_sms),
-                                        _stream(stream)), "ep_grouped_weight_grad")
+    dev = torch.cuda.current_device()
+    g, E, _, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
+    yr, N = _fp8_rows(grad_out, grad_out_scales, lead, "grad_out", dev)
+    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
+    gp = _dev_ptr(grad_w, _BF16, "grad_w", dev)
+    if grad_w.shape != (E, N, K):
+        raise ValueError(f"grad_w must be [{E}, {N}, {K}], got {list(grad_w.shape)}")
+    _check(lib().ep_grouped_weight_grad(g, yr, N, xr, K, gp, num_sms, _stream(stream)), "ep_grouped_weight_grad")
 
 
 class Handle:
