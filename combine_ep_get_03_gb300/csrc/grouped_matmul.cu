@@ -106,50 +106,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kEpilogueWarps) {
     registers_down<kOtherRegisters>();
-    if (warp == kEpilogueWarps && lane == 0) {
+    if (warp == kEpilogueWarps) {
       uint32_t it = 0;
-      for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
-        bool ok = true;
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           const int st = it % kStages;
-          if (it >= kStages && !(ok = wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err))) break;
-          unsigned char* a = stages + st * kStageBytes;
-          unsigned char* b = a + kTileM * kBlockK;
-          mbar_arrive_expect_tx(&s.full[st], kStageBytes);
-          tma_load_2d(a, &map_x, kb * kBlockK, static_cast<int>(c.row), &s.full[st]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = kSwiglu ? c.n * 128 + (q >> 1) * 64 + (q & 1) * F : c.n * kTileN + q * 64;
-            tma_load_3d(b + q * 64 * kBlockK, &map_w, kb * kBlockK, n, c.group, &s.full[st]);
+          if (it >= kStages) {
+            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
+            if (!ok) break;
           }
+          if (elect_one()) {
+            unsigned char* a = stages + st * kStageBytes;
+            unsigned char* b = a + kTileM * kBlockK;
+            mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+            tma_load_2d(a, &map_x, kb * kBlockK, static_cast<int>(c.row), &s.full[st]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int n = kSwiglu ? c.n * 128 + (q >> 1) * 64 + (q & 1) * F : c.n * kTileN + q * 64;
+              tma_load_3d(b + q * 64 * kBlockK, &map_w, kb * kBlockK, n, c.group, &s.full[st]);
+            }
+          }
+          __syncwarp();
         }
-        if (!ok) break;
       }
       // no load may outlive the block: wait for the last fill of every stage
-      const uint32_t last = it < kStages ? it : kStages;
-      for (uint32_t i = it - last; i < it; ++i) {
-        const uint32_t parity = (i / kStages) & 1;
+      for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) {
         int none = 0;
-        wait_or_quit(&s.full[i % kStages], parity, &none, err);
+        wait_or_quit(&s.full[i % kStages], (i / kStages) & 1, &none, err);
       }
-    }
-    if (warp == kEpilogueWarps + 1 && lane == 0) {
+    } else if (warp == kEpilogueWarps + 1) {
       constexpr uint32_t desc = mma_desc(kTileM, kTileN, false);
+      const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
       uint32_t it = 0;
       bool ok = true;
       for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           const int st = it % kStages, ac = it & 1;
-          if (it >= 2 && !(ok = wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err))) break;
-          if (!(ok = wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err))) break;
+          ok = __all_sync(kFullMask, (it < 2 || wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err)) &&
+                                         wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
+          if (!ok) break;
           tmem_fence_after();
-          const uint32_t a = smem_u32(stages + st * kStageBytes), b = a + kTileM * kBlockK;
+          if (elect_one()) {
+            // descriptors count 16-byte units; 32 channels are two
+            const uint64_t a = first + st * (kStageBytes >> 4), b = a + (kTileM * kBlockK >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8(tmem + ac * kTileN, smem_desc(a + j * 32, 16, 1024), smem_desc(b + j * 32, 16, 1024), desc, j > 0);
-          mma_commit(&s.empty[st]);
-          mma_commit(&s.acc_full[ac]);
+            for (int j = 0; j < 4; ++j) mma_f8(tmem + ac * kTileN, a + 2 * j, b + 2 * j, desc, j > 0);
+            mma_commit(&s.acc_full[ac]);
+            mma_commit(&s.empty[st]);
+          }
+          __syncwarp();
         }
       }
       // nor may an MMA: its last accumulator is complete before TMEM goes back
@@ -177,9 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* sw0 = p.w_scales + (static_cast<long long>(c.group) * Gn + min(n0, Gn - 1)) * Gk;
       const float* sw1 = kSwiglu ? sw0 + static_cast<long long>(F >> 7) * Gk : sw0;
       const float* sx = p.x.scales + (live ? row * p.x.row_stride : 0);
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
       float nx = live ? sx[0] : 0.0f, nw0 = sw0[0], nw1 = kSwiglu ? sw1[0] : 0.0f;
       for (int kb = 0; kb < blocks_k; ++kb, ++it) {
         const int ac = it & 1;
@@ -206,9 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
           }
           const float f = kSwiglu && q >= 2 ? f1 : f0;
-          const uint64_t ff = pack2(f, f);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], pack2u(v[q & 1][2 * j], v[q & 1][2 * j + 1]), ff);
+          for (int j = 0; j < 32; ++j) acc[q * 32 + j] = fmaf(__uint_as_float(v[q & 1][j]), f, acc[q * 32 + j]);
         }
       }
       if (!ok) break;
@@ -220,11 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 8; ++q) {
             uint32_t v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float lo, hi;
-              unpack2(acc[q * 8 + j], &lo, &hi);
-              v[j] = pack_bf16x2(lo, hi);
-            }
+            for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(acc[q * 16 + 2 * j], acc[q * 16 + 2 * j + 1]);
             if (col + q * 16 + 16 <= p.N)
               store32(o + q * 16, v, wide);
             else if (col + q * 16 + 8 <= p.N)
@@ -239,14 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ag = 0.0f, au = 0.0f, aa = 0.0f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-          float g, u;
-          {
-            float lo, hi;
-            unpack2(acc[j >> 1], &lo, &hi);
-            g = (j & 1) ? hi : lo;
-            unpack2(acc[32 + (j >> 1)], &lo, &hi);
-            u = (j & 1) ? hi : lo;
-          }
+          const float g = acc[j], u = acc[64 + j];
           ag = fmaxf(ag, fabsf(g));
           au = fmaxf(au, fabsf(u));
           aa = fmaxf(aa, fabsf(__fdividef(g, 1.0f + __expf(-g)) * u * w));
@@ -267,12 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float sc = group_scale(fmaxf(amax[0][part][in_tile], amax[1][part][in_tile]), &inv);
               if (half == 0) *p.pre.scale(row, c.n + part * (F >> 7)) = sc;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float x[4];
-                unpack2(acc[part * 32 + 2 * j], x, x + 1);
-                unpack2(acc[part * 32 + 2 * j + 1], x + 2, x + 3);
-                q[j] = quant4(x, inv);
-              }
+              for (int j = 0; j < 16; ++j) q[j] = quant4(acc + part * 64 + 4 * j, inv);
               unsigned char* o = p.pre.data + row * p.N + part * F + f;
               const bool w32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
               store32(o, q, w32);
@@ -283,14 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (half == 0) *p.act.scale(row, c.n) = sc;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float g[4], u[4];
-            unpack2(acc[2 * j], g, g + 1);
-            unpack2(acc[2 * j + 1], g + 2, g + 3);
-            unpack2(acc[32 + 2 * j], u, u + 1);
-            unpack2(acc[32 + 2 * j + 1], u + 2, u + 3);
+            float a[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i] * w;
-            q[j] = quant4(g, inv);
+            for (int i = 0; i < 4; ++i)
+              a[i] = __fdividef(acc[4 * j + i], 1.0f + __expf(-acc[4 * j + i])) * acc[64 + 4 * j + i] * w;
+            q[j] = quant4(a, inv);
           }
           unsigned char* o = p.act.data + row * F + f;
           const bool w32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;

@@ -213,34 +213,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       ++used;
     }
   } else if (warp == kLoadWarps + kStoreWarps) {
-    if (lane == 0) {
-      constexpr uint32_t desc = mma_desc(kTileN, kTileK, true);
-      uint32_t it = 0, used = 0;
-      bool ok = true;
-      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile c = tile_at(p.groups, tiles_n, tiles_k, t, false);
-        if (c.rows == 0) continue;
-        const int ac = used & 1, blocks = (c.rows + kRows - 1) / kRows;
-        if (used >= 2 && !(ok = wait_or_quit(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err))) break;
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int st = it % kStages;
-          if (!(ok = wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err))) break;
-          tmem_fence_after();
-          const uint32_t dy = smem_u32(stages + st * kStageBytes), x = dy + kTileN / 64 * kChunkBytes;
-          const int steps = (min(kRows, c.rows - b * kRows) + 15) >> 4;  // 16 rows an MMA
-          for (int j = 0; j < steps; ++j)
-            mma_f16(tmem + ac * kTileK, smem_desc(dy + j * 2048, kChunkBytes, 1024), smem_desc(x + j * 2048, kChunkBytes, 1024),
-                    desc, b > 0 || j > 0);
+    constexpr uint32_t desc = mma_desc(kTileN, kTileK, true);
+    const uint64_t first = smem_desc(smem_u32(stages), kChunkBytes, 1024);
+    uint32_t it = 0, used = 0;
+    bool ok = true;
+    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile c = tile_at(p.groups, tiles_n, tiles_k, t, false);
+      if (c.rows == 0) continue;
+      const int ac = used & 1, blocks = (c.rows + kRows - 1) / kRows;
+      ok = __all_sync(kFullMask, used < 2 || wait_or_quit(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err));
+      if (!ok) break;
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const int st = it % kStages;
+        ok = __all_sync(kFullMask, wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
+        if (!ok) break;
+        tmem_fence_after();
+        if (elect_one()) {
+          // descriptors count 16-byte units; an MMA takes 16 rows of 128 bytes
+          const uint64_t dy = first + st * (kStageBytes >> 4), x = dy + (kTileN / 64 * kChunkBytes >> 4);
+          const int steps = (min(kRows, c.rows - b * kRows) + 15) >> 4;
+#pragma unroll
+          for (int j = 0; j < kRows / 16; ++j)
+            if (j < steps) mma_f16(tmem + ac * kTileK, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
           mma_commit(&s.empty[st]);
         }
-        // also after a wait that gave up: what was issued ends before TMEM goes back
-        mma_commit(&s.acc_full[ac]);
-        ++used;
+        __syncwarp();
       }
-      for (uint32_t i = used < 2 ? 0 : used - 2; i < used; ++i) {
-        int none = 0;
-        wait_or_quit(&s.acc_full[i & 1], (i >> 1) & 1, &none, err);
-      }
+      // also after a wait that gave up: what was issued ends before TMEM goes back
+      if (elect_one()) mma_commit(&s.acc_full[ac]);
+      __syncwarp();
+      ++used;
+    }
+    for (uint32_t i = used < 2 ? 0 : used - 2; i < used; ++i) {
+      int none = 0;
+      wait_or_quit(&s.acc_full[i & 1], (i >> 1) & 1, &none, err);
     }
   } else {
     const int quarter = warp & 3;
