@@ -6,12 +6,14 @@
 // and stored as e4m3 with scales, the pre-activations kept as e4m3 if asked.
 //
 // Tile 128 rows x 256 columns, a block per SM that walks over tiles.  One
-// thread loads 48 KB stages by TMA (128 channels of both operands, 128-byte
-// swizzle), one issues the MMAs: four per stage into a fresh TMEM accumulator,
-// since every 128 channels carry their own scale.  Two accumulators of 256
-// columns alternate, so while the tensor cores fill one, eight warps read the
-// other (a thread owns a row, so its factor sx * sw is one number) and add it,
-// scaled, to fp32 registers: 128 a thread.
+// warp loads 48 KB stages by TMA (128 channels of both operands, 128-byte
+// swizzle); four MMAs a stage go into a fresh TMEM accumulator, since every
+// 128 channels carry their own scale.  Two accumulators of 256 columns
+// alternate, so while the tensor cores fill one, eight warps read the other (a
+// thread owns a row, so its factor sx * sw is one number) and add it, scaled,
+// to fp32 registers: 128 a thread.  Each accumulator has its own issuing warp:
+// a wait on a barrier that is already complete takes some 180 cycles here, two
+// of them and the issue 620, more than the 512 of a stage's MMAs.
 //
 // SwiGLU takes its 256 columns as gate 64, up 64, gate 64, up 64 so that a
 // thread holds gate and up of the same channel and the row's 128-channel
@@ -32,7 +34,7 @@ constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
 constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // load, MMA and two idle warps fill the third warpgroup
+constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and an idle warp fill the third warpgroup
 // Registers: launched with 168 a thread; the third warpgroup hands most of its
 // own to the two that hold accumulators.
 constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 216, kOtherRegisters = 72;
@@ -136,33 +138,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         int none = 0;
         wait_or_quit(&s.full[i % kStages], (i / kStages) & 1, &none, err);
       }
-    } else if (warp == kEpilogueWarps + 1) {
+    } else if (warp <= kEpilogueWarps + 2) {
+      const int ac = warp - kEpilogueWarps - 1;  // the warp's accumulator: even or odd blocks of k
       constexpr uint32_t desc = mma_desc(kTileM, kTileN, false);
       const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
-      uint32_t it = 0;
-      bool ok = true;
-      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-          const int st = it % kStages, ac = it & 1;
-          ok = __all_sync(kFullMask, (it < 2 || wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err)) &&
-                                         wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
-          if (!ok) break;
-          tmem_fence_after();
-          if (elect_one()) {
-            // descriptors count 16-byte units; 32 channels are two
-            const uint64_t a = first + st * (kStageBytes >> 4), b = a + (kTileM * kBlockK >> 4);
+      const long long mine = tiles > blockIdx.x ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+      const uint32_t all = static_cast<uint32_t>(mine * blocks_k);  // blocks of k of this block's tiles
+      uint32_t it = ac;
+      for (; it < all; it += 2) {
+        const int st = it % kStages;
+        const bool ok = __all_sync(kFullMask, (it < 2 || wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err)) &&
+                                                  wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
+        if (!ok) break;
+        tmem_fence_after();
+        if (elect_one()) {
+          // descriptors count 16-byte units; 32 channels are two
+          const uint64_t a = first + st * (kStageBytes >> 4), b = a + (kTileM * kBlockK >> 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f8(tmem + ac * kTileN, a + 2 * j, b + 2 * j, desc, j > 0);
-            mma_commit(&s.acc_full[ac]);
-            mma_commit(&s.empty[st]);
-          }
-          __syncwarp();
+          for (int j = 0; j < 4; ++j) mma_f8(tmem + ac * kTileN, a + 2 * j, b + 2 * j, desc, j > 0);
+          mma_commit(&s.acc_full[ac]);
+          mma_commit(&s.empty[st]);
         }
+        __syncwarp();
       }
       // nor may an MMA: its last accumulator is complete before TMEM goes back
-      for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) {
+      if (it >= 2) {
         int none = 0;
-        wait_or_quit(&s.acc_full[i & 1], (i >> 1) & 1, &none, err);
+        wait_or_quit(&s.acc_full[ac], ((it - 2) >> 1) & 1, &none, err);
       }
     }
   } else {
