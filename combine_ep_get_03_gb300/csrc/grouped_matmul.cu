@@ -37,9 +37,10 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and an idle warp fill the third warpgroup
 // Registers: launched with 168 a thread; the third warpgroup hands most of its
 // own to the two that hold accumulators.
-constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 216, kOtherRegisters = 72;
+constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 232, kOtherRegisters = 40;
 static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegisters <= kThreads * kLaunchRegisters, "");
 constexpr uint32_t kTmemColumns = 512;
+constexpr int kScalesAhead = 5;
 
 struct Shared {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], amax_full;
@@ -72,6 +73,8 @@ __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* pref
 }
 
 }  // namespace
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" : : "l"(p)); }
 
 template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -190,11 +193,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
       float nx = live ? sx[0] : 0.0f, nw0 = sw0[0], nw1 = kSwiglu ? sw1[0] : 0.0f;
+#pragma unroll
+      for (int i = 1; i < kScalesAhead; ++i)
+        if (live && i < blocks_k) prefetch_l1(sx + i * p.x.group_stride);
       for (int kb = 0; kb < blocks_k; ++kb, ++it) {
         const int ac = it & 1;
         const float f0 = nx * nw0, f1 = kSwiglu ? nx * nw1 : f0;
         if (kb + 1 < blocks_k) {
-          nx = live ? sx[(kb + 1) * p.x.group_stride] : 0.0f;
+          // one block ahead in registers, kScalesAhead in L1
+          if (live) {
+            sx += p.x.group_stride;
+            nx = *sx;
+            if (kb + kScalesAhead < blocks_k) prefetch_l1(sx + (kScalesAhead - 1) * p.x.group_stride);
+          }
           nw0 = sw0[kb + 1];
           if (kSwiglu) nw1 = sw1[kb + 1];
         }
