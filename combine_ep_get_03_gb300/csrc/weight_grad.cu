@@ -11,11 +11,12 @@
 // put back on the fp32 sums.  That costs x two roundings to 11 bits, an eighth
 // of the rounding of the bf16 result.
 //
-// Tile 128 (n) x 256 (k).  Eight warps fetch e4m3 rows 64 at a time, widen
-// and store them with the 128-byte swizzle, rows along the long axis (both
-// operands "MN major", so nothing is transposed); one thread issues four MMAs
-// for them; four more warps write the previous tile from the other TMEM
-// accumulator.  Rows past the group's end enter as zeros.
+// Tile 128 (n) x 256 (k), 64 rows a stage.  Two teams of eight warps take
+// every other stage: they fetch e4m3 rows a turn ahead (also across tiles),
+// widen and store them with the 128-byte swizzle, rows along the long axis (both operands "MN major", so nothing is
+// transposed); one warp issues four MMAs a stage; four more write the previous
+// tile from the other TMEM accumulator; one looks up the next tile's largest
+// scale.  Rows past the group's end enter as zeros.
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "tcgen05.cuh"
@@ -28,34 +29,75 @@ constexpr int kTileN = 128, kTileK = 256, kRows = 64;
 constexpr int kStages = 4;
 constexpr int kChunkBytes = kRows * 128;  // 64 columns of f16
 constexpr int kStageBytes = (kTileN + kTileK) / 64 * kChunkBytes;
-constexpr int kLoadWarps = 8, kStoreWarps = 4;
-constexpr int kThreads = (kLoadWarps + kStoreWarps + 1) * 32;
+constexpr int kTeams = 2, kTeamWarps = 8, kLoadWarps = kTeams * kTeamWarps, kStoreWarps = 4;
+constexpr int kMmaWarp = kLoadWarps + kStoreWarps, kScaleWarp = kMmaWarp + 1;
+constexpr int kThreads = (kScaleWarp + 1) * 32;
 constexpr uint32_t kTmemColumns = 512;
-constexpr int kExponents = 8;  // tiles whose exponents are kept: stages + accumulators + 1, rounded up
+constexpr int kExponents = 4;  // tiles whose exponents are kept
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], max_full;
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], exp_full[kExponents], exp_empty[kExponents];
   uint32_t tmem;
   int quit;
-  float max_part[2][kLoadWarps][2];
   int exponent[kExponents][2];
 };
 
-struct Tile {
-  int group, n, k, rows;
-  long long row;
+// First row and row count of every group, in shared memory.
+struct Group {
+  int row, rows;
 };
 
-__device__ __forceinline__ Tile tile_at(const GroupArgs& a, int tiles_n, int tiles_k, long long t, bool report) {
-  Tile c;
-  const long long per = static_cast<long long>(tiles_n) * tiles_k;
-  c.group = static_cast<int>(t / per);
-  const int local = static_cast<int>(t % per);
-  c.n = local / tiles_k;
-  c.k = local % tiles_k;
-  c.rows = group_span(a, c.group, &c.row, report);
-  return c;
-}
+// The block's tiles that have rows, one after another.
+struct Walk {
+  const Group* groups;
+  int tiles_n, tiles_k;
+  long long t, tiles;
+  int group, n, k, rows;
+  __device__ __forceinline__ void set() {
+    const long long per = static_cast<long long>(tiles_n) * tiles_k;
+    group = static_cast<int>(t / per);
+    const int local = static_cast<int>(t % per);
+    n = local / tiles_k;
+    k = local % tiles_k;
+    rows = groups[group].rows;
+  }
+  __device__ __forceinline__ bool settle() {  // at t or after it
+    for (; t < tiles; t += gridDim.x) {
+      set();
+      if (rows) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool next() {
+    t += gridDim.x;
+    return settle();
+  }
+  __device__ __forceinline__ int blocks() const { return (rows + kRows - 1) / kRows; }
+  __device__ __forceinline__ long long row() const { return groups[group].row; }
+};
+
+// A block of rows of a walk: block b of the used-th tile that has rows.
+struct Cursor {
+  Walk w;
+  int b, blocks;
+  uint32_t used;
+  bool on;
+  __device__ __forceinline__ void begin(const Walk& walk) {
+    w = walk;
+    b = 0;
+    used = 0;
+    on = w.settle();
+    blocks = on ? w.blocks() : 0;
+  }
+  __device__ __forceinline__ void step() {
+    if (on && ++b == blocks) {
+      on = w.next();
+      blocks = on ? w.blocks() : 0;
+      b = 0;
+      ++used;
+    }
+  }
+};
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -91,8 +133,20 @@ __device__ __forceinline__ void store_chunk(unsigned char* tile, int r, int c, c
   sts128(line + (((u + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
 }
 
-// One thread's part of 64 rows, all of one row: chunks c, c + 4 of dy and
-// c, c + 4, c + 8, c + 12 of x (c = thread mod 4), and the row's scales.
+// A load that stays where it is written, far ahead of its use.
+__device__ __forceinline__ uint4 ld_ahead(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_ahead_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// One thread's part of 64 rows: of one row, chunks c, c + 4 of dy and c, c + 4,
+// c + 8, c + 12 of x (c = thread mod 4), and the scales of both halves of x.
 struct Fetched {
   uint4 dy[2], x[4];
   float y_scale, x_scale[2];
@@ -107,120 +161,129 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* quit = &s.quit;
   int* err = p.groups.err;
+  Group* groups = reinterpret_cast<Group*>(&s + 1);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], kLoadWarps), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], kTeamWarps), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kStoreWarps);
-    mbar_init(&s.max_full, kLoadWarps);
+    for (int i = 0; i < kExponents; ++i) mbar_init(&s.exp_full[i], 1), mbar_init(&s.exp_empty[i], kStoreWarps);
     s.quit = 0;
     mbar_init_fence();
   }
-  if (warp == kLoadWarps + kStoreWarps) tmem_alloc(&s.tmem, kTmemColumns);
+  if (warp == kMmaWarp) tmem_alloc(&s.tmem, kTmemColumns);
+  for (int g = threadIdx.x; g < p.groups.G; g += kThreads) {
+    long long start;
+    groups[g].rows = group_span(p.groups, g, &start, blockIdx.x == 0);
+    groups[g].row = static_cast<int>(start);
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
-  const int tiles_n = p.N / kTileN, tiles_k = (p.K + kTileK - 1) / kTileK;
-  const long long tiles = static_cast<long long>(p.groups.G) * tiles_n * tiles_k;
+  Walk w;
+  w.groups = groups;
+  w.tiles_n = p.N / kTileN;
+  w.tiles_k = (p.K + kTileK - 1) / kTileK;
+  w.tiles = static_cast<long long>(p.groups.G) * w.tiles_n * w.tiles_k;
+  w.t = blockIdx.x;
 
   if (warp < kLoadWarps) {
-    const int tid = threadIdx.x;
+    const int team = warp / kTeamWarps, tid = threadIdx.x % (kTeamWarps * 32);
     const int my_row = tid >> 2, chunk = tid & 3;
-    uint32_t it = 0, used = 0;                        // stages filled, tiles with rows
-    bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile c = tile_at(p.groups, tiles_n, tiles_k, t, blockIdx.x == 0 && tid == 0);
-      if (c.rows == 0) continue;
-      const int group0 = c.k * 2, groups = p.K >> 7;
-      const bool second = group0 + 1 < groups;
-      const unsigned char* dy0 = p.dy.data + (c.row + my_row) * p.N + c.n * kTileN + chunk * 16;
-      const unsigned char* x0 = p.x.data + (c.row + my_row) * p.K + c.k * kTileK + chunk * 16;
-      const float* dy_scale = p.dy.scale(c.row + my_row, c.n);
-      const float* x_scale = p.x.scale(c.row + my_row, group0);
-      const int blocks = (c.rows + kRows - 1) / kRows;
-      auto fetch = [&](int b, Fetched& f) {
-        const long long r = static_cast<long long>(b) * kRows;
-        const bool on = my_row + r < c.rows;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+    Cursor now, next;  // the team's block and the one it fetches
+    now.begin(w);
+    if (team) now.step();
+    next = now;
+    auto fetch = [&](Fetched& d) {
+      const long long r = next.w.row() + next.b * kRows + my_row;
+      const bool on = next.on && next.b * kRows + my_row < next.w.rows;
+      const bool second = on && next.w.k * 2 + 1 < (p.K >> 7);
+      const unsigned char* dy = p.dy.data + r * p.N + next.w.n * kTileN + chunk * 16;
+      const unsigned char* x = p.x.data + r * p.K + next.w.k * kTileK + chunk * 16;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) f.dy[j] = on ? ld_stream(dy0 + r * p.N + j * 64) : zero;
+      for (int j = 0; j < 2; ++j) d.dy[j] = on ? ld_ahead(dy + j * 64) : zero;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f.x[j] = on && (j < 2 || second) ? ld_stream(x0 + r * p.K + j * 64) : zero;
-        f.y_scale = on ? dy_scale[r * p.dy.row_stride] : 0.0f;
-        f.x_scale[0] = on ? x_scale[r * p.x.row_stride] : 0.0f;
-        f.x_scale[1] = on && second ? x_scale[r * p.x.row_stride + p.x.group_stride] : 0.0f;
-      };
-      Fetched ahead[2];  // two blocks of rows are on their way
-      fetch(0, ahead[0]);
-      fetch(1, ahead[1]);
-      // the largest scale of each half of the tile
-      float m0 = 0.0f, m1 = 0.0f;
-      for (int r = tid; r < c.rows; r += kLoadWarps * 32) {
-        const float y = *p.dy.scale(c.row + r, c.n);
-        m0 = fmaxf(m0, fabsf(y * *p.x.scale(c.row + r, group0)));
-        if (second) m1 = fmaxf(m1, fabsf(y * *p.x.scale(c.row + r, group0 + 1)));
+      for (int j = 0; j < 4; ++j) d.x[j] = (j < 2 ? on : second) ? ld_ahead(x + j * 64) : zero;
+      d.y_scale = on ? ld_ahead_f32(p.dy.scale(r, next.w.n)) : 0.0f;
+      d.x_scale[0] = on ? ld_ahead_f32(p.x.scale(r, next.w.k * 2)) : 0.0f;
+      d.x_scale[1] = second ? ld_ahead_f32(p.x.scale(r, next.w.k * 2 + 1)) : 0.0f;
+    };
+    Fetched d;
+    if (next.on) fetch(d);
+    uint32_t tile = ~0u;  // whose exponents `down` holds
+    float down[2] = {1.0f, 1.0f};
+    for (uint32_t it = team; now.on; it += kTeams) {
+      const int st = it % kStages;
+      bool ok = true;
+      if (now.used != tile) {
+        tile = now.used;
+        const int e = tile % kExponents;
+        ok = wait_or_quit(&s.exp_full[e], (tile / kExponents) & 1, quit, err);
+        down[0] = power_of_two(-s.exponent[e][0]);
+        down[1] = power_of_two(-s.exponent[e][1]);
+      }
+      if (it >= kStages) ok = ok && wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err);
+      if (!__all_sync(kFullMask, ok)) break;
+      unsigned char* dy_tile = stages + st * kStageBytes;
+      unsigned char* x_tile = dy_tile + kTileN / 64 * kChunkBytes;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) store_chunk(dy_tile, my_row, chunk + 4 * j, d.dy[j], 0u, false);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float sc = d.y_scale * d.x_scale[j >> 1] * down[j >> 1];
+        uint32_t h;
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(sc));
+        store_chunk(x_tile, my_row, chunk + 4 * j, d.x[j], h, true);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.full[st]);
+      next.step();
+      next.step();
+      if (next.on) fetch(d);
+      now = next;
+    }
+  } else if (warp == kScaleWarp) {
+    // the largest scale of each half of the tiles to come: 2^e above it
+    uint32_t used = 0;
+    for (bool on = w.settle(); on; on = w.next(), ++used) {
+      const int e = used % kExponents;
+      if (used >= kExponents &&
+          !__all_sync(kFullMask, wait_or_quit(&s.exp_empty[e], ((used / kExponents) & 1) ^ 1, quit, err)))
+        break;
+      const bool second = w.k * 2 + 1 < (p.K >> 7);
+      const float* ys = p.dy.scale(w.row(), w.n);
+      const float* xs = p.x.scale(w.row(), w.k * 2);
+      float m[2] = {0.0f, 0.0f};
+#pragma unroll 8
+      for (int r = lane; r < w.rows; r += 32) {
+        const float y = ys[r * p.dy.row_stride];
+        m[0] = fmaxf(m[0], fabsf(y * xs[r * p.x.row_stride]));
+        if (second) m[1] = fmaxf(m[1], fabsf(y * xs[r * p.x.row_stride + p.x.group_stride]));
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) {
-        m0 = fmaxf(m0, __shfl_xor_sync(kFullMask, m0, d));
-        m1 = fmaxf(m1, __shfl_xor_sync(kFullMask, m1, d));
+        m[0] = fmaxf(m[0], __shfl_xor_sync(kFullMask, m[0], d));
+        m[1] = fmaxf(m[1], __shfl_xor_sync(kFullMask, m[1], d));
       }
       if (lane == 0) {
-        s.max_part[used & 1][warp][0] = m0;
-        s.max_part[used & 1][warp][1] = m1;
-        mbar_arrive(&s.max_full);
-      }
-      ok = __all_sync(kFullMask, wait_or_quit(&s.max_full, used & 1, quit, err));
-      if (!ok) break;
-      float down[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float m = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kLoadWarps; ++w) m = fmaxf(m, s.max_part[used & 1][w][h]);
-        // 2^e > m; a scale without a finite largest is used as it is
-        int e = m > 0.0f && m < 3.0e38f ? ilogbf(m) + 1 : 0;
-        e = max(-100, min(100, e));
-        if (tid == 0) s.exponent[used % kExponents][h] = e;
-        down[h] = power_of_two(-e);
-      }
-      auto block = [&](int b, Fetched& f) {
-        const int st = it % kStages;
-        if (it >= kStages) {
-          ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
-          if (!ok) return;
+        for (int h = 0; h < 2; ++h) {
+          // a scale without a finite largest is used as it is
+          const int x = m[h] > 0.0f && m[h] < 3.0e38f ? ilogbf(m[h]) + 1 : 0;
+          s.exponent[e][h] = max(-100, min(100, x));
         }
-        unsigned char* dy_tile = stages + st * kStageBytes;
-        unsigned char* x_tile = dy_tile + kTileN / 64 * kChunkBytes;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) store_chunk(dy_tile, my_row, chunk + 4 * j, f.dy[j], 0u, false);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float sc = f.y_scale * f.x_scale[j >> 1] * down[j >> 1];
-          uint32_t h;
-          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(sc));
-          store_chunk(x_tile, my_row, chunk + 4 * j, f.x[j], h, true);
-        }
-        fetch(b + 2, f);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[st]);
-        ++it;
-      };
-      for (int b = 0; ok && b < blocks; b += 2) {
-        block(b, ahead[0]);
-        if (ok && b + 1 < blocks) block(b + 1, ahead[1]);
+        mbar_arrive(&s.exp_full[e]);
       }
-      ++used;
+      __syncwarp();
     }
-  } else if (warp == kLoadWarps + kStoreWarps) {
+  } else if (warp == kMmaWarp) {
     constexpr uint32_t desc = mma_desc(kTileN, kTileK, true);
     const uint64_t first = smem_desc(smem_u32(stages), kChunkBytes, 1024);
     uint32_t it = 0, used = 0;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile c = tile_at(p.groups, tiles_n, tiles_k, t, false);
-      if (c.rows == 0) continue;
-      const int ac = used & 1, blocks = (c.rows + kRows - 1) / kRows;
+    for (bool on = w.settle(); ok && on; on = w.next()) {
+      const int ac = used & 1, blocks = w.blocks();
       ok = __all_sync(kFullMask, used < 2 || wait_or_quit(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err));
       if (!ok) break;
       for (int b = 0; b < blocks; ++b, ++it) {
@@ -231,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
         if (elect_one()) {
           // descriptors count 16-byte units; an MMA takes 16 rows of 128 bytes
           const uint64_t dy = first + st * (kStageBytes >> 4), x = dy + (kTileN / 64 * kChunkBytes >> 4);
-          const int steps = (min(kRows, c.rows - b * kRows) + 15) >> 4;
+          const int steps = (min(kRows, w.rows - b * kRows) + 15) >> 4;
 #pragma unroll
           for (int j = 0; j < kRows / 16; ++j)
             if (j < steps) mma_f16(tmem + ac * kTileK, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
@@ -253,19 +316,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const bool wide = (reinterpret_cast<uintptr_t>(p.dw) & 31) == 0;
     uint32_t used = 0;
-    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Tile c = tile_at(p.groups, tiles_n, tiles_k, t, false);
-      uint16_t* o = p.dw + (static_cast<long long>(c.group) * p.N + c.n * kTileN + quarter * 32 + lane) * p.K + c.k * kTileK;
-      const int columns = min(kTileK, p.K - c.k * kTileK);
-      if (c.rows == 0) {
+    for (; w.t < w.tiles; w.t += gridDim.x) {
+      w.set();
+      uint16_t* o = p.dw + (static_cast<long long>(w.group) * p.N + w.n * kTileN + quarter * 32 + lane) * p.K + w.k * kTileK;
+      const int columns = min(kTileK, p.K - w.k * kTileK);
+      if (w.rows == 0) {
         const uint32_t zero[8] = {};
         for (int q = 0; q < columns; q += 16) store32(o + q, zero, wide);
         continue;
       }
-      const int ac = used & 1;
-      if (!__all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (used >> 1) & 1, quit, err))) break;
+      const int ac = used & 1, e = used % kExponents;
+      if (!__all_sync(kFullMask, wait_or_quit(&s.exp_full[e], (used / kExponents) & 1, quit, err) &&
+                                     wait_or_quit(&s.acc_full[ac], (used >> 1) & 1, quit, err)))
+        break;
       tmem_fence_after();
-      const float up[2] = {power_of_two(s.exponent[used % kExponents][0]), power_of_two(s.exponent[used % kExponents][1])};
+      const float up[2] = {power_of_two(s.exponent[e][0]), power_of_two(s.exponent[e][1])};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.exp_empty[e]);
 #pragma unroll
       for (int q = 0; q < kTileK / 32; ++q) {
         uint32_t v[32];
@@ -280,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
         if (q * 32 < columns) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t w[8];
+            uint32_t x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              w[j] = pack_bf16x2(__uint_as_float(v[h * 16 + 2 * j]) * f, __uint_as_float(v[h * 16 + 2 * j + 1]) * f);
-            store32(o + q * 32 + h * 16, w, wide);
+              x[j] = pack_bf16x2(__uint_as_float(v[h * 16 + 2 * j]) * f, __uint_as_float(v[h * 16 + 2 * j + 1]) * f);
+            store32(o + q * 32 + h * 16, x, wide);
           }
         }
       }
@@ -294,14 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == kLoadWarps + kStoreWarps) {
+  if (warp == kMmaWarp) {
     tmem_fence_after();
     tmem_free(tmem, kTmemColumns);
   }
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream) {
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
+  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared) + sizeof(Group) * p.groups.G;
   static std::atomic<unsigned long long> ready;  // devices set up, a bit each
   const cudaError_t e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
   if (e != cudaSuccess) return e;
