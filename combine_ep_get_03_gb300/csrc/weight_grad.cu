@@ -112,14 +112,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void sts128(unsigned char* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" : : "r"(smem_u32(p)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" : : "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 codes of row r, 16-channel chunk c of an operand, to its f16 tile.  A
-// phase of a warp's 16-byte stores covers two rows of one 64-channel block,
-// whose swizzled units are the even and the odd ones: no bank conflict.
-__device__ __forceinline__ void store_chunk(unsigned char* tile, int r, int c, const uint4& q, uint32_t scale, bool scaled) {
+// 16 codes to f16, at the two shared-memory addresses of their 16-byte units.
+__device__ __forceinline__ void store_chunk(uint32_t lo, uint32_t hi, const uint4& q, uint32_t scale, bool scaled) {
   uint32_t h[8];
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -127,10 +125,8 @@ __device__ __forceinline__ void store_chunk(unsigned char* tile, int r, int c, c
     e4m3x4_to_f16(w[i], &h[2 * i], &h[2 * i + 1]);
     if (scaled) h[2 * i] = mul_f16x2(h[2 * i], scale), h[2 * i + 1] = mul_f16x2(h[2 * i + 1], scale);
   }
-  unsigned char* line = tile + (c >> 2) * kChunkBytes + r * 128;
-  const int u = (c & 3) * 2, x = r & 7;
-  sts128(line + ((u ^ x) << 4), h[0], h[1], h[2], h[3]);
-  sts128(line + (((u + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
+  sts128(lo, h[0], h[1], h[2], h[3]);
+  sts128(hi, h[4], h[5], h[6], h[7]);
 }
 
 // A load that stays where it is written, far ahead of its use.
@@ -189,25 +185,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
   if (warp < kLoadWarps) {
     const int team = warp / kTeamWarps, tid = threadIdx.x % (kTeamWarps * 32);
     const int my_row = tid >> 2, chunk = tid & 3;
+    // Row my_row, chunk c = chunk + 4 j of an operand lies in 64-channel block j
+    // at swizzled units 2 chunk and 2 chunk + 1.  A phase of a warp's 16-byte
+    // stores covers two rows, whose units are the even and the odd ones: no
+    // bank conflict.
+    const uint32_t line = smem_u32(stages) + my_row * 128;
+    const uint32_t unit_lo = line + (((2 * chunk) ^ (my_row & 7)) << 4);
+    const uint32_t unit_hi = line + (((2 * chunk + 1) ^ (my_row & 7)) << 4);
     Cursor now, next;  // the team's block and the one it fetches
     now.begin(w);
     if (team) now.step();
     next = now;
+    // what the fetched tile's block 0 would read, and steps from block to block
+    const unsigned char *dy = nullptr, *x = nullptr;
+    const float *dy_scale = nullptr, *x_scale = nullptr;
+    const long long dy_step = static_cast<long long>(kRows) * p.N, x_step = static_cast<long long>(kRows) * p.K;
+    const long long dys_step = kRows * p.dy.row_stride, xs_step = kRows * p.x.row_stride;
+    bool second = false;
+    auto aim = [&]() {
+      const long long r = next.w.row() + my_row;
+      dy = p.dy.data + r * p.N + next.w.n * kTileN + chunk * 16 + next.b * dy_step;
+      x = p.x.data + r * p.K + next.w.k * kTileK + chunk * 16 + next.b * x_step;
+      dy_scale = p.dy.scale(r, next.w.n) + next.b * dys_step;
+      x_scale = p.x.scale(r, next.w.k * 2) + next.b * xs_step;
+      second = next.w.k * 2 + 1 < (p.K >> 7);
+    };
     auto fetch = [&](Fetched& d) {
-      const long long r = next.w.row() + next.b * kRows + my_row;
-      const bool on = next.on && next.b * kRows + my_row < next.w.rows;
-      const bool second = on && next.w.k * 2 + 1 < (p.K >> 7);
-      const unsigned char* dy = p.dy.data + r * p.N + next.w.n * kTileN + chunk * 16;
-      const unsigned char* x = p.x.data + r * p.K + next.w.k * kTileK + chunk * 16;
+      const bool on = next.b * kRows + my_row < next.w.rows;
       const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) d.dy[j] = on ? ld_ahead(dy + j * 64) : zero;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d.x[j] = (j < 2 ? on : second) ? ld_ahead(x + j * 64) : zero;
-      d.y_scale = on ? ld_ahead_f32(p.dy.scale(r, next.w.n)) : 0.0f;
-      d.x_scale[0] = on ? ld_ahead_f32(p.x.scale(r, next.w.k * 2)) : 0.0f;
-      d.x_scale[1] = second ? ld_ahead_f32(p.x.scale(r, next.w.k * 2 + 1)) : 0.0f;
+      for (int j = 0; j < 4; ++j) d.x[j] = on && (j < 2 || second) ? ld_ahead(x + j * 64) : zero;
+      d.y_scale = on ? ld_ahead_f32(dy_scale) : 0.0f;
+      d.x_scale[0] = on ? ld_ahead_f32(x_scale) : 0.0f;
+      d.x_scale[1] = on && second ? ld_ahead_f32(x_scale + p.x.group_stride) : 0.0f;
     };
+    auto advance = [&]() {
+      if (next.b + kTeams < next.blocks) {
+        next.b += kTeams;
+        dy += kTeams * dy_step;
+        x += kTeams * x_step;
+        dy_scale += kTeams * dys_step;
+        x_scale += kTeams * xs_step;
+      } else {
+        for (int i = 0; i < kTeams; ++i) next.step();
+        if (next.on) aim();
+      }
+    };
+    if (next.on) aim();
     Fetched d;
     if (next.on) fetch(d);
     uint32_t tile = ~0u;  // whose exponents `down` holds
@@ -224,22 +250,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       }
       if (it >= kStages) ok = ok && wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err);
       if (!__all_sync(kFullMask, ok)) break;
-      unsigned char* dy_tile = stages + st * kStageBytes;
-      unsigned char* x_tile = dy_tile + kTileN / 64 * kChunkBytes;
+      const uint32_t lo = unit_lo + st * kStageBytes, hi = unit_hi + st * kStageBytes;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) store_chunk(dy_tile, my_row, chunk + 4 * j, d.dy[j], 0u, false);
+      for (int j = 0; j < 2; ++j) store_chunk(lo + j * kChunkBytes, hi + j * kChunkBytes, d.dy[j], 0u, false);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float sc = d.y_scale * d.x_scale[j >> 1] * down[j >> 1];
         uint32_t h;
         asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(sc));
-        store_chunk(x_tile, my_row, chunk + 4 * j, d.x[j], h, true);
+        store_chunk(lo + (2 + j) * kChunkBytes, hi + (2 + j) * kChunkBytes, d.x[j], h, true);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.full[st]);
-      next.step();
-      next.step();
+      advance();
       if (next.on) fetch(d);
       now = next;
     }
