@@ -37,6 +37,11 @@ bool groups_ok(const ep_groups_t* g) {
                        g->rows_per_group * g->num_groups <= g->rows);
 }
 
+// Tiles of a product over `rows` rows are counted in 32 bits.
+bool tiles_ok(const ep_groups_t* g, int N) {
+  return (g->rows / 128 + g->num_groups) * ((N + 127) / 128) < INT_MAX / 2;
+}
+
 ep::GroupArgs groups_of(const ep_groups_t* g) {
   return ep::GroupArgs{g->count, g->offset, g->num_groups, g->rows, g->offset ? 0 : g->rows_per_group, g->status};
 }
@@ -151,7 +156,8 @@ ep_status_t ep_gate_backward(const void* logits, ep_logits_t logits_type, int64_
 ep_status_t ep_grouped_matmul(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w, const float* w_scales,
                               int N, int K, void* out, int num_sms, ep_stream_t stream) {
   if (!groups_ok(groups) || N < 8 || N % 8 != 0 || K < 128 || K % 128 != 0) return EP_ERR_INVALID_ARG;
-  if (static_cast<long long>(groups->num_groups) * N > INT_MAX || !w || !w_scales || !aligned(w, 16) || !aligned(w_scales, 4))
+  if (static_cast<long long>(groups->num_groups) * N > INT_MAX || !tiles_ok(groups, N) || !w || !w_scales ||
+      !aligned(w, 16) || !aligned(w_scales, 4))
     return EP_ERR_INVALID_ARG;
   if (groups->rows == 0) return EP_OK;
   if (!rows_ok(x) || !out || !aligned(out, 16)) return EP_ERR_INVALID_ARG;
@@ -174,7 +180,7 @@ ep_status_t ep_grouped_matmul_swiglu(const ep_groups_t* groups, const ep_fp8_row
                                      const ep_fp8_rows_t* act, const ep_fp8_rows_t* pre, int num_sms,
                                      ep_stream_t stream) {
   if (!groups_ok(groups) || F < 128 || F % 128 != 0 || K < 128 || K % 128 != 0) return EP_ERR_INVALID_ARG;
-  if (static_cast<long long>(groups->num_groups) * F * 2 > INT_MAX || !w || !w_scales || !aligned(w, 16) ||
+  if (static_cast<long long>(groups->num_groups) * F * 2 > INT_MAX || !tiles_ok(groups, 2 * F) || !w || !w_scales || !aligned(w, 16) ||
       !aligned(w_scales, 4) || !aligned(row_weights, 4))
     return EP_ERR_INVALID_ARG;
   if (groups->rows == 0) return EP_OK;
@@ -221,7 +227,9 @@ ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* gr
 ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_t* grad_out, int N,
                                    const ep_fp8_rows_t* x, int K, void* grad_w, int num_sms, ep_stream_t stream) {
   if (!groups_ok(groups) || N < 128 || N % 128 != 0 || K < 128 || K % 128 != 0) return EP_ERR_INVALID_ARG;
-  if (!grad_w || !aligned(grad_w, 16)) return EP_ERR_INVALID_ARG;
+  if (static_cast<long long>(groups->num_groups) * (N / 128) * ((K + 255) / 256) > INT_MAX / 2 || !grad_w ||
+      !aligned(grad_w, 16))
+    return EP_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (groups->rows == 0)
     return status_of(cudaMemsetAsync(grad_w, 0, static_cast<size_t>(groups->num_groups) * N * K * 2, s), "weight gradient memset");

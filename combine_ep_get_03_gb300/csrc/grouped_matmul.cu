@@ -56,17 +56,17 @@ struct Tile {
   int rows;         // live rows of the tile
 };
 
-__device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* prefix, int tiles_n, long long t) {
+__device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* prefix, int tiles_n, unsigned t) {
   // tiles of a group are ordered column tile by column tile, row tiles inside
-  const int g = find_group(prefix, a.G, static_cast<unsigned>(t / tiles_n));
+  const int g = find_group(prefix, a.G, t / static_cast<unsigned>(tiles_n));
   Tile r;
   long long start;
   const int count = group_span(a, g, &start, false);
   const int tiles_m = (count + kTileM - 1) / kTileM;
-  const long long local = t - static_cast<long long>(prefix[g]) * tiles_n;
+  const unsigned local = t - prefix[g] * tiles_n;
   r.group = g;
-  r.n = tiles_m ? static_cast<int>(local / tiles_m) : 0;
-  const int m = tiles_m ? static_cast<int>(local % tiles_m) : 0;
+  r.n = tiles_m ? static_cast<int>(local / static_cast<unsigned>(tiles_m)) : 0;
+  const int m = static_cast<int>(local) - r.n * tiles_m;
   r.row = start + static_cast<long long>(m) * kTileM;
   r.rows = tiles_m ? min(kTileM, count - m * kTileM) : 0;
   return r;
@@ -107,14 +107,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int F = p.N >> 1;
   const int tiles_n = kSwiglu ? (F + kTileN / 2 - 1) / (kTileN / 2) : (p.N + kTileN - 1) / kTileN;
   const int blocks_k = p.K / kBlockK;
-  const long long tiles = static_cast<long long>(prefix[p.groups.G]) * tiles_n;
+  const unsigned tiles = prefix[p.groups.G] * tiles_n;
 
   if (warp >= kEpilogueWarps) {
     registers_down<kOtherRegisters>();
     if (warp == kEpilogueWarps) {
       uint32_t it = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           const int st = it % kStages;
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ac = warp - kEpilogueWarps - 1;  // the warp's accumulator: even or odd blocks of k
       constexpr uint32_t desc = mma_desc(kTileM, kTileN, false);
       const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
-      const long long mine = tiles > blockIdx.x ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-      const uint32_t all = static_cast<uint32_t>(mine * blocks_k);  // blocks of k of this block's tiles
+      const unsigned mine = tiles > blockIdx.x ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+      const uint32_t all = mine * blocks_k;  // blocks of k of this block's tiles
       uint32_t it = ac;
       for (; it < all; it += 2) {
         const int st = it % kStages;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     int turn = 0;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, turn ^= 1) {
+    for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x, turn ^= 1) {
       const Tile c = tile_at(p.groups, prefix, tiles_n, t);
       const long long row = c.row + in_tile;
       const bool live = in_tile < c.rows;

@@ -17,7 +17,7 @@ namespace ep {
 
 constexpr int kSwigluBackwardThreads = 256;
 
-__global__ void __launch_bounds__(kSwigluBackwardThreads) k_swiglu_backward(const SwigluBackwardArgs p) {
+__global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(const SwigluBackwardArgs p) {
   extern __shared__ unsigned prefix[];
   __shared__ unsigned sums[32];
   groups_prefix(p.groups, 1, prefix, sums);
@@ -58,10 +58,10 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads) k_swiglu_backward(cons
           const float d = (j & 1) ? bf16_hi(wd[j >> 1]) : bf16_lo(wd[j >> 1]);
           const float s = __fdividef(1.0f, 1.0f + __expf(-gate));
           const float silu = gate * s;
-          dw = fmaf(d * silu, up, dw);
-          const float t = d * w;
-          dg[j] = t * up * (s * fmaf(gate, 1.0f - s, 1.0f));
-          du[j] = t * silu;
+          du[j] = d * silu;
+          dw = fmaf(du[j], up, dw);
+          // s (1 + g (1 - s)) = s (1 + g - silu)
+          dg[j] = d * up * (s * (1.0f + gate - silu));
           ag = fmaxf(ag, fabsf(dg[j]));
           au = fmaxf(au, fabsf(du[j]));
         }
@@ -73,7 +73,10 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads) k_swiglu_backward(cons
       }
       if (on) {
         float ig, iu;
-        const float sg = group_scale(ag, &ig), su = group_scale(au, &iu);
+        // the row's weight multiplies the group's largest and the inverse scale
+        const float sg = group_scale(ag * fabsf(w), &ig), su = group_scale(au * fabsf(w), &iu);
+        ig *= w;
+        iu *= w;
         unsigned char* q = p.grad_pre.data + row * (2LL * F) + f;
         *reinterpret_cast<uint4*>(q) = make_uint4(quant4(dg, ig), quant4(dg + 4, ig), quant4(dg + 8, ig), quant4(dg + 12, ig));
         *reinterpret_cast<uint4*>(q + F) = make_uint4(quant4(du, iu), quant4(du + 4, iu), quant4(du + 8, iu), quant4(du + 12, iu));
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads) k_swiglu_backward(cons
 
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& p, int sms, cudaStream_t stream) {
   const long long need = (p.groups.rows + kSwigluBackwardThreads / 32 - 1) / (kSwigluBackwardThreads / 32);
-  const long long most = 2LL * sms;
+  const long long most = 3LL * sms;
   const unsigned blocks = static_cast<unsigned>(need < most ? (need > 0 ? need : 1) : most);
   return launch_kernel(k_swiglu_backward, dim3(blocks), dim3(kSwigluBackwardThreads),
                        sizeof(unsigned) * (p.groups.G + 1), stream, p);

@@ -51,14 +51,13 @@ struct Group {
 struct Walk {
   const Group* groups;
   int tiles_n, tiles_k;
-  long long t, tiles;
+  unsigned t, tiles;
   int group, n, k, rows;
   __device__ __forceinline__ void set() {
-    const long long per = static_cast<long long>(tiles_n) * tiles_k;
-    group = static_cast<int>(t / per);
-    const int local = static_cast<int>(t % per);
-    n = local / tiles_k;
-    k = local % tiles_k;
+    const unsigned row = t / static_cast<unsigned>(tiles_k);
+    k = static_cast<int>(t - row * tiles_k);
+    group = static_cast<int>(row / static_cast<unsigned>(tiles_n));
+    n = static_cast<int>(row - group * tiles_n);
     rows = groups[group].rows;
   }
   __device__ __forceinline__ bool settle() {  // at t or after it
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
   w.groups = groups;
   w.tiles_n = p.N / kTileN;
   w.tiles_k = (p.K + kTileK - 1) / kTileK;
-  w.tiles = static_cast<long long>(p.groups.G) * w.tiles_n * w.tiles_k;
+  w.tiles = static_cast<unsigned>(p.groups.G) * w.tiles_n * w.tiles_k;
   w.t = blockIdx.x;
 
   if (warp < kLoadWarps) {
