@@ -17,6 +17,59 @@ namespace ep {
 
 constexpr int kSwigluBackwardThreads = 256;
 
+namespace {
+
+// Two fp32 operations an instruction: the kernel is bound by issue before
+// memory, 39 instructions a channel without them and 22 with.
+__device__ __forceinline__ uint64_t bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(r);
+}
+// 2^x and 1/x to about one part in 2^22
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Sixteen products x * inv as e4m3 codes.
+__device__ __forceinline__ uint4 quant16(const float2* x, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = mul2(x[2 * j], make_float2(inv, inv)), b = mul2(x[2 * j + 1], make_float2(inv, inv));
+    w[j] = pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+
 __global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(const SwigluBackwardArgs p) {
   extern __shared__ unsigned prefix[];
   __shared__ unsigned sums[32];
@@ -33,11 +86,11 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(c
     if (slot >= static_cast<unsigned>(n)) continue;
     const long long row = start + slot;
     const float w = p.row_weights ? p.row_weights[row] : 1.0f;
-    float dw = 0.0f;
+    float2 dw = make_float2(0.0f, 0.0f);
     for (int f0 = 0; f0 < F; f0 += 512) {
       const int f = f0 + lane * 16;
       const bool on = f < F;  // whole groups of eight lanes
-      float dg[16], du[16];
+      float2 dg[8], du[8];
       float ag = 0.0f, au = 0.0f;
       if (on) {
         const unsigned char* pg = p.pre.data + row * (2LL * F) + f;
@@ -47,23 +100,28 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(c
         const float sg = *p.pre.scale(row, f >> 7), su = *p.pre.scale(row, Gf + (f >> 7));
         const uint32_t wg[4] = {qg.x, qg.y, qg.z, qg.w}, wu[4] = {qu.x, qu.y, qu.z, qu.w};
         const uint32_t wd[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        constexpr float kLog2e = 1.44269504088896341f;
+        const float2 sg2 = make_float2(sg, sg), su2 = make_float2(su, su);
+        const float2 arg2 = make_float2(-sg * kLog2e, -sg * kLog2e);
+        const float2 one = make_float2(1.0f, 1.0f), minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          e4m3x4_to_f32(wg[j], dg + 4 * j);
-          e4m3x4_to_f32(wu[j], du + 4 * j);
+          e4m3x4_to_f32(wg[j], &dg[2 * j].x);
+          e4m3x4_to_f32(wu[j], &du[2 * j].x);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float gate = dg[j] * sg, up = du[j] * su;
-          const float d = (j & 1) ? bf16_hi(wd[j >> 1]) : bf16_lo(wd[j >> 1]);
-          const float s = __fdividef(1.0f, 1.0f + __expf(-gate));
-          const float silu = gate * s;
-          du[j] = d * silu;
-          dw = fmaf(du[j], up, dw);
+        for (int j = 0; j < 8; ++j) {
+          const float2 gate = mul2(dg[j], sg2), up = mul2(du[j], su2), t = mul2(dg[j], arg2);
+          const float2 d = make_float2(bf16_lo(wd[j]), bf16_hi(wd[j]));
+          const float2 e = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), one);
+          const float2 s = make_float2(rcp_fast(e.x), rcp_fast(e.y));
+          const float2 silu = mul2(gate, s);
+          du[j] = mul2(d, silu);
+          dw = fma2(du[j], up, dw);
           // s (1 + g (1 - s)) = s (1 + g - silu)
-          dg[j] = d * up * (s * (1.0f + gate - silu));
-          ag = fmaxf(ag, fabsf(dg[j]));
-          au = fmaxf(au, fabsf(du[j]));
+          dg[j] = mul2(mul2(d, mul2(up, s)), fma2(silu, minus, add2(gate, one)));
+          ag = fmaxf(ag, fmaxf(fabsf(dg[j].x), fabsf(dg[j].y)));
+          au = fmaxf(au, fmaxf(fabsf(du[j].x), fabsf(du[j].y)));
         }
       }
 #pragma unroll
@@ -78,8 +136,8 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(c
         ig *= w;
         iu *= w;
         unsigned char* q = p.grad_pre.data + row * (2LL * F) + f;
-        *reinterpret_cast<uint4*>(q) = make_uint4(quant4(dg, ig), quant4(dg + 4, ig), quant4(dg + 8, ig), quant4(dg + 12, ig));
-        *reinterpret_cast<uint4*>(q + F) = make_uint4(quant4(du, iu), quant4(du + 4, iu), quant4(du + 8, iu), quant4(du + 12, iu));
+        *reinterpret_cast<uint4*>(q) = quant16(dg, ig);
+        *reinterpret_cast<uint4*>(q + F) = quant16(du, iu);
         if ((lane & 7) == 0) {
           *p.grad_pre.scale(row, f >> 7) = sg;
           *p.grad_pre.scale(row, Gf + (f >> 7)) = su;
@@ -87,9 +145,10 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads, 3) k_swiglu_backward(c
       }
     }
     if (p.grad_row_weights) {
+      dw.x += dw.y;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) dw += __shfl_xor_sync(kFullMask, dw, d);
-      if (lane == 0) p.grad_row_weights[row] = dw;
+      for (int d = 16; d; d >>= 1) dw.x += __shfl_xor_sync(kFullMask, dw.x, d);
+      if (lane == 0) p.grad_row_weights[row] = dw.x;
     }
   }
 }
