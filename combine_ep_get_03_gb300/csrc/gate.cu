@@ -37,11 +37,12 @@ __device__ __forceinline__ unsigned long long* work_sums(unsigned* w) {
 }
 __device__ __forceinline__ int* work_counts(unsigned* w, int E) { return reinterpret_cast<int*>(w + 4 + 2 * E); }
 
-// Order-preserving image of a float; 0 for what is never chosen.
+// Order-preserving image of a float, equal for -0 and +0.  -inf, and NaN in its
+// place, have the image kNever; what is not above it is never chosen.
+constexpr unsigned kNever = 0x007fffffu;
 __device__ __forceinline__ unsigned order_key(float v) {
-  if (!(v > -CUDART_INF_F)) return 0u;
-  const unsigned b = __float_as_uint(v + 0.0f);  // -0 and +0 tie
-  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+  const unsigned b = __float_as_uint(fmaxf(v + 0.0f, -CUDART_INF_F));
+  return b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 
 template <typename T>
@@ -89,19 +90,40 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// Unnormalised score of a logit: exp(v - m) for softmax with m the largest
-// logit; for sigmoid exp(min(v,0) - m) / (1 + exp(-|v|)) with m the largest
+// e^(x - m) to about two parts in 10^7 near x = m; base = m log2(e), whose
+// rounding is common to a row and cancels when the row is normalised.
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp_from(float x, float base) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(x, kLog2e, -base)));
+  return r;
+}
+
+// Unnormalised score of a logit: e^(v - m) for softmax with m the largest
+// logit; for sigmoid e^(min(v,0) - m) / (1 + e^-|v|) with m the largest
 // min(v,0), which stays away from 0/0 when every sigmoid underflows.
-__device__ __forceinline__ float score_of(float v, float m, int sigmoid) {
-  if (!sigmoid) return expf(v - m);
-  return __fdividef(expf(fminf(v, 0.0f) - m), 1.0f + expf(-fabsf(v)));
-}
-__device__ __forceinline__ float score_base(float vmax, int sigmoid) {
-  const float m = sigmoid ? fminf(vmax, 0.0f) : vmax;
-  return m == -CUDART_INF_F ? 0.0f : m;
-}
-// 1 for softmax, 1 - sigmoid(v) for sigmoid
-__device__ __forceinline__ float slope_of(float v, int sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + expf(v)) : 1.0f; }
+struct Scorer {
+  int sigmoid;
+  float m, base;
+  __device__ __forceinline__ Scorer(float vmax, int sig) : sigmoid(sig) {
+    m = sig ? fminf(vmax, 0.0f) : vmax;
+    if (m == -CUDART_INF_F) m = 0.0f;
+    base = m * kLog2e;
+  }
+  // *slope: d log(score) / dv -- 1 for softmax, 1 - sigmoid(v) for sigmoid
+  __device__ __forceinline__ float operator()(float v, float* slope = nullptr) const {
+    if (!sigmoid) {
+      if (slope) *slope = 1.0f;
+      return exp_from(v, base);
+    }
+    const float e = exp_from(-fabsf(v), 0.0f);
+    const float r = __fdividef(1.0f, 1.0f + e);
+    if (slope) *slope = (v >= 0.0f ? e : 1.0f) * r;
+    if (v != v) return v;
+    // with m = 0 the numerator is at hand
+    return (m == 0.0f ? (v >= 0.0f ? 1.0f : e) : exp_from(fminf(v, 0.0f), base)) * r;
+  }
+};
 
 // The lane's values sorted out of the keys c[] (order keys whose low bits are
 // replaced by the inverted index, 0 = never chosen): the largest of the warp.
@@ -111,6 +133,25 @@ __device__ __forceinline__ unsigned local_max(const unsigned* c) {
 #pragma unroll
   for (int j = 1; j < VPL; ++j) m = max(m, c[j]);
   return m;
+}
+
+// A lane's keys in descending order (Batcher's merge exchange network), so
+// that dropping the largest is a shift.
+template <int VPL>
+__device__ __forceinline__ void sort_down(unsigned* c) {
+#pragma unroll
+  for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < VPL; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < VPL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const unsigned a = c[i + j], b = c[i + j + k];
+            c[i + j] = max(a, b);
+            c[i + j + k] = min(a, b);
+          }
 }
 
 template <typename T, int VPL>
@@ -149,12 +190,12 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       float m = v[0];
 #pragma unroll
       for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
-      m = score_base(warp_max(m), p.sigmoid);
       {
+        const Scorer score(warp_max(m), p.sigmoid);
         float x[VPL], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          x[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+          x[j] = score(v[j]);  // 0 past E, where v is -inf
           sum += x[j];
         }
         sum = warp_sum(sum);
@@ -226,17 +267,28 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         const unsigned key = order_key(v[j]);
-        c[j] = key && usable(j) ? (key & ~kIndex) | (kIndex - (lane * VPL + j)) : 0u;
+        c[j] = usable(j) ? (key & ~kIndex) | (kIndex - (lane * VPL + j)) : 0u;
       }
-      unsigned best = local_max<VPL>(c), my_key = 0u;
+      constexpr bool kSorted = VPL <= 16;  // more keys cost more to sort than to search again
+      if (kSorted) sort_down<VPL>(c);
+      unsigned best = kSorted ? c[0] : local_max<VPL>(c), my_key = 0u;
       constexpr int kMore = sizeof(T) == 4 ? 1 : 0;
       for (int i = 0; i < k + kMore && i < 32; ++i) {
         const unsigned top = __reduce_max_sync(kFullMask, best);
-        if (top == 0u) break;
+        if (top <= kNever) break;
         if (lane == i) my_key = top;
+        if (kSorted) {
+          if (best == top) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
-        best = local_max<VPL>(c);
+            for (int j = 0; j + 1 < VPL; ++j) c[j] = c[j + 1];
+            c[VPL - 1] = 0u;
+          }
+          best = c[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
+          best = local_max<VPL>(c);
+        }
       }
       bool again = false;
       if (kMore) {
@@ -251,7 +303,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
         for (int i = 0; i < k; ++i) {
           best = local_max<VPL>(c);
           const unsigned top = __reduce_max_sync(kFullMask, best);
-          if (top == 0u) break;
+          if (top <= kNever) break;
           const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
           int at = 0;
 #pragma unroll
@@ -267,7 +319,8 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       // weights of the chosen: their logits once more, from the cache
       const float my_v = my_id >= 0 ? load_logit(static_cast<const T*>(p.logits) + t * p.ld + my_id) : -CUDART_INF_F;
       const float top_v = __shfl_sync(kFullMask, my_v, 0);
-      const float s = my_id >= 0 ? score_of(my_v, score_base(top_v, p.sigmoid), p.sigmoid) : 0.0f;
+      const Scorer score(top_v, p.sigmoid);
+      const float s = my_id >= 0 ? score(my_v) : 0.0f;
       const float s_all = warp_sum(s);
       my_w = my_id >= 0 ? s / s_all : 0.0f;
       if (my_id >= 0) atomicAdd(&s_count[my_id], 1);
@@ -291,33 +344,38 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   }
   unsigned long long* sums = work_sums(p.work);
   int* counts = work_counts(p.work, E);
-  for (int e = tid; e < E; e += blockDim.x) {
-    if (s_sum[e] > 0.0f) atomicAdd(&sums[e], static_cast<unsigned long long>(__double2ull_rn(static_cast<double>(s_sum[e]) * kFixed)));
-    if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
+  const bool alone = gridDim.x == 1;  // the block's sums are everybody's
+  if (!alone) {
+    for (int e = tid; e < E; e += blockDim.x) {
+      if (s_sum[e] > 0.0f) atomicAdd(&sums[e], __double2ull_rn(static_cast<double>(s_sum[e]) * kFixed));
+      if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
+    }
+    if (tid == 0) {
+      if (s_live) atomicAdd(&p.work[2], static_cast<unsigned>(s_live));
+      if (s_bad) atomicOr(&p.work[1], 1u);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(&p.work[0], 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
   }
-  if (tid == 0) {
-    if (s_live) atomicAdd(&p.work[2], static_cast<unsigned>(s_live));
-    if (s_bad) atomicOr(&p.work[1], 1u);
-  }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) s_last = atomicAdd(&p.work[0], 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!s_last) return;
   // every block's sums are in: results, and the work space back to zero
-  __threadfence();
-  const int tokens = static_cast<int>(__ldcg(&p.work[2]));
-  const bool any_bad = __ldcg(&p.work[1]) != 0u;
+  const int tokens = alone ? s_live : static_cast<int>(__ldcg(&p.work[2]));
+  const bool any_bad = alone ? s_bad != 0 : __ldcg(&p.work[1]) != 0u;
   float part = 0.0f;
   for (int e = tid; e < E; e += blockDim.x) {
-    const int n = __ldcg(&counts[e]);
-    float pe = tokens ? static_cast<float>(static_cast<double>(__ldcg(&sums[e])) * (1.0 / kFixed) / tokens) : 0.0f;
-    if (any_bad) pe = CUDART_NAN_F;
+    const int n = alone ? s_count[e] : __ldcg(&counts[e]);
+    const double sum = alone ? static_cast<double>(s_sum[e]) : static_cast<double>(__ldcg(&sums[e])) * (1.0 / kFixed);
+    const float pe = any_bad ? CUDART_NAN_F : tokens ? static_cast<float>(sum / tokens) : 0.0f;
     p.count[e] = n;
     p.prob[e] = pe;
     part = fmaf(static_cast<float>(n), pe, part);
-    sums[e] = 0ull;
-    counts[e] = 0;
+    if (!alone) {
+      sums[e] = 0ull;
+      counts[e] = 0;
+    }
   }
   part = warp_sum(part);
   if (lane == 0) s_part[warp] = part;
@@ -327,9 +385,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
     for (int w = 0; w < kWarps; ++w) sum += s_part[w];
     p.count[E] = tokens;
     *p.loss = tokens ? p.coef * E / (static_cast<float>(k) * tokens) * sum : 0.0f;
-    p.work[0] = 0u;
-    p.work[1] = 0u;
-    p.work[2] = 0u;
+    if (!alone) p.work[0] = p.work[1] = p.work[2] = 0u;
   }
 }
 
@@ -393,12 +449,14 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
           id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
           if (id >= 0) v = load_logit(row + id);
         }
-        const float m = score_base(warp_max(v), p.sigmoid);
-        const float s = id >= 0 ? score_of(v, m, p.sigmoid) : 0.0f;
+        const Scorer score(warp_max(v), p.sigmoid);
+        float slope;
+        const float x = score(v, &slope);
+        const float s = id >= 0 ? x : 0.0f;
         const float all = warp_sum(s);
         const float w = id >= 0 ? s / all : 0.0f;
         const float mean_dw = warp_sum(id >= 0 ? w * dw : 0.0f);
-        if (id >= 0) atomicAdd(chosen + id, w * slope_of(v, p.sigmoid) * (dw - mean_dw));
+        if (id >= 0) atomicAdd(chosen + id, w * slope * (dw - mean_dw));
       }
       if (balance) {
         float v[VPL];
@@ -406,11 +464,13 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
         float m = v[0];
 #pragma unroll
         for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
-        m = score_base(warp_max(m), p.sigmoid);
+        const Scorer score(warp_max(m), p.sigmoid);
         float sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          d[j] = lane * VPL + j < E ? score_of(v[j], m, p.sigmoid) : 0.0f;
+          float slope;
+          d[j] = score(v[j], &slope);  // 0 past E, where v is -inf
+          v[j] = slope;
           sum += d[j];
           dot = fmaf(d[j], c[j], dot);
         }
@@ -420,7 +480,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
         dot *= inv;
         const float scale = coef * inv;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) d[j] = scale * d[j] * slope_of(v[j], p.sigmoid) * (c[j] - dot);
+        for (int j = 0; j < VPL; ++j) d[j] = scale * d[j] * v[j] * (c[j] - dot);
       }
       if (p.grad_weights) {
         __syncwarp();
