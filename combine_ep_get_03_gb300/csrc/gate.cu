@@ -28,7 +28,7 @@ namespace ep {
 // Warps of a block: as many as leave room for a row of floats each.
 __host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 2; }
 __host__ __device__ constexpr int index_bits(int vpl) { return vpl == 1 ? 5 : 1 + index_bits(vpl / 2); }
-constexpr double kFixed = 68719476736.0;  // 2^36
+constexpr float kFixed = 68719476736.0f;  // 2^36
 
 // work: [0] finished blocks, [1] set if a row had no finite sum, [2] unmasked
 // tokens, [3] unused, then E u64 sums, then E counts
@@ -82,6 +82,19 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kFullMask, x, d);
+  return x;
+}
+// s / all, exactly 1 where s is all there is (its gradient is then exactly 0).
+__device__ __forceinline__ float share_of(float s, float all) { return s == all ? 1.0f : __fdividef(s, all); }
+
+// Sum and largest over the first k lanes, for the lanes below the next power
+// of two; lanes from k on hold 0 and -inf.
+__device__ __forceinline__ float sum_first(float x, int k) {
+  for (int d = 1; d < k; d <<= 1) x += __shfl_xor_sync(kFullMask, x, d);
+  return x;
+}
+__device__ __forceinline__ float max_first(float x, int k) {
+  for (int d = 1; d < k; d <<= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, d));
   return x;
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -200,12 +213,11 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
         }
         sum = warp_sum(sum);
         bad |= !(sum < CUDART_INF_F);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // a row of -inf has no probability
+        const float inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;  // a row of -inf has no probability
 #pragma unroll
         for (int j = 0; j < VPL; ++j) acc[j] = fmaf(x[j], inv, acc[j]);
       }
-      bool allowed = true;  // the lane's experts, where groups are whole lanes
-      unsigned long long kept = ~0ull;
+      // experts of groups that are not kept drop out of the choice
       if (p.groups > 1) {
         if (span) {
           unsigned key = 0u;
@@ -214,13 +226,16 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
           for (int d = 1; d < span; d <<= 1) key = max(key, __shfl_xor_sync(kFullMask, key, d));
           // 0: taken, past the last expert, or not the group's first lane
           unsigned mine = (lane & (span - 1)) == 0 && lane * VPL < E ? max(key, 1u) : 0u;
-          allowed = false;
+          bool allowed = false;  // groups are whole lanes
           for (int i = 0; i < p.keep; ++i) {
             const unsigned top = __reduce_max_sync(kFullMask, mine);
             const int src = __ffs(__ballot_sync(kFullMask, mine == top)) - 1;
             if (lane == src) mine = 0u;
             if ((lane & ~(span - 1)) == src) allowed = true;
           }
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (!allowed) v[j] = -CUDART_INF_F;
         } else {
           for (int g = lane; g < p.groups; g += 32) s_group[g] = 0u;
           __syncwarp();
@@ -240,7 +255,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
           if (lane * VPL < E) atomicMax(&s_group[g], best);
           __syncwarp();
           // lane l ranks groups 2l and 2l + 1; 0: taken or absent
-          kept = 0ull;
+          unsigned long long kept = 0ull;
           unsigned g0 = 2 * lane < p.groups ? max(s_group[2 * lane], 1u) : 0u;
           unsigned g1 = 2 * lane + 1 < p.groups ? max(s_group[2 * lane + 1], 1u) : 0u;
           for (int i = 0; i < p.keep; ++i) {
@@ -253,11 +268,11 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
             }
           }
           __syncwarp();
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (!((kept >> (min(lane * VPL + j, E - 1) / gs)) & 1ull)) v[j] = -CUDART_INF_F;
         }
       }
-      auto usable = [&](int j) {
-        return allowed && (span || p.groups == 1 || ((kept >> min((lane * VPL + j) / gs, 63)) & 1ull));
-      };
       // The k largest, one after another.  A key's low bits give way to the
       // inverted index, so one warp maximum names the expert and the owner
       // drops it by comparing.  bf16 keys lose nothing; of fp32 keys 32 - kBits
@@ -266,8 +281,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       unsigned c[VPL];
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const unsigned key = order_key(v[j]);
-        c[j] = usable(j) ? (key & ~kIndex) | (kIndex - (lane * VPL + j)) : 0u;
+        c[j] = (order_key(v[j]) & ~kIndex) | (kIndex - (lane * VPL + j));
       }
       constexpr bool kSorted = VPL <= 16;  // more keys cost more to sort than to search again
       if (kSorted) sort_down<VPL>(c);
@@ -278,11 +292,10 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
         if (top <= kNever) break;
         if (lane == i) my_key = top;
         if (kSorted) {
-          if (best == top) {
+          const bool mine = best == top;
 #pragma unroll
-            for (int j = 0; j + 1 < VPL; ++j) c[j] = c[j + 1];
-            c[VPL - 1] = 0u;
-          }
+          for (int j = 0; j + 1 < VPL; ++j) c[j] = mine ? c[j + 1] : c[j];
+          c[VPL - 1] = mine ? 0u : c[VPL - 1];
           best = c[0];
         } else {
 #pragma unroll
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
         if (lane < k && my_key) my_id = static_cast<int>(kIndex - (my_key & kIndex));
       } else {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) c[j] = usable(j) ? order_key(v[j]) : 0u;
+        for (int j = 0; j < VPL; ++j) c[j] = order_key(v[j]);
         for (int i = 0; i < k; ++i) {
           best = local_max<VPL>(c);
           const unsigned top = __reduce_max_sync(kFullMask, best);
@@ -321,8 +334,8 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       const float top_v = __shfl_sync(kFullMask, my_v, 0);
       const Scorer score(top_v, p.sigmoid);
       const float s = my_id >= 0 ? score(my_v) : 0.0f;
-      const float s_all = warp_sum(s);
-      my_w = my_id >= 0 ? s / s_all : 0.0f;
+      const float s_all = sum_first(s, k);
+      my_w = my_id >= 0 ? share_of(s, s_all) : 0.0f;
       if (my_id >= 0) atomicAdd(&s_count[my_id], 1);
     }
     if (lane < k) {
@@ -332,7 +345,8 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
     }
   }
   // the block's sums, warp after warp so that their order is fixed
-  for (int w = 0; w < kWarps; ++w) {
+  const int busy = min(kWarps, p.T - static_cast<int>(blockIdx.x) * kWarps);  // warps that had a token
+  for (int w = 0; w < busy; ++w) {
     if (w == warp) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
@@ -347,7 +361,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   const bool alone = gridDim.x == 1;  // the block's sums are everybody's
   if (!alone) {
     for (int e = tid; e < E; e += blockDim.x) {
-      if (s_sum[e] > 0.0f) atomicAdd(&sums[e], __double2ull_rn(static_cast<double>(s_sum[e]) * kFixed));
+      if (s_sum[e] > 0.0f) atomicAdd(&sums[e], __float2ull_rn(s_sum[e] * kFixed));
       if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
     }
     if (tid == 0) {
@@ -367,8 +381,8 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   float part = 0.0f;
   for (int e = tid; e < E; e += blockDim.x) {
     const int n = alone ? s_count[e] : __ldcg(&counts[e]);
-    const double sum = alone ? static_cast<double>(s_sum[e]) : static_cast<double>(__ldcg(&sums[e])) * (1.0 / kFixed);
-    const float pe = any_bad ? CUDART_NAN_F : tokens ? static_cast<float>(sum / tokens) : 0.0f;
+    const float sum = alone ? s_sum[e] : __ull2float_rn(__ldcg(&sums[e])) * (1.0f / kFixed);
+    const float pe = any_bad ? CUDART_NAN_F : tokens ? sum / tokens : 0.0f;
     p.count[e] = n;
     p.prob[e] = pe;
     part = fmaf(static_cast<float>(n), pe, part);
@@ -439,28 +453,28 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
     for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
     if (!p.mask || p.mask[t]) {
       const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+      float v[VPL];
+      if (balance) load_row<T, VPL>(row, E, lane, p.vec, v);
       int id = -1;
       if (p.grad_weights) {
-        float dw = 0.0f, v = -CUDART_INF_F;
+        float dw = 0.0f, x = -CUDART_INF_F;
         if (lane < k) {
           const long long o = static_cast<long long>(t) * k + lane;
           const long long wide = load_topk_id(p.idx, o, p.ids32);
           dw = p.grad_weights[o];
           id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
-          if (id >= 0) v = load_logit(row + id);
+          if (id >= 0) x = load_logit(row + id);
         }
-        const Scorer score(warp_max(v), p.sigmoid);
+        const Scorer score(max_first(x, k), p.sigmoid);
         float slope;
-        const float x = score(v, &slope);
+        x = score(x, &slope);
         const float s = id >= 0 ? x : 0.0f;
-        const float all = warp_sum(s);
-        const float w = id >= 0 ? s / all : 0.0f;
-        const float mean_dw = warp_sum(id >= 0 ? w * dw : 0.0f);
+        const float all = sum_first(s, k);
+        const float w = id >= 0 ? share_of(s, all) : 0.0f;
+        const float mean_dw = sum_first(id >= 0 ? w * dw : 0.0f, k);
         if (id >= 0) atomicAdd(chosen + id, w * slope * (dw - mean_dw));
       }
       if (balance) {
-        float v[VPL];
-        load_row<T, VPL>(row, E, lane, p.vec, v);
         float m = v[0];
 #pragma unroll
         for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
         }
         sum = warp_sum(sum);
         dot = warp_sum(dot);
-        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : CUDART_NAN_F);
+        const float inv = sum > 0.0f ? __fdividef(1.0f, sum) : (sum == 0.0f ? 0.0f : CUDART_NAN_F);
         dot *= inv;
         const float scale = coef * inv;
 #pragma unroll
@@ -500,7 +514,7 @@ namespace {
 template <typename T, int VPL>
 cudaError_t launch_vpl(const GateArgs& p, bool backward, int sms, cudaStream_t s) {
   constexpr int kWarps = gate_warps(VPL);
-  const int need = (p.T + kWarps - 1) / kWarps, most = sms * (32 / kWarps);
+  const int need = (p.T + kWarps - 1) / kWarps, most = sms * ((backward ? 48 : 32) / kWarps);
   const dim3 grid(need < 1 ? 1 : need < most ? need : most), block(kWarps * 32);
   const size_t smem = sizeof(float) * (backward ? kWarps * 32 * VPL : 2 * p.E + (p.groups > 1 ? kWarps * p.groups : 0));
   return backward ? launch_kernel(k_gate_backward<T, VPL>, grid, block, smem, s, p)
