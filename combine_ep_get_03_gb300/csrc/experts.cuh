@@ -108,15 +108,24 @@ __device__ __forceinline__ int find_group(const unsigned* prefix, int G, unsigne
 // Bounded wait on an mbarrier phase for kernels whose warps wait on one
 // another: one that gives up latches EP_ERR_TIMEOUT and raises `quit`, which
 // ends every other warp's wait too.
+// `kCluster`: the barrier's arrivals may come from the cluster's other block.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, volatile int* quit, int* err) {
   const uint32_t addr = smem_u32(bar);
   for (int it = 0; it < kSpinLimit; ++it) {
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
+    if (kCluster)
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(done)
+          : "r"(addr), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(done)
+          : "r"(addr), "r"(parity)
+          : "memory");
     if (done) return true;
     if (it >= 64) {
       if (*quit) return false;
@@ -165,6 +174,24 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
 }
 
 // ------------------------------------------------------------------ launches
+
+// Kernel launch in clusters of two blocks.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute pair[1];
+  pair[0].id = cudaLaunchAttributeClusterDimension;
+  pair[0].val.clusterDim.x = 2;
+  pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
+  cfg.attrs = pair;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // Once per kernel and device: the whole shared memory for dynamic use, and the
 // register count that a kernel moving registers between warps relies on.

@@ -328,7 +328,6 @@ EncodeTiled encode_tiled() {
 
 }  // namespace
 
-// A tensor map over e4m3 bytes [planes][rows][width], box 128 x box_rows.
 cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows) {
   EncodeTiled enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;

@@ -26,8 +26,75 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// A 4-byte asynchronous copy, 0 instead where `on` is false (src is not read),
+// and an arrival on `bar` (counted in its expected arrivals) when this
+// thread's copies so far have landed.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" : : "r"(smem_u32(bar)) : "memory");
+}
+
+// A tensor map over bytes [planes][rows][width] (2-D where planes is 0), box
+// 128 x box_rows, 128-byte swizzle.
+cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" : : "l"(map) : "memory");
+}
+
+// ------------------------------------------------------------------ pairs of blocks
+//
+// A cluster of two blocks on neighbouring SMs whose tensor cores work on one
+// tile of twice the rows.  Block 0 issues; each block holds its rows of A, half
+// of B and its rows of the accumulator.
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" : : : "memory");
+}
+// An arrival on block 0's barrier at the place of `bar`.  It says that this
+// block's tensor core may read what fence_proxy_async_smem ordered before it, or
+// may write TMEM that has been read; no thread of block 0 reads memory on its
+// account.  (With release at cluster scope each arrival waits some 1000 cycles
+// for all of the thread's writes.)
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n"
+      :
+      : "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* slot, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :
+               : "r"(smem_u32(slot)), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" : : "r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void pair_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      :
+      : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// An arrival on both blocks' barriers when every MMA that this thread issued
+// has finished.
+__device__ __forceinline__ void pair_mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :
+               : "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
+               : "memory");
 }
 
 // ------------------------------------------------------------------ TMEM

@@ -4,19 +4,24 @@
 //
 // The contraction runs over rows, and both scales change with the row, so they
 // cannot be taken out of the sum: the operands are widened to f16 on the way
-// to shared memory and multiplied by f16 tensor-core instructions with fp32
-// accumulation.  A 128-column tile of dy lies in one scale group, so dy enters
-// as its codes (exact in f16) and x carries the product of both scales,
-// divided by a power of two that brings the tile's largest below one and is
-// put back on the fp32 sums.  That costs x two roundings to 11 bits, an eighth
-// of the rounding of the bf16 result.
+// to shared memory, multiplied by their scales, and go through f16
+// tensor-core instructions with fp32 accumulation.  The scales of an operand's
+// 128 channels are first divided by the power of two that brings the largest
+// of the group's rows to [64, 128) (448 x 128 still fits f16), which is put
+// back on the sums; rows whose scale is 2^-21 of the largest or more keep 11
+// bits.  Two roundings to 11 bits are an eighth of the bf16 result's own.
 //
-// Tile 128 (n) x 256 (k), 64 rows a stage.  Two teams of eight warps take
-// every other stage: they fetch e4m3 rows a turn ahead (also across tiles),
-// widen and store them with the 128-byte swizzle, rows along the long axis (both operands "MN major", so nothing is
-// transposed); one warp issues four MMAs a stage; four more write the previous
-// tile from the other TMEM accumulator; one looks up the next tile's largest
-// scale.  Rows past the group's end enter as zeros.
+// Shared memory is what bounds it: a widened 64-row stage is written once and
+// read once per MMA.  So two blocks on neighbouring SMs share a tile of 256 (n)
+// x 256 (k): each widens its 128 columns of dy and of x, 32 KB a stage instead
+// of the 48 KB of a 128 x 256 tile of its own, for the same MMA time.  One warp
+// fetches e4m3 rows (TMA) and scales (asynchronous copies) four stages ahead,
+// across tiles; two teams of eight warps take every other stage, widen it and
+// store it with the 128-byte swizzle, rows along the long axis (both operands
+// "MN major", so nothing is transposed).  One warp of the first block issues
+// four MMAs a stage; four warps write the previous tile from the other TMEM
+// accumulator; one looks up the next tiles' largest scales.  Rows past the
+// group's end enter as zeros.
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "tcgen05.cuh"
@@ -25,54 +30,57 @@ namespace ep {
 
 namespace {
 
-constexpr int kTileN = 128, kTileK = 256, kRows = 64;
-constexpr int kStages = 4;
+constexpr int kPair = 256;     // the pair's tile: 256 x 256
+constexpr int kOwn = 128;      // a block's columns of dy, of x and rows of the accumulator
+constexpr int kRows = 64;
+constexpr int kStages = 4;     // widened; even, so that a stage belongs to one team
+constexpr int kRawStages = 4;  // as fetched
 constexpr int kChunkBytes = kRows * 128;  // 64 columns of f16
-constexpr int kStageBytes = (kTileN + kTileK) / 64 * kChunkBytes;
+constexpr int kStageBytes = 2 * kOwn / 64 * kChunkBytes;
+constexpr int kRawBytes = 2 * kOwn * kRows, kScaleBytes = 2 * 4 * kRows;  // dy, x; their scales
 constexpr int kTeams = 2, kTeamWarps = 8, kLoadWarps = kTeams * kTeamWarps, kStoreWarps = 4;
-constexpr int kMmaWarp = kLoadWarps + kStoreWarps, kScaleWarp = kMmaWarp + 1;
-constexpr int kThreads = (kScaleWarp + 1) * 32;
+constexpr int kMmaWarp = kLoadWarps + kStoreWarps, kScaleWarp = kMmaWarp + 1, kFetchWarp = kMmaWarp + 2;
+constexpr int kThreads = (kFetchWarp + 1) * 32;
 constexpr uint32_t kTmemColumns = 512;
-constexpr int kExponents = 4;  // tiles whose exponents are kept
+constexpr int kExponents = 8;  // tiles whose exponents are kept: at least stages + 2
 
 struct Shared {
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], exp_full[kExponents], exp_empty[kExponents];
   uint32_t tmem;
   int quit;
-  int exponent[kExponents][2];
+  int exponent[kExponents][3];  // of the block's dy, of both halves of x
 };
 
-// First row and row count of every group, in shared memory.
-struct Group {
-  int row, rows;
-};
-
-// The block's tiles that have rows, one after another.
+// The pair's tiles that have rows, one after another.
 struct Walk {
-  const Group* groups;
+  const GroupArgs* groups;
+  const int* counts;  // rows of every group, in shared memory
   int tiles_n, tiles_k;
-  unsigned t, tiles;
+  unsigned t, tiles, step;
   int group, n, k, rows;
   __device__ __forceinline__ void set() {
     const unsigned row = t / static_cast<unsigned>(tiles_k);
     k = static_cast<int>(t - row * tiles_k);
     group = static_cast<int>(row / static_cast<unsigned>(tiles_n));
     n = static_cast<int>(row - group * tiles_n);
-    rows = groups[group].rows;
+    rows = counts[group];
   }
   __device__ __forceinline__ bool settle() {  // at t or after it
-    for (; t < tiles; t += gridDim.x) {
+    for (; t < tiles; t += step) {
       set();
       if (rows) return true;
     }
     return false;
   }
   __device__ __forceinline__ bool next() {
-    t += gridDim.x;
+    t += step;
     return settle();
   }
   __device__ __forceinline__ int blocks() const { return (rows + kRows - 1) / kRows; }
-  __device__ __forceinline__ long long row() const { return groups[group].row; }
+  __device__ __forceinline__ long long row() const {
+    return groups->offset ? static_cast<long long>(groups->offset[group]) : group * groups->rows_per_group;
+  }
 };
 
 // A block of rows of a walk: block b of the used-th tile that has rows.
@@ -115,218 +123,224 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" : : "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 codes to f16, at the two shared-memory addresses of their 16-byte units.
-__device__ __forceinline__ void store_chunk(uint32_t lo, uint32_t hi, const uint4& q, uint32_t scale, bool scaled) {
-  uint32_t h[8];
+// 16 codes times their scale, as f16 at the two shared-memory addresses of
+// their 16-byte units.
+__device__ __forceinline__ void store_chunk(uint32_t lo, uint32_t hi, const uint4& q, float scale) {
+  uint32_t h[8], f;
+  asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(f) : "f"(scale));
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     e4m3x4_to_f16(w[i], &h[2 * i], &h[2 * i + 1]);
-    if (scaled) h[2 * i] = mul_f16x2(h[2 * i], scale), h[2 * i + 1] = mul_f16x2(h[2 * i + 1], scale);
+    h[2 * i] = mul_f16x2(h[2 * i], f);
+    h[2 * i + 1] = mul_f16x2(h[2 * i + 1], f);
   }
   sts128(lo, h[0], h[1], h[2], h[3]);
   sts128(hi, h[4], h[5], h[6], h[7]);
 }
 
-// A load that stays where it is written, far ahead of its use.
-__device__ __forceinline__ uint4 ld_ahead(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// 2^e that brings m to [64, 128); a largest scale of 0 or without a finite
+// value leaves the scales as they are.
+__device__ __forceinline__ int exponent_of(float m) {
+  const int e = m > 0.0f && m < 3.0e38f ? ilogbf(m) - 6 : 0;
+  return max(-60, min(60, e));
 }
-__device__ __forceinline__ float ld_ahead_f32(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
-
-// One thread's part of 64 rows: of one row, chunks c, c + 4 of dy and c, c + 4,
-// c + 8, c + 12 of x (c = thread mod 4), and the scales of both halves of x.
-struct Fetched {
-  uint4 dy[2], x[4];
-  float y_scale, x_scale[2];
-};
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) 
+    k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ WeightGradArgs p) {
   extern __shared__ unsigned char raw[];
   unsigned char* stages = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared& s = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  unsigned char* raws = stages + kStages * kStageBytes;
+  unsigned char* raw_scales = raws + kRawStages * kRawBytes;
+  Shared& s = *reinterpret_cast<Shared*>(raw_scales + kRawStages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* quit = &s.quit;
   int* err = p.groups.err;
-  Group* groups = reinterpret_cast<Group*>(&s + 1);
+  const int rank = static_cast<int>(cluster_rank());
+  int* counts = reinterpret_cast<int*>(&s + 1);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], kTeamWarps), mbar_init(&s.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kStoreWarps);
+    // the fetching thread's own arrival and one of every lane's copies
+    for (int i = 0; i < kRawStages; ++i) mbar_init(&s.raw_full[i], 1 + 32), mbar_init(&s.raw_empty[i], kTeamWarps);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 2 * kTeamWarps), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], 2 * kStoreWarps);
     for (int i = 0; i < kExponents; ++i) mbar_init(&s.exp_full[i], 1), mbar_init(&s.exp_empty[i], kStoreWarps);
     s.quit = 0;
     mbar_init_fence();
   }
-  if (warp == kMmaWarp) tmem_alloc(&s.tmem, kTmemColumns);
+  if (warp == kMmaWarp) pair_tmem_alloc(&s.tmem, kTmemColumns);
   for (int g = threadIdx.x; g < p.groups.G; g += kThreads) {
     long long start;
-    groups[g].rows = group_span(p.groups, g, &start, blockIdx.x == 0);
-    groups[g].row = static_cast<int>(start);
+    counts[g] = group_span(p.groups, g, &start, blockIdx.x == 0);
   }
   tmem_fence_before();
   __syncthreads();
+  cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
   Walk w;
-  w.groups = groups;
-  w.tiles_n = p.N / kTileN;
-  w.tiles_k = (p.K + kTileK - 1) / kTileK;
+  w.groups = &p.groups;
+  w.counts = counts;
+  w.tiles_n = (p.N + kPair - 1) / kPair;
+  w.tiles_k = (p.K + kPair - 1) / kPair;
   w.tiles = static_cast<unsigned>(p.groups.G) * w.tiles_n * w.tiles_k;
-  w.t = blockIdx.x;
+  w.t = blockIdx.x >> 1;
+  w.step = gridDim.x >> 1;
 
   if (warp < kLoadWarps) {
-    const int team = warp / kTeamWarps, tid = threadIdx.x % (kTeamWarps * 32);
-    const int my_row = tid >> 2, chunk = tid & 3;
-    // Row my_row, chunk c = chunk + 4 j of an operand lies in 64-channel block j
-    // at swizzled units 2 chunk and 2 chunk + 1.  A phase of a warp's 16-byte
-    // stores covers two rows, whose units are the even and the odd ones: no
-    // bank conflict.
-    const uint32_t line = smem_u32(stages) + my_row * 128;
-    const uint32_t unit_lo = line + (((2 * chunk) ^ (my_row & 7)) << 4);
-    const uint32_t unit_hi = line + (((2 * chunk + 1) ^ (my_row & 7)) << 4);
-    Cursor now, next;  // the team's block and the one it fetches
+    const int team = warp / kTeamWarps;
+    // A warp's 32 chunks of 16 channels are eight of each of four rows.  Eight
+    // lanes in a row hold four chunks of each of two rows r and r ^ 5.  Both
+    // tiles are swizzled by the row (chunk or 16-byte unit ^ row mod 8): the raw
+    // chunks of the two rows differ in bit 2, the widened units 2 (c mod 4) and
+    // the next in bit 0, so a phase of either 16-byte access meets all banks once.
+    const int pair = (warp % kTeamWarps) * 2 + (lane >> 4);
+    const int my_row = (pair >> 2) * 8 + ((pair & 3) ^ ((lane & 4) ? 5 : 0));
+    const int c4 = lane & 3, chunk = c4 + ((lane >> 3) & 1) * 4;
+    const uint32_t line = smem_u32(stages) + (chunk >> 2) * kChunkBytes + my_row * 128;
+    const uint32_t unit_lo = line + (((2 * c4) ^ (my_row & 7)) << 4);
+    const uint32_t unit_hi = line + (((2 * c4 + 1) ^ (my_row & 7)) << 4);
+    const unsigned char* my_raw = raws + my_row * kOwn + ((chunk ^ (my_row & 7)) << 4);
+    const float* my_scales = reinterpret_cast<const float*>(raw_scales) + my_row;
+    Cursor now;
     now.begin(w);
     if (team) now.step();
-    next = now;
-    // what the fetched tile's block 0 would read, and steps from block to block
-    const unsigned char *dy = nullptr, *x = nullptr;
-    const float *dy_scale = nullptr, *x_scale = nullptr;
-    const long long dy_step = static_cast<long long>(kRows) * p.N, x_step = static_cast<long long>(kRows) * p.K;
-    const long long dys_step = kRows * p.dy.row_stride, xs_step = kRows * p.x.row_stride;
-    bool second = false;
-    auto aim = [&]() {
-      const long long r = next.w.row() + my_row;
-      dy = p.dy.data + r * p.N + next.w.n * kTileN + chunk * 16 + next.b * dy_step;
-      x = p.x.data + r * p.K + next.w.k * kTileK + chunk * 16 + next.b * x_step;
-      dy_scale = p.dy.scale(r, next.w.n) + next.b * dys_step;
-      x_scale = p.x.scale(r, next.w.k * 2) + next.b * xs_step;
-      second = next.w.k * 2 + 1 < (p.K >> 7);
-    };
-    auto fetch = [&](Fetched& d) {
-      const bool on = next.b * kRows + my_row < next.w.rows;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) d.dy[j] = on ? ld_ahead(dy + j * 64) : zero;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d.x[j] = on && (j < 2 || second) ? ld_ahead(x + j * 64) : zero;
-      d.y_scale = on ? ld_ahead_f32(dy_scale) : 0.0f;
-      d.x_scale[0] = on ? ld_ahead_f32(x_scale) : 0.0f;
-      d.x_scale[1] = on && second ? ld_ahead_f32(x_scale + p.x.group_stride) : 0.0f;
-    };
-    auto advance = [&]() {
-      if (next.b + kTeams < next.blocks) {
-        next.b += kTeams;
-        dy += kTeams * dy_step;
-        x += kTeams * x_step;
-        dy_scale += kTeams * dys_step;
-        x_scale += kTeams * xs_step;
-      } else {
-        for (int i = 0; i < kTeams; ++i) next.step();
-        if (next.on) aim();
-      }
-    };
-    if (next.on) aim();
-    Fetched d;
-    if (next.on) fetch(d);
-    uint32_t tile = ~0u;  // whose exponents `down` holds
-    float down[2] = {1.0f, 1.0f};
+    uint32_t tile = ~0u;  // whose exponents `dy_down` and `x_down` hold
+    float dy_down = 1.0f, x_down = 1.0f;
     for (uint32_t it = team; now.on; it += kTeams) {
-      const int st = it % kStages;
+      const int st = it % kStages, rs = it % kRawStages;
       bool ok = true;
       if (now.used != tile) {
         tile = now.used;
         const int e = tile % kExponents;
         ok = wait_or_quit(&s.exp_full[e], (tile / kExponents) & 1, quit, err);
-        down[0] = power_of_two(-s.exponent[e][0]);
-        down[1] = power_of_two(-s.exponent[e][1]);
+        dy_down = power_of_two(-s.exponent[e][0]);
+        x_down = power_of_two(-s.exponent[e][1 + rank]);
       }
-      if (it >= kStages) ok = ok && wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err);
+      ok = ok && wait_or_quit(&s.raw_full[rs], (it / kRawStages) & 1, quit, err);
       if (!__all_sync(kFullMask, ok)) break;
+      uint4 q[4];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool on = now.b * kRows + my_row + 32 * j < now.w.rows;  // else another group's row
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        q[j] = on ? lds128(my_raw + rs * kRawBytes + j * 32 * kOwn) : zero;
+        q[2 + j] = on ? lds128(my_raw + rs * kRawBytes + kOwn * kRows + j * 32 * kOwn) : zero;
+        f[j] = my_scales[rs * (kScaleBytes / 4) + j * 32];
+        f[2 + j] = my_scales[rs * (kScaleBytes / 4) + kRows + j * 32];
+      }
+      if (it >= kStages &&
+          !__all_sync(kFullMask, wait_or_quit<true>(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err)))
+        break;
       const uint32_t lo = unit_lo + st * kStageBytes, hi = unit_hi + st * kStageBytes;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) store_chunk(lo + j * kChunkBytes, hi + j * kChunkBytes, d.dy[j], 0u, false);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float sc = d.y_scale * d.x_scale[j >> 1] * down[j >> 1];
-        uint32_t h;
-        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(sc));
-        store_chunk(lo + (2 + j) * kChunkBytes, hi + (2 + j) * kChunkBytes, d.x[j], h, true);
+      for (int j = 0; j < 2; ++j) {
+        store_chunk(lo + j * 32 * 128, hi + j * 32 * 128, q[j], f[j] * dy_down);
+        store_chunk(lo + 2 * kChunkBytes + j * 32 * 128, hi + 2 * kChunkBytes + j * 32 * 128, q[2 + j], f[2 + j] * x_down);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.full[st]);
-      advance();
-      if (next.on) fetch(d);
-      now = next;
+      if (lane == 0) {
+        mbar_arrive(&s.raw_empty[rs]);
+        mbar_arrive_first(&s.full[st]);
+      }
+      for (int i = 0; i < kTeams; ++i) now.step();
+    }
+  } else if (warp == kFetchWarp) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (bool on = w.settle(); ok && on; on = w.next()) {
+      const int blocks = w.blocks(), n = w.n * 2 + rank, k = w.k * 2 + rank;
+      const bool in_n = n < (p.N >> 7), in_k = k < (p.K >> 7);
+      const long long first = w.row();
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const int rs = it % kRawStages;
+        if (it >= kRawStages &&
+            !(ok = __all_sync(kFullMask, wait_or_quit(&s.raw_empty[rs], ((it / kRawStages) & 1) ^ 1, quit, err))))
+          break;
+        const long long r = first + b * kRows;
+        if (elect_one()) {
+          // columns past the matrix and rows past the buffer read as zeros
+          mbar_arrive_expect_tx(&s.raw_full[rs], kRawBytes);
+          tma_load_2d(raws + rs * kRawBytes, &map_dy, n * kOwn, static_cast<int>(r), &s.raw_full[rs]);
+          tma_load_2d(raws + rs * kRawBytes + kOwn * kRows, &map_x, k * kOwn, static_cast<int>(r), &s.raw_full[rs]);
+        }
+        __syncwarp();
+        const uint32_t dst = smem_u32(raw_scales + rs * kScaleBytes) + lane * 4;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool live = b * kRows + lane + 32 * j < w.rows;
+          copy_async4(dst + j * 128, live && in_n ? p.dy.scale(r + lane + 32 * j, n) : p.dy.scales, live && in_n);
+          copy_async4(dst + 4 * kRows + j * 128, live && in_k ? p.x.scale(r + lane + 32 * j, k) : p.x.scales, live && in_k);
+        }
+        copy_async_arrive(&s.raw_full[rs]);
+      }
+    }
+    // no copy may outlive the block: wait for the last fill of every stage
+    for (uint32_t i = it < kRawStages ? 0 : it - kRawStages; i < it; ++i) {
+      int none = 0;
+      wait_or_quit(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, &none, err);
     }
   } else if (warp == kScaleWarp) {
-    // the largest scale of each half of the tiles to come: 2^e above it
+    // the exponents of the tiles to come
     uint32_t used = 0;
     for (bool on = w.settle(); on; on = w.next(), ++used) {
       const int e = used % kExponents;
       if (used >= kExponents &&
           !__all_sync(kFullMask, wait_or_quit(&s.exp_empty[e], ((used / kExponents) & 1) ^ 1, quit, err)))
         break;
-      const bool second = w.k * 2 + 1 < (p.K >> 7);
-      const float* ys = p.dy.scale(w.row(), w.n);
-      const float* xs = p.x.scale(w.row(), w.k * 2);
-      float m[2] = {0.0f, 0.0f};
+      const int n = w.n * 2 + rank, k = w.k * 2;
+      const bool in_n = n < (p.N >> 7), second = k + 1 < (p.K >> 7);
+      const float* ys = p.dy.scale(w.row(), n);
+      const float* xs = p.x.scale(w.row(), k);
+      float m[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll 8
       for (int r = lane; r < w.rows; r += 32) {
-        const float y = ys[r * p.dy.row_stride];
-        m[0] = fmaxf(m[0], fabsf(y * xs[r * p.x.row_stride]));
-        if (second) m[1] = fmaxf(m[1], fabsf(y * xs[r * p.x.row_stride + p.x.group_stride]));
+        if (in_n) m[0] = fmaxf(m[0], fabsf(ys[r * p.dy.row_stride]));
+        m[1] = fmaxf(m[1], fabsf(xs[r * p.x.row_stride]));
+        if (second) m[2] = fmaxf(m[2], fabsf(xs[r * p.x.row_stride + p.x.group_stride]));
       }
 #pragma unroll
-      for (int d = 16; d; d >>= 1) {
-        m[0] = fmaxf(m[0], __shfl_xor_sync(kFullMask, m[0], d));
-        m[1] = fmaxf(m[1], __shfl_xor_sync(kFullMask, m[1], d));
-      }
+      for (int d = 16; d; d >>= 1)
+#pragma unroll
+        for (int h = 0; h < 3; ++h) m[h] = fmaxf(m[h], __shfl_xor_sync(kFullMask, m[h], d));
       if (lane == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // a scale without a finite largest is used as it is
-          const int x = m[h] > 0.0f && m[h] < 3.0e38f ? ilogbf(m[h]) + 1 : 0;
-          s.exponent[e][h] = max(-100, min(100, x));
-        }
+        for (int h = 0; h < 3; ++h) s.exponent[e][h] = exponent_of(m[h]);
         mbar_arrive(&s.exp_full[e]);
       }
       __syncwarp();
     }
   } else if (warp == kMmaWarp) {
-    constexpr uint32_t desc = mma_desc(kTileN, kTileK, true);
+    constexpr uint32_t desc = mma_desc(kPair, kPair, true);
     const uint64_t first = smem_desc(smem_u32(stages), kChunkBytes, 1024);
     uint32_t it = 0, used = 0;
     bool ok = true;
-    for (bool on = w.settle(); ok && on; on = w.next()) {
+    for (bool on = rank == 0 && w.settle(); ok && on; on = w.next()) {
       const int ac = used & 1, blocks = w.blocks();
-      ok = __all_sync(kFullMask, used < 2 || wait_or_quit(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err));
+      ok = __all_sync(kFullMask, used < 2 || wait_or_quit<true>(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err));
       if (!ok) break;
       for (int b = 0; b < blocks; ++b, ++it) {
         const int st = it % kStages;
-        ok = __all_sync(kFullMask, wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
+        ok = __all_sync(kFullMask, wait_or_quit<true>(&s.full[st], (it / kStages) & 1, quit, err));
         if (!ok) break;
         tmem_fence_after();
         if (elect_one()) {
           // descriptors count 16-byte units; an MMA takes 16 rows of 128 bytes
-          const uint64_t dy = first + st * (kStageBytes >> 4), x = dy + (kTileN / 64 * kChunkBytes >> 4);
+          const uint64_t dy = first + st * (kStageBytes >> 4), x = dy + (2 * kChunkBytes >> 4);
           const int steps = (min(kRows, w.rows - b * kRows) + 15) >> 4;
 #pragma unroll
           for (int j = 0; j < kRows / 16; ++j)
-            if (j < steps) mma_f16(tmem + ac * kTileK, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
-          mma_commit(&s.empty[st]);
+            if (j < steps) pair_mma_f16(tmem + ac * kPair, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
+          pair_mma_commit(&s.empty[st]);
         }
         __syncwarp();
       }
       // also after a wait that gave up: what was issued ends before TMEM goes back
-      if (elect_one()) mma_commit(&s.acc_full[ac]);
+      if (elect_one()) pair_mma_commit(&s.acc_full[ac]);
       __syncwarp();
       ++used;
     }
@@ -339,10 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const bool wide = (reinterpret_cast<uintptr_t>(p.dw) & 31) == 0;
     uint32_t used = 0;
-    for (; w.t < w.tiles; w.t += gridDim.x) {
+    for (; w.t < w.tiles; w.t += w.step) {
       w.set();
-      uint16_t* o = p.dw + (static_cast<long long>(w.group) * p.N + w.n * kTileN + quarter * 32 + lane) * p.K + w.k * kTileK;
-      const int columns = min(kTileK, p.K - w.k * kTileK);
+      const int n = w.n * kPair + rank * kOwn, k = w.k * kPair;
+      const int columns = n < p.N ? min(kPair, p.K - k) : 0;
+      uint16_t* o = p.dw + (static_cast<long long>(w.group) * p.N + n + quarter * 32 + lane) * p.K + k;
       if (w.rows == 0) {
         const uint32_t zero[8] = {};
         for (int q = 0; q < columns; q += 16) store32(o + q, zero, wide);
@@ -350,21 +365,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
       }
       const int ac = used & 1, e = used % kExponents;
       if (!__all_sync(kFullMask, wait_or_quit(&s.exp_full[e], (used / kExponents) & 1, quit, err) &&
-                                     wait_or_quit(&s.acc_full[ac], (used >> 1) & 1, quit, err)))
+                                     wait_or_quit<true>(&s.acc_full[ac], (used >> 1) & 1, quit, err)))
         break;
       tmem_fence_after();
-      const float up[2] = {power_of_two(s.exponent[e][0]), power_of_two(s.exponent[e][1])};
+      const float up[2] = {power_of_two(s.exponent[e][0] + s.exponent[e][1]), power_of_two(s.exponent[e][0] + s.exponent[e][2])};
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.exp_empty[e]);
 #pragma unroll
-      for (int q = 0; q < kTileK / 32; ++q) {
+      for (int q = 0; q < kPair / 32; ++q) {
         uint32_t v[32];
-        tmem_load32(lanes + ac * kTileK + q * 32, v);
+        tmem_load32(lanes + ac * kPair + q * 32, v);
         tmem_load_wait(v);
-        if (q == kTileK / 32 - 1) {
+        if (q == kPair / 32 - 1) {
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
+          if (lane == 0) mbar_arrive_first(&s.acc_empty[ac]);
         }
         const float f = up[q >> 2];
         if (q * 32 < columns) {
@@ -384,18 +399,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_weight_grad(const WeightGradArg
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  cluster_sync();  // the other block arrives on this one's barriers until here
   if (warp == kMmaWarp) {
     tmem_fence_after();
-    tmem_free(tmem, kTmemColumns);
+    pair_tmem_free(tmem, kTmemColumns);
   }
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream) {
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared) + sizeof(Group) * p.groups.G;
+  CUtensorMap map_dy, map_x;
+  cudaError_t e = make_byte_map(&map_dy, p.dy.data, p.N, p.groups.rows, 0, kRows);
+  if (e == cudaSuccess) e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, kRows);
   static std::atomic<unsigned long long> ready;  // devices set up, a bit each
-  const cudaError_t e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
+  if (e == cudaSuccess) e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_weight_grad, dim3(sms), dim3(kThreads), smem, stream, p);
+  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
+                      sizeof(Shared) + sizeof(int) * p.groups.G;
+  // pairs of blocks: an even number of SMs, two at least
+  return launch_pairs(k_weight_grad, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, p);
 }
 
 }  // namespace ep
