@@ -14,10 +14,10 @@
 // Shared memory is what bounds it: a widened 64-row stage is written once and
 // read once per MMA.  So two blocks on neighbouring SMs share a tile of 256 (n)
 // x 256 (k): each widens its 128 columns of dy and of x, 32 KB a stage instead
-// of the 48 KB of a 128 x 256 tile of its own, for the same MMA time.  One warp
-// fetches e4m3 rows (TMA) and scales (asynchronous copies) four stages ahead,
-// across tiles; two teams of eight warps take every other stage, widen it and
-// store it with the 128-byte swizzle, rows along the long axis (both operands
+// of the 48 KB of a 128 x 256 tile of its own, for the same MMA time.  Two warps
+// fetch e4m3 rows (TMA) and scales (asynchronous copies) four stages ahead,
+// across tiles; four teams of four warps take a stage each in turn, widen it
+// and store it with the 128-byte swizzle, rows along the long axis (both operands
 // "MN major", so nothing is transposed).  One warp of the first block issues
 // four MMAs a stage; four warps write the previous tile from the other TMEM
 // accumulator; one looks up the next tiles' largest scales.  Rows past the
@@ -33,14 +33,15 @@ namespace {
 constexpr int kPair = 256;     // the pair's tile: 256 x 256
 constexpr int kOwn = 128;      // a block's columns of dy, of x and rows of the accumulator
 constexpr int kRows = 64;
-constexpr int kStages = 4;     // widened; even, so that a stage belongs to one team
-constexpr int kRawStages = 4;  // as fetched
+constexpr int kStages = 4;     // widened
+constexpr int kRawStages = 4;  // as fetched; both a multiple of the teams: a stage belongs to one
 constexpr int kChunkBytes = kRows * 128;  // 64 columns of f16
 constexpr int kStageBytes = 2 * kOwn / 64 * kChunkBytes;
 constexpr int kRawBytes = 2 * kOwn * kRows, kScaleBytes = 2 * 4 * kRows;  // dy, x; their scales
-constexpr int kTeams = 2, kTeamWarps = 8, kLoadWarps = kTeams * kTeamWarps, kStoreWarps = 4;
+constexpr int kTeams = 4, kTeamWarps = 4, kPass = 4 * kTeamWarps, kLoadWarps = kTeams * kTeamWarps, kStoreWarps = 4;
 constexpr int kMmaWarp = kLoadWarps + kStoreWarps, kScaleWarp = kMmaWarp + 1, kFetchWarp = kMmaWarp + 2;
-constexpr int kThreads = (kFetchWarp + 1) * 32;
+constexpr int kFetchWarps = 2;
+constexpr int kThreads = (kFetchWarp + kFetchWarps) * 32;
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kExponents = 8;  // tiles whose exponents are kept: at least stages + 2
 
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* my_scales = reinterpret_cast<const float*>(raw_scales) + my_row;
     Cursor now;
     now.begin(w);
-    if (team) now.step();
+    for (int i = 0; i < team; ++i) now.step();
     uint32_t tile = ~0u;  // whose exponents `dy_down` and `x_down` hold
     float dy_down = 1.0f, x_down = 1.0f;
     for (uint32_t it = team; now.on; it += kTeams) {
@@ -221,66 +222,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = ok && wait_or_quit(&s.raw_full[rs], (it / kRawStages) & 1, quit, err);
       if (!__all_sync(kFullMask, ok)) break;
-      uint4 q[4];
-      float f[4];
+      // the whole part to registers, so that the stage refills meanwhile
+      const unsigned char* raw_at = my_raw + rs * kRawBytes;
+      const float* scales_at = my_scales + rs * (kScaleBytes / 4);
+      const int left = now.w.rows - now.b * kRows - my_row;  // rows past it are another group's
+      uint4 q[2][kRows / kPass];
+      float f[2][kRows / kPass];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool on = now.b * kRows + my_row + 32 * j < now.w.rows;  // else another group's row
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        q[j] = on ? lds128(my_raw + rs * kRawBytes + j * 32 * kOwn) : zero;
-        q[2 + j] = on ? lds128(my_raw + rs * kRawBytes + kOwn * kRows + j * 32 * kOwn) : zero;
-        f[j] = my_scales[rs * (kScaleBytes / 4) + j * 32];
-        f[2 + j] = my_scales[rs * (kScaleBytes / 4) + kRows + j * 32];
+      for (int j = 0; j < kRows / kPass; ++j) {
+        const bool on = j * kPass < left;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          q[h][j] = on ? lds128(raw_at + h * kOwn * kRows + j * kPass * kOwn) : make_uint4(0, 0, 0, 0);
+          f[h][j] = scales_at[h * kRows + j * kPass] * (h ? x_down : dy_down);
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.raw_empty[rs]);
       if (it >= kStages &&
           !__all_sync(kFullMask, wait_or_quit<true>(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err)))
         break;
       const uint32_t lo = unit_lo + st * kStageBytes, hi = unit_hi + st * kStageBytes;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        store_chunk(lo + j * 32 * 128, hi + j * 32 * 128, q[j], f[j] * dy_down);
-        store_chunk(lo + 2 * kChunkBytes + j * 32 * 128, hi + 2 * kChunkBytes + j * 32 * 128, q[2 + j], f[2 + j] * x_down);
-      }
+      for (int j = 0; j < kRows / kPass; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          store_chunk(lo + h * 2 * kChunkBytes + j * kPass * 128, hi + h * 2 * kChunkBytes + j * kPass * 128, q[h][j], f[h][j]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.raw_empty[rs]);
-        mbar_arrive_first(&s.full[st]);
-      }
+      if (lane == 0) mbar_arrive_first(&s.full[st]);
       for (int i = 0; i < kTeams; ++i) now.step();
     }
-  } else if (warp == kFetchWarp) {
-    uint32_t it = 0;
-    bool ok = true;
-    for (bool on = w.settle(); ok && on; on = w.next()) {
-      const int blocks = w.blocks(), n = w.n * 2 + rank, k = w.k * 2 + rank;
+  } else if (warp >= kFetchWarp) {
+    const int mine = warp - kFetchWarp;
+    Cursor c;
+    c.begin(w);
+    for (int i = 0; i < mine; ++i) c.step();
+    uint32_t it = mine;
+    for (; c.on; it += kFetchWarps) {
+      const int n = c.w.n * 2 + rank, k = c.w.k * 2 + rank;
       const bool in_n = n < (p.N >> 7), in_k = k < (p.K >> 7);
-      const long long first = w.row();
-      for (int b = 0; b < blocks; ++b, ++it) {
-        const int rs = it % kRawStages;
-        if (it >= kRawStages &&
-            !(ok = __all_sync(kFullMask, wait_or_quit(&s.raw_empty[rs], ((it / kRawStages) & 1) ^ 1, quit, err))))
-          break;
-        const long long r = first + b * kRows;
-        if (elect_one()) {
-          // columns past the matrix and rows past the buffer read as zeros
-          mbar_arrive_expect_tx(&s.raw_full[rs], kRawBytes);
-          tma_load_2d(raws + rs * kRawBytes, &map_dy, n * kOwn, static_cast<int>(r), &s.raw_full[rs]);
-          tma_load_2d(raws + rs * kRawBytes + kOwn * kRows, &map_x, k * kOwn, static_cast<int>(r), &s.raw_full[rs]);
-        }
-        __syncwarp();
-        const uint32_t dst = smem_u32(raw_scales + rs * kScaleBytes) + lane * 4;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool live = b * kRows + lane + 32 * j < w.rows;
-          copy_async4(dst + j * 128, live && in_n ? p.dy.scale(r + lane + 32 * j, n) : p.dy.scales, live && in_n);
-          copy_async4(dst + 4 * kRows + j * 128, live && in_k ? p.x.scale(r + lane + 32 * j, k) : p.x.scales, live && in_k);
-        }
-        copy_async_arrive(&s.raw_full[rs]);
+      const int rs = it % kRawStages;
+      const long long r = c.w.row() + c.b * kRows;
+      if (it >= kRawStages &&
+          !__all_sync(kFullMask, wait_or_quit(&s.raw_empty[rs], ((it / kRawStages) & 1) ^ 1, quit, err)))
+        break;
+      if (elect_one()) {
+        // columns past the matrix and rows past the buffer read as zeros
+        mbar_arrive_expect_tx(&s.raw_full[rs], kRawBytes);
+        tma_load_2d(raws + rs * kRawBytes, &map_dy, n * kOwn, static_cast<int>(r), &s.raw_full[rs]);
+        tma_load_2d(raws + rs * kRawBytes + kOwn * kRows, &map_x, k * kOwn, static_cast<int>(r), &s.raw_full[rs]);
       }
+      __syncwarp();
+      const uint32_t dst = smem_u32(raw_scales + rs * kScaleBytes) + lane * 4;
+      const float* dy_scale = p.dy.scale(r + lane, n);
+      const float* x_scale = p.x.scale(r + lane, k);
+      const int left = c.w.rows - c.b * kRows - lane;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool live = 32 * j < left;
+        copy_async4(dst + j * 128, live && in_n ? dy_scale + j * 32 * p.dy.row_stride : p.dy.scales, live && in_n);
+        copy_async4(dst + 4 * kRows + j * 128, live && in_k ? x_scale + j * 32 * p.x.row_stride : p.x.scales, live && in_k);
+      }
+      copy_async_arrive(&s.raw_full[rs]);
+      for (int i = 0; i < kFetchWarps; ++i) c.step();
     }
     // no copy may outlive the block: wait for the last fill of every stage
-    for (uint32_t i = it < kRawStages ? 0 : it - kRawStages; i < it; ++i) {
+    for (uint32_t i = it < kRawStages ? mine : it - kRawStages; i < it; i += kFetchWarps) {
       int none = 0;
       wait_or_quit(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, &none, err);
     }
