@@ -109,24 +109,29 @@ __device__ __forceinline__ int find_group(const unsigned* prefix, int G, unsigne
 // another: one that gives up latches EP_ERR_TIMEOUT and raises `quit`, which
 // ends every other warp's wait too.
 // `kCluster`: the barrier's arrivals may come from the cluster's other block.
+template <bool kCluster>
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  if (kCluster)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return done != 0;
+}
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, volatile int* quit, int* err) {
   const uint32_t addr = smem_u32(bar);
+  if (phase_done<kCluster>(addr, parity)) return true;
   for (int it = 0; it < kSpinLimit; ++it) {
-    uint32_t done;
-    if (kCluster)
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-          : "=r"(done)
-          : "r"(addr), "r"(parity)
-          : "memory");
-    else
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-          : "=r"(done)
-          : "r"(addr), "r"(parity)
-          : "memory");
-    if (done) return true;
+    if (phase_done<kCluster>(addr, parity)) return true;
     if (it >= 64) {
       if (*quit) return false;
       __nanosleep(32);

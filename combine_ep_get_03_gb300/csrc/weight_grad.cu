@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ac = used & 1, blocks = w.blocks();
       ok = __all_sync(kFullMask, used < 2 || wait_or_quit<true>(&s.acc_empty[ac], ((used >> 1) & 1) ^ 1, quit, err));
       if (!ok) break;
-      for (int b = 0; b < blocks; ++b, ++it) {
+      int left = w.rows;
+      for (int b = 0; b < blocks; ++b, ++it, left -= kRows) {
         const int st = it % kStages;
         ok = __all_sync(kFullMask, wait_or_quit<true>(&s.full[st], (it / kStages) & 1, quit, err));
         if (!ok) break;
@@ -339,10 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           // descriptors count 16-byte units; an MMA takes 16 rows of 128 bytes
           const uint64_t dy = first + st * (kStageBytes >> 4), x = dy + (2 * kChunkBytes >> 4);
-          const int steps = (min(kRows, w.rows - b * kRows) + 15) >> 4;
 #pragma unroll
           for (int j = 0; j < kRows / 16; ++j)
-            if (j < steps) pair_mma_f16(tmem + ac * kPair, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
+            if (16 * j < left) pair_mma_f16(tmem + ac * kPair, dy + 128 * j, x + 128 * j, desc, b > 0 || j > 0);
           pair_mma_commit(&s.empty[st]);
         }
         __syncwarp();
