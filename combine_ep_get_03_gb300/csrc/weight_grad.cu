@@ -222,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = ok && wait_or_quit(&s.raw_full[rs], (it / kRawStages) & 1, quit, err);
       if (!__all_sync(kFullMask, ok)) break;
-      // the whole part to registers, so that the stage refills meanwhile
       const unsigned char* raw_at = my_raw + rs * kRawBytes;
       const float* scales_at = my_scales + rs * (kScaleBytes / 4);
       const int left = now.w.rows - now.b * kRows - my_row;  // rows past it are another group's
@@ -237,8 +236,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           f[h][j] = scales_at[h * kRows + j * kPass] * (h ? x_down : dy_down);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.raw_empty[rs]);
       if (it >= kStages &&
           !__all_sync(kFullMask, wait_or_quit<true>(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err)))
         break;
@@ -250,7 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_chunk(lo + h * 2 * kChunkBytes + j * kPass * 128, hi + h * 2 * kChunkBytes + j * kPass * 128, q[h][j], f[h][j]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first(&s.full[st]);
+      // the raw stage goes back only now: its loads are complete once their values
+      // have been stored, not when they have been issued
+      if (lane == 0) {
+        mbar_arrive(&s.raw_empty[rs]);
+        mbar_arrive_first(&s.full[st]);
+      }
       for (int i = 0; i < kTeams; ++i) now.step();
     }
   } else if (warp >= kFetchWarp) {
@@ -377,8 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       tmem_fence_after();
       const float up[2] = {power_of_two(s.exponent[e][0] + s.exponent[e][1]), power_of_two(s.exponent[e][0] + s.exponent[e][2])};
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.exp_empty[e]);
 #pragma unroll
       for (int q = 0; q < kPair / 32; ++q) {
         uint32_t v[32];
@@ -401,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // the exponents have been used, not only read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.exp_empty[e]);
       ++used;
     }
   }
