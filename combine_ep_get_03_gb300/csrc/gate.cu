@@ -103,12 +103,10 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// e^(x - m) to about two parts in 10^7 near x = m; base = m log2(e), whose
-// rounding is common to a row and cancels when the row is normalised.
-constexpr float kLog2e = 1.44269504088896341f;
-__device__ __forceinline__ float exp_from(float x, float base) {
+// e^x to a few parts in 10^7 for the x that matter (an error of 2^-24 |x|).
+__device__ __forceinline__ float exp_of(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(x, kLog2e, -base)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
   return r;
 }
 
@@ -117,24 +115,23 @@ __device__ __forceinline__ float exp_from(float x, float base) {
 // min(v,0), which stays away from 0/0 when every sigmoid underflows.
 struct Scorer {
   int sigmoid;
-  float m, base;
+  float m;
   __device__ __forceinline__ Scorer(float vmax, int sig) : sigmoid(sig) {
     m = sig ? fminf(vmax, 0.0f) : vmax;
     if (m == -CUDART_INF_F) m = 0.0f;
-    base = m * kLog2e;
   }
   // *slope: d log(score) / dv -- 1 for softmax, 1 - sigmoid(v) for sigmoid
   __device__ __forceinline__ float operator()(float v, float* slope = nullptr) const {
     if (!sigmoid) {
       if (slope) *slope = 1.0f;
-      return exp_from(v, base);
+      return exp_of(v - m);
     }
-    const float e = exp_from(-fabsf(v), 0.0f);
+    const float e = exp_of(-fabsf(v));
     const float r = __fdividef(1.0f, 1.0f + e);
     if (slope) *slope = (v >= 0.0f ? e : 1.0f) * r;
     if (v != v) return v;
     // with m = 0 the numerator is at hand
-    return (m == 0.0f ? (v >= 0.0f ? 1.0f : e) : exp_from(fminf(v, 0.0f), base)) * r;
+    return (m == 0.0f ? (v >= 0.0f ? 1.0f : e) : exp_of(fminf(v, 0.0f) - m)) * r;
   }
 };
 
