@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libep_gb300.so")
 SOURCES = ["api.cu", "layout.cu", "dispatch.cu", "combine.cu", "ll_dispatch.cu", "layout_noalloc.cu", "scatter_tma.cu", "dispatch_fused.cu",
-           "experts_api.cu", "gate.cu", "grouped_matmul.cu", "swiglu_backward.cu", "weight_grad.cu"]
+           "em_weights.cu", "experts_api.cu", "gate.cu", "grouped_matmul.cu", "swiglu_backward.cu", "weight_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -9,6 +9,7 @@
 
 #include "ep.h"
 #include "ep_internal.h"
+#include "experts.cuh"
 #include "routing.cuh"
 
 struct ep_handle {
@@ -902,6 +903,36 @@ ep_status_t ep_em_combine(ep_handle_t h, const void* y, int64_t y_rows, void* ou
   ep::launch_combine(a, ep::kSrcExpertMajor, false, blocks, reinterpret_cast<cudaStream_t>(stream));
   if (h->debug) std::fprintf(stderr, "[ep] em combine T=%d: %d blocks\n", T, blocks);
   return cuda_status(cudaGetLastError(), "k_combine(em) launch");
+}
+
+ep_status_t ep_em_get_groups(ep_handle_t h, int* group_offset, int* group_count, ep_stream_t stream) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  if (h->T_em < 0) return EP_ERR_STATE;
+  if (!aligned4(group_offset) || !aligned4(group_count)) return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_device(h);
+  if (st != EP_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (group_offset)
+    e = cudaMemcpyAsync(group_offset, h->em_offset, sizeof(int) * (h->E + 1), cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess && group_count)
+    e = cudaMemcpyAsync(group_count, h->em_count, sizeof(int) * h->E, cudaMemcpyDeviceToDevice, s);
+  return cuda_status(e, "ep_em_get_groups");
+}
+
+ep_status_t ep_em_combine_weights(ep_handle_t h, const float* row_weights, int64_t rows, float* topk_weights,
+                                  ep_stream_t stream) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  if (h->T_em < 0) return EP_ERR_STATE;
+  if (rows < 0 || (h->T_em > 0 && (!topk_weights || (rows > 0 && !row_weights))) || !aligned4(row_weights) ||
+      !aligned4(topk_weights))
+    return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_device(h);
+  if (st != EP_OK || h->T_em == 0) return st;
+  return cuda_status(ep::launch_em_combine_weights(h->em_idx, h->em_slot, h->em_offset, row_weights, rows,
+                                                   static_cast<long long>(h->T_em) * h->k, topk_weights, h->err,
+                                                   reinterpret_cast<cudaStream_t>(stream)),
+                     "k_em_combine_weights launch");
 }
 
 ep_status_t ep_get_buffer_size_hint(int R, int E, int k, int H, int max_tpr, ep_dtype_t dtype, ep_layout_t layout,

@@ -275,5 +275,8 @@ cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& p, int sms, cudaStr
 cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream);
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream);
 size_t gate_work_bytes(int E);
+// out[i] = row_weights[the expert-major row of entry i], 0 where masked.
+cudaError_t launch_em_combine_weights(const int* idx, const int* slot, const int* offset, const float* row_weights,
+                                      long long rows, long long entries, float* out, int* err, cudaStream_t stream);
 
 }  // namespace ep

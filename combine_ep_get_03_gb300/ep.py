@@ -67,6 +67,8 @@ def lib() -> ctypes.CDLL:
             L.ep_em_dispatch.argtypes = [P, P, P, I, P, P, I64, I64, P, P, I, P]
             L.ep_em_get_layout.argtypes = [P, P, P, P]
             L.ep_em_combine.argtypes = [P, P, I64, P, I, P]
+            L.ep_em_get_groups.argtypes = [P, P, P, P]
+            L.ep_em_combine_weights.argtypes = [P, P, I64, P, P]
             L.ep_get_buffer_size_hint.argtypes = [I, I, I, I, I, I, I, I, P, P]
             L.ep_layout_and_dispatch.argtypes = [P, P, I, P, P, I, P, P, I64, P, P, P, I, P]
             L.ep_low_latency_dispatch.argtypes = [P, P, P, I, I, P, P, P, P, I, P]
@@ -89,7 +91,7 @@ def lib() -> ctypes.CDLL:
                       "ep_dispatch", "ep_combine", "ep_layout_and_dispatch", "ep_low_latency_dispatch",
                       "ep_low_latency_combine", "ep_combine_ex", "ep_handle_set_topk_idx_bits",
                       "ep_em_layout_and_dispatch", "ep_em_dispatch", "ep_em_get_layout", "ep_em_combine",
-                      "ep_get_buffer_size_hint", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
+                      "ep_get_buffer_size_hint", "ep_em_get_groups", "ep_em_combine_weights", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
                       "ep_grouped_matmul", "ep_grouped_matmul_swiglu", "ep_grouped_swiglu_backward",
                       "ep_grouped_weight_grad",
                       "ep_get_device_status", "ep_check_wait_timeout", "ep_get_dispatch_layout_noalloc"):
@@ -299,6 +301,21 @@ def ep_em_get_layout(h, num_experts: int, stream=None, check: bool = True):
 def ep_em_combine(h, y, out, num_sms: int = 0, stream=None) -> None:
     _check(lib().ep_em_combine(h, _ptr(y, (torch.bfloat16,), "y"), y.shape[0], _ptr(out, (torch.bfloat16,), "out"),
                                int(num_sms), _stream(stream)), "ep_em_combine")
+
+
+def ep_em_get_groups(h, group_offset=None, group_count=None, stream=None) -> None:
+    """Copy the last expert-major layout's group offsets [E+1] and counts [E]
+    to device tensors, without synchronising."""
+    _check(lib().ep_em_get_groups(h, _ptr(group_offset, (torch.int32,), "group_offset"),
+                                  _ptr(group_count, (torch.int32,), "group_count"), _stream(stream)),
+           "ep_em_get_groups")
+
+
+def ep_em_combine_weights(h, row_weights, topk_weights, stream=None) -> None:
+    """topk_weights [T, k] = the value of each entry's expert-major row, 0 where masked."""
+    _check(lib().ep_em_combine_weights(h, _ptr(row_weights, (torch.float32,), "row_weights"), row_weights.numel(),
+                                       _ptr(topk_weights, (torch.float32,), "topk_weights"), _stream(stream)),
+           "ep_em_combine_weights")
 
 
 def ep_get_buffer_size_hint(num_ranks, num_experts, num_topk, hidden, max_tokens_per_rank, dtype: int,
@@ -769,6 +786,17 @@ class Handle:
             raise ValueError(f"y must be [rows, {self.H}]")
         self._need(out, self.T_em * self.H, "out")
         ep_em_combine(self.ptr, y, out, num_sms, stream)
+
+    def em_get_groups(self, group_offset=None, group_count=None, stream=None):
+        self._need(group_offset, self.E + 1, "group_offset")
+        self._need(group_count, self.E, "group_count")
+        ep_em_get_groups(self.ptr, group_offset, group_count, stream)
+
+    def em_combine_weights(self, row_weights, topk_weights, stream=None):
+        if self.T_em is None:
+            raise RuntimeError("expert-major combine before any expert-major layout")
+        self._need(topk_weights, self.T_em * self.k, "topk_weights")
+        ep_em_combine_weights(self.ptr, row_weights, topk_weights, stream)
 
     def get_device_status(self, stream=None):
         return ep_get_device_status(self.ptr, stream)

@@ -316,6 +316,22 @@ ep_status_t ep_em_get_layout(ep_handle_t h, int* num_recv_tokens_per_expert, int
 ep_status_t ep_em_combine(ep_handle_t h, const void* y, int64_t y_rows, void* out, int num_sms,
                           ep_stream_t stream);
 
+/* Copy the last expert-major layout's groups to device memory, on `stream`
+ * and without synchronising: what the grouped calls below take.
+ * Out (each may be NULL): group_offset dev int32 [E+1] (first row of each
+ * group, [E] = rows used), group_count dev int32 [E] (rows per expert). */
+ep_status_t ep_em_get_groups(ep_handle_t h, int* group_offset, int* group_count, ep_stream_t stream);
+
+/* One value per expert-major row back to its (token, k) entry: topk_weights
+ * dev fp32 [T][k], entry (t, j) = row_weights[its row of the last expert-major
+ * layout], 0 where masked.  On the dispatch's own recv_weights this gives back
+ * topk_weights; on the gradient of the rows' weights it is the gradient of
+ * topk_weights (as combined_topk_weights in ep_combine_ex).  row_weights: dev
+ * fp32 [rows]; an entry whose row is at or past `rows` gets 0 and latches
+ * EP_ERR_CAPACITY. */
+ep_status_t ep_em_combine_weights(ep_handle_t h, const float* row_weights, int64_t rows, float* topk_weights,
+                                  ep_stream_t stream);
+
 /* Receive-buffer sizes for a configuration, before any routing is known
  * (the pages' get_buffer_size_hint: the size needed, to allocate once or to
  * check that an existing buffer can be reused; vi.news.hada.io, "Giao diện
