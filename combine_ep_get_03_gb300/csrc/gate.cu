@@ -26,7 +26,7 @@
 namespace ep {
 
 // Warps of a block: as many as leave room for a row of floats each.
-__host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 2; }
+__host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 1; }
 __host__ __device__ constexpr int index_bits(int vpl) { return vpl == 1 ? 5 : 1 + index_bits(vpl / 2); }
 constexpr float kFixed = 68719476736.0f;  // 2^36
 
@@ -37,11 +37,11 @@ __device__ __forceinline__ unsigned long long* work_sums(unsigned* w) {
 }
 __device__ __forceinline__ int* work_counts(unsigned* w, int E) { return reinterpret_cast<int*>(w + 4 + 2 * E); }
 
-// Order-preserving image of a float, equal for -0 and +0.  -inf, and NaN in its
-// place, have the image kNever; what is not above it is never chosen.
+// Order-preserving image of a float that is not NaN, equal for -0 and +0.
+// -inf has the image kNever; what is not above it is never chosen.
 constexpr unsigned kNever = 0x007fffffu;
 __device__ __forceinline__ unsigned order_key(float v) {
-  const unsigned b = __float_as_uint(fmaxf(v + 0.0f, -CUDART_INF_F));
+  const unsigned b = __float_as_uint(v + 0.0f);
   return b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 
@@ -110,30 +110,46 @@ __device__ __forceinline__ float exp_of(float x) {
   return r;
 }
 
-// Unnormalised score of a logit: e^(v - m) for softmax with m the largest
-// logit; for sigmoid e^(min(v,0) - m) / (1 + e^-|v|) with m the largest
-// min(v,0), which stays away from 0/0 when every sigmoid underflows.
-struct Scorer {
-  int sigmoid;
-  float m;
-  __device__ __forceinline__ Scorer(float vmax, int sig) : sigmoid(sig) {
-    m = sig ? fminf(vmax, 0.0f) : vmax;
-    if (m == -CUDART_INF_F) m = 0.0f;
+// Unnormalised score of a logit v, and its slope d log(score) / dv:
+//   softmax            e^(v - m), m the row's largest;              slope 1
+//   sigmoid, m >= 0    1 / (1 + e^-v);                               slope 1 - sigmoid(v)
+//   sigmoid, m < 0     e^(v - m) / (1 + e^v), which stays away from 0/0 when
+//                      every sigmoid underflows;                     slope 1 - sigmoid(v)
+// One kind holds for a row, so it is chosen once and the logits' arithmetic has
+// no selection (the half-rate integer and compare pipe bounds these kernels).
+enum ScoreKind { kSoftmax, kSigmoid, kSmallSigmoid };
+__device__ __forceinline__ ScoreKind score_kind(float& m, int sigmoid) {
+  if (m == -CUDART_INF_F) m = 0.0f;
+  return !sigmoid ? kSoftmax : m < 0.0f ? kSmallSigmoid : kSigmoid;
+}
+template <ScoreKind kKind>
+__device__ __forceinline__ float score_of(float v, float m, float* slope) {
+  if (kKind == kSoftmax) {
+    if (slope) *slope = 1.0f;
+    return exp_of(v - m);
   }
-  // *slope: d log(score) / dv -- 1 for softmax, 1 - sigmoid(v) for sigmoid
-  __device__ __forceinline__ float operator()(float v, float* slope = nullptr) const {
-    if (!sigmoid) {
-      if (slope) *slope = 1.0f;
-      return exp_of(v - m);
-    }
-    const float e = exp_of(-fabsf(v));
-    const float r = __fdividef(1.0f, 1.0f + e);
-    if (slope) *slope = (v >= 0.0f ? e : 1.0f) * r;
-    if (v != v) return v;
-    // with m = 0 the numerator is at hand
-    return (m == 0.0f ? (v >= 0.0f ? 1.0f : e) : exp_of(fminf(v, 0.0f) - m)) * r;
+  const float e = exp_of(kKind == kSigmoid ? -v : v);
+  const float r = __fdividef(1.0f, 1.0f + e);  // 0 from e = 2^126 on
+  if (kKind == kSigmoid) {
+    if (slope) *slope = fminf(e, 3.0e38f) * r;
+    return r;
   }
-};
+  if (slope) *slope = r;
+  return exp_of(v - m) * r;
+}
+template <int N>
+__device__ __forceinline__ void score_row(ScoreKind kind, const float* v, float m, float* x, float* slope) {
+  if (kind == kSoftmax) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = score_of<kSoftmax>(v[j], m, slope ? slope + j : nullptr);
+  } else if (kind == kSigmoid) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = score_of<kSigmoid>(v[j], m, slope ? slope + j : nullptr);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = score_of<kSmallSigmoid>(v[j], m, slope ? slope + j : nullptr);
+  }
+}
 
 // The lane's values sorted out of the keys c[] (order keys whose low bits are
 // replaced by the inverted index, 0 = never chosen): the largest of the warp.
@@ -169,15 +185,14 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   constexpr int kWarps = gate_warps(VPL);
   constexpr int kBits = index_bits(VPL);
   constexpr unsigned kIndex = (1u << kBits) - 1u;
-  extern __shared__ float sm[];  // [E] sums, then [E] counts, then [warps][groups] keys
-  float* s_sum = sm;
-  int* s_count = reinterpret_cast<int*>(sm + p.E);
-  unsigned* s_group = reinterpret_cast<unsigned*>(sm + 2 * p.E) + (threadIdx.x >> 5) * p.groups;
+  extern __shared__ __align__(16) float sm[];  // [warps][32 VPL] sums, [E] counts, [warps][groups] keys
+  int* s_count = reinterpret_cast<int*>(sm + kWarps * 32 * VPL);
+  unsigned* s_group = reinterpret_cast<unsigned*>(s_count + p.E) + (threadIdx.x >> 5) * p.groups;
   __shared__ int s_live, s_bad, s_last;
   __shared__ float s_part[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.E, k = p.k;
-  for (int e = tid; e < E; e += blockDim.x) s_sum[e] = 0.0f, s_count[e] = 0;
+  for (int e = tid; e < E; e += blockDim.x) s_count[e] = 0;
   if (tid == 0) s_live = 0, s_bad = 0;
   __syncthreads();
 
@@ -197,42 +212,46 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       float v[VPL];
       load_row<T, VPL>(static_cast<const T*>(p.logits) + t * p.ld, E, lane, p.vec, v);
       // probabilities over all experts
-      float m = v[0];
+      float mine = v[0];
 #pragma unroll
-      for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
+      for (int j = 1; j < VPL; ++j) mine = fmaxf(mine, v[j]);
       {
-        const Scorer score(warp_max(m), p.sigmoid);
+        float m = warp_max(mine);
+        const ScoreKind kind = score_kind(m, p.sigmoid);
         float x[VPL], sum = 0.0f;
+        score_row<VPL>(kind, v, m, x, nullptr);  // 0 past E, where v is -inf
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          x[j] = score(v[j]);  // 0 past E, where v is -inf
-          sum += x[j];
-        }
+        for (int j = 0; j < VPL; ++j) sum += x[j];
         sum = warp_sum(sum);
-        bad |= !(sum < CUDART_INF_F);
+        if (!(sum < CUDART_INF_F)) {
+          // a NaN, or an infinity under softmax: the sums are marked, and the
+          // choice goes on without the NaNs
+          bad = true;
+          mine = -CUDART_INF_F;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) {
+            v[j] = fmaxf(v[j], -CUDART_INF_F);
+            mine = fmaxf(mine, v[j]);
+          }
+        }
         const float inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;  // a row of -inf has no probability
 #pragma unroll
         for (int j = 0; j < VPL; ++j) acc[j] = fmaf(x[j], inv, acc[j]);
       }
       // experts of groups that are not kept drop out of the choice
+      bool allowed = true;  // the lane's experts, where groups are whole lanes
       if (p.groups > 1) {
         if (span) {
-          unsigned key = 0u;
-#pragma unroll
-          for (int j = 0; j < VPL; ++j) key = max(key, order_key(v[j]));
-          for (int d = 1; d < span; d <<= 1) key = max(key, __shfl_xor_sync(kFullMask, key, d));
+          for (int d = 1; d < span; d <<= 1) mine = fmaxf(mine, __shfl_xor_sync(kFullMask, mine, d));
           // 0: taken, past the last expert, or not the group's first lane
-          unsigned mine = (lane & (span - 1)) == 0 && lane * VPL < E ? max(key, 1u) : 0u;
-          bool allowed = false;  // groups are whole lanes
+          unsigned key = (lane & (span - 1)) == 0 && lane * VPL < E ? order_key(mine) : 0u;
+          allowed = false;
           for (int i = 0; i < p.keep; ++i) {
-            const unsigned top = __reduce_max_sync(kFullMask, mine);
-            const int src = __ffs(__ballot_sync(kFullMask, mine == top)) - 1;
-            if (lane == src) mine = 0u;
+            const unsigned top = __reduce_max_sync(kFullMask, key);
+            const int src = __ffs(__ballot_sync(kFullMask, key == top)) - 1;
+            if (lane == src) key = 0u;
             if ((lane & ~(span - 1)) == src) allowed = true;
           }
-#pragma unroll
-          for (int j = 0; j < VPL; ++j)
-            if (!allowed) v[j] = -CUDART_INF_F;
         } else {
           for (int g = lane; g < p.groups; g += 32) s_group[g] = 0u;
           __syncwarp();
@@ -283,21 +302,22 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       constexpr bool kSorted = VPL <= 16;  // more keys cost more to sort than to search again
       if (kSorted) sort_down<VPL>(c);
       unsigned best = kSorted ? c[0] : local_max<VPL>(c), my_key = 0u;
+      if (!allowed) best = 0u;
       constexpr int kMore = sizeof(T) == 4 ? 1 : 0;
       for (int i = 0; i < k + kMore && i < 32; ++i) {
         const unsigned top = __reduce_max_sync(kFullMask, best);
         if (top <= kNever) break;
         if (lane == i) my_key = top;
         if (kSorted) {
-          const bool mine = best == top;
+          const bool drop = best == top;
 #pragma unroll
-          for (int j = 0; j + 1 < VPL; ++j) c[j] = mine ? c[j + 1] : c[j];
-          c[VPL - 1] = mine ? 0u : c[VPL - 1];
-          best = c[0];
+          for (int j = 0; j + 1 < VPL; ++j) c[j] = drop ? c[j + 1] : c[j];
+          c[VPL - 1] = drop ? 0u : c[VPL - 1];
+          best = allowed ? c[0] : 0u;
         } else {
 #pragma unroll
           for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
-          best = local_max<VPL>(c);
+          best = allowed ? local_max<VPL>(c) : 0u;
         }
       }
       bool again = false;
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
         if (lane < k && my_key) my_id = static_cast<int>(kIndex - (my_key & kIndex));
       } else {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) c[j] = order_key(v[j]);
+        for (int j = 0; j < VPL; ++j) c[j] = allowed ? order_key(v[j]) : 0u;
         for (int i = 0; i < k; ++i) {
           best = local_max<VPL>(c);
           const unsigned top = __reduce_max_sync(kFullMask, best);
@@ -328,9 +348,10 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       }
       // weights of the chosen: their logits once more, from the cache
       const float my_v = my_id >= 0 ? load_logit(static_cast<const T*>(p.logits) + t * p.ld + my_id) : -CUDART_INF_F;
-      const float top_v = __shfl_sync(kFullMask, my_v, 0);
-      const Scorer score(top_v, p.sigmoid);
-      const float s = my_id >= 0 ? score(my_v) : 0.0f;
+      float top_v = __shfl_sync(kFullMask, my_v, 0);
+      float s;
+      score_row<1>(score_kind(top_v, p.sigmoid), &my_v, top_v, &s, nullptr);
+      if (my_id < 0) s = 0.0f;
       const float s_all = sum_first(s, k);
       my_w = my_id >= 0 ? share_of(s, s_all) : 0.0f;
       if (my_id >= 0) atomicAdd(&s_count[my_id], 1);
@@ -341,24 +362,25 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       p.weights[o] = my_w;
     }
   }
-  // the block's sums, warp after warp so that their order is fixed
-  const int busy = min(kWarps, p.T - static_cast<int>(blockIdx.x) * kWarps);  // warps that had a token
-  for (int w = 0; w < busy; ++w) {
-    if (w == warp) {
+  // the block's sums, in the order of its warps
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (lane * VPL + j < E) s_sum[lane * VPL + j] += acc[j];
-      if (lane == 0) s_live += live;
-      if (bad) s_bad = 1;
-    }
-    __syncthreads();
-  }
+  for (int j = 0; j < VPL; ++j) sm[warp * 32 * VPL + lane * VPL + j] = acc[j];
+  if (lane == 0 && live) atomicAdd(&s_live, live);
+  if (bad) s_bad = 1;
+  __syncthreads();
+  const int busy = min(kWarps, p.T - static_cast<int>(blockIdx.x) * kWarps);  // warps that had a token
+  auto block_sum = [&](int e) {
+    float sum = 0.0f;
+    for (int w = 0; w < busy; ++w) sum += sm[w * 32 * VPL + e];
+    return sum;
+  };
   unsigned long long* sums = work_sums(p.work);
   int* counts = work_counts(p.work, E);
   const bool alone = gridDim.x == 1;  // the block's sums are everybody's
   if (!alone) {
     for (int e = tid; e < E; e += blockDim.x) {
-      if (s_sum[e] > 0.0f) atomicAdd(&sums[e], __float2ull_rn(s_sum[e] * kFixed));
+      const float sum = block_sum(e);
+      if (sum > 0.0f) atomicAdd(&sums[e], __float2ull_rn(sum * kFixed));
       if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
     }
     if (tid == 0) {
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   float part = 0.0f;
   for (int e = tid; e < E; e += blockDim.x) {
     const int n = alone ? s_count[e] : __ldcg(&counts[e]);
-    const float sum = alone ? s_sum[e] : __ull2float_rn(__ldcg(&sums[e])) * (1.0f / kFixed);
+    const float sum = alone ? block_sum(e) : __ull2float_rn(__ldcg(&sums[e])) * (1.0f / kFixed);
     const float pe = any_bad ? CUDART_NAN_F : tokens ? sum / tokens : 0.0f;
     p.count[e] = n;
     p.prob[e] = pe;
@@ -462,10 +484,9 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
           id = wide >= 0 && wide < E ? static_cast<int>(wide) : -1;
           if (id >= 0) x = load_logit(row + id);
         }
-        const Scorer score(max_first(x, k), p.sigmoid);
-        float slope;
-        x = score(x, &slope);
-        const float s = id >= 0 ? x : 0.0f;
+        float m = max_first(x, k), s, slope;
+        score_row<1>(score_kind(m, p.sigmoid), &x, m, &s, &slope);
+        if (id < 0) s = 0.0f;
         const float all = sum_first(s, k);
         const float w = id >= 0 ? share_of(s, all) : 0.0f;
         const float mean_dw = sum_first(id >= 0 ? w * dw : 0.0f, k);
@@ -475,13 +496,11 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
         float m = v[0];
 #pragma unroll
         for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
-        const Scorer score(warp_max(m), p.sigmoid);
+        m = warp_max(m);
         float sum = 0.0f, dot = 0.0f;
+        score_row<VPL>(score_kind(m, p.sigmoid), v, m, d, v);  // 0 past E, where v is -inf; v: the slopes
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          float slope;
-          d[j] = score(v[j], &slope);  // 0 past E, where v is -inf
-          v[j] = slope;
           sum += d[j];
           dot = fmaf(d[j], c[j], dot);
         }
@@ -513,7 +532,8 @@ cudaError_t launch_vpl(const GateArgs& p, bool backward, int sms, cudaStream_t s
   constexpr int kWarps = gate_warps(VPL);
   const int need = (p.T + kWarps - 1) / kWarps, most = sms * ((backward ? 48 : 32) / kWarps);
   const dim3 grid(need < 1 ? 1 : need < most ? need : most), block(kWarps * 32);
-  const size_t smem = sizeof(float) * (backward ? kWarps * 32 * VPL : 2 * p.E + (p.groups > 1 ? kWarps * p.groups : 0));
+  const size_t smem =
+      sizeof(float) * (kWarps * 32 * VPL + (backward ? 0 : p.E + (p.groups > 1 ? kWarps * p.groups : 0)));
   return backward ? launch_kernel(k_gate_backward<T, VPL>, grid, block, smem, s, p)
                   : launch_kernel(k_gate_forward<T, VPL>, grid, block, smem, s, p);
 }
