@@ -304,20 +304,35 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
       unsigned best = kSorted ? c[0] : local_max<VPL>(c), my_key = 0u;
       if (!allowed) best = 0u;
       constexpr int kMore = sizeof(T) == 4 ? 1 : 0;
-      for (int i = 0; i < k + kMore && i < 32; ++i) {
-        const unsigned top = __reduce_max_sync(kFullMask, best);
-        if (top <= kNever) break;
-        if (lane == i) my_key = top;
-        if (kSorted) {
+      if (kSorted && k <= 8) {
+        // after pick i at most 8 - i more are wanted: shorter shifts
+#pragma unroll
+        for (int i = 0; i < 8 + kMore; ++i) {
+          if (i >= k + kMore) break;
+          const unsigned top = __reduce_max_sync(kFullMask, best);
+          if (top <= kNever) break;
+          if (lane == i) my_key = top;
           const bool drop = best == top;
 #pragma unroll
-          for (int j = 0; j + 1 < VPL; ++j) c[j] = drop ? c[j + 1] : c[j];
-          c[VPL - 1] = drop ? 0u : c[VPL - 1];
+          for (int j = 0; j < VPL && j < 8 - i; ++j) c[j] = drop ? (j + 1 < VPL ? c[j + 1] : 0u) : c[j];
           best = allowed ? c[0] : 0u;
-        } else {
+        }
+      } else {
+        for (int i = 0; i < k + kMore && i < 32; ++i) {
+          const unsigned top = __reduce_max_sync(kFullMask, best);
+          if (top <= kNever) break;
+          if (lane == i) my_key = top;
+          if (kSorted) {
+            const bool drop = best == top;
 #pragma unroll
-          for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
-          best = allowed ? local_max<VPL>(c) : 0u;
+            for (int j = 0; j + 1 < VPL; ++j) c[j] = drop ? c[j + 1] : c[j];
+            c[VPL - 1] = drop ? 0u : c[VPL - 1];
+            best = allowed ? c[0] : 0u;
+          } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) c[j] = c[j] == top ? 0u : c[j];
+            best = allowed ? local_max<VPL>(c) : 0u;
+          }
         }
       }
       bool again = false;
