@@ -11,7 +11,10 @@
 // 128 channels carry their own scale.  Two accumulators of 256 columns
 // alternate, so while the tensor cores fill one, eight warps read the other (a
 // thread owns a row, so its factor sx * sw is one number) and add it, scaled,
-// to fp32 registers: 128 a thread.  Each accumulator has its own issuing warp:
+// to fp32 registers: 128 a thread.  The scales come with their operands: a
+// fourth warp copies a block's 130 numbers to shared memory, asynchronously,
+// so that the adding warps neither hold pointers nor wait for memory.  Each
+// accumulator has its own issuing warp:
 // a wait on a barrier that is already complete takes some 180 cycles here, two
 // of them and the issue 620, more than the 512 of a stage's MMAs.
 //
@@ -34,19 +37,20 @@ constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
 constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and an idle warp fill the third warpgroup
+constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and a scale warp are the third warpgroup
 // Registers: launched with 168 a thread; the third warpgroup hands most of its
 // own to the two that hold accumulators.
 constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 232, kOtherRegisters = 40;
 static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegisters <= kThreads * kLaunchRegisters, "");
 constexpr uint32_t kTmemColumns = 512;
-constexpr int kScalesAhead = 5;
+constexpr int kScaleSlots = 8;  // blocks of k whose scales are kept: a slot's reader is done two accumulators earlier
 
 struct Shared {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], amax_full;
   uint32_t tmem;
   int quit;
   unsigned sums[32];
+  float x_scale[kScaleSlots][kTileM], w_scale[kScaleSlots][2];
   float amax[2][2][3][kTileM];  // [tile parity][half][gate, up, act][row]
 };
 
@@ -74,8 +78,6 @@ __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* pref
 
 }  // namespace
 
-__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" : : "l"(p)); }
-
 template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grouped_matmul(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -89,7 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* err = p.groups.err;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+    // the loading thread's arrival and one of each of the scale warp's lanes
+    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1 + 32), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kEpilogueWarps);
     mbar_init(&s.amax_full, kEpilogueWarps);
     s.quit = 0;
@@ -169,13 +172,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         int none = 0;
         wait_or_quit(&s.acc_full[ac], ((it - 2) >> 1) & 1, &none, err);
       }
+    } else {
+      // the scales of every block of k, with its operands: 128 rows' and the
+      // weights' two (the tile's halves, or gate and up)
+      const int Gn = (p.N + 127) >> 7;
+      uint32_t it = 0;
+      bool ok = true;
+      for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const Tile c = tile_at(p.groups, prefix, tiles_n, t);
+        const float* sx = p.x.scales + (c.row + lane) * p.x.row_stride;
+        const long long step = 32 * p.x.row_stride;
+        const int n0 = kSwiglu ? c.n + (lane & 1) * (F >> 7) : c.n * 2 + (lane & 1);
+        const float* sw = p.w_scales + (static_cast<long long>(c.group) * Gn + min(n0, Gn - 1)) * blocks_k;
+        for (int kb = 0; kb < blocks_k; ++kb, ++it) {
+          const int st = it % kStages, slot = it % kScaleSlots;
+          if (it >= kStages) {
+            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
+            if (!ok) break;
+          }
+          const uint32_t dst = smem_u32(&s.x_scale[slot][lane]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (32 * j + lane < c.rows) copy_async4(dst + j * 128, sx + j * step, true);
+          if (lane < 2) copy_async4(smem_u32(&s.w_scale[slot][lane]), sw + kb, true);
+          copy_async_arrive(&s.full[st]);
+          sx += p.x.group_stride;
+        }
+      }
+      asm volatile("cp.async.wait_all;" : : : "memory");
     }
   } else {
     registers_up<kEpilogueRegisters>();
     const int half = warp >> 2, quarter = warp & 3;
     const int in_tile = quarter * 32 + lane;  // the thread's row in the tile
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (kTileN / 2);
-    const int Gk = blocks_k, Gn = (p.N + 127) >> 7;
     const bool wide = kSwiglu ? false : ((reinterpret_cast<uintptr_t>(p.out) | (static_cast<uintptr_t>(p.N) * 2)) & 31) == 0;
     uint32_t it = 0;
     int turn = 0;
@@ -184,37 +214,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile c = tile_at(p.groups, prefix, tiles_n, t);
       const long long row = c.row + in_tile;
       const bool live = in_tile < c.rows;
-      // the columns' scale blocks: one for plain tiles, gate and up for SwiGLU
-      const int n0 = kSwiglu ? c.n : c.n * 2 + half;
-      const float* sw0 = p.w_scales + (static_cast<long long>(c.group) * Gn + min(n0, Gn - 1)) * Gk;
-      const float* sw1 = kSwiglu ? sw0 + static_cast<long long>(F >> 7) * Gk : sw0;
-      const float* sx = p.x.scales + (live ? row * p.x.row_stride : 0);
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      float nx = live ? sx[0] : 0.0f, nw0 = sw0[0], nw1 = kSwiglu ? sw1[0] : 0.0f;
-#pragma unroll
-      for (int i = 1; i < kScalesAhead; ++i)
-        if (live && i < blocks_k) prefetch_l1(sx + i * p.x.group_stride);
       for (int kb = 0; kb < blocks_k; ++kb, ++it) {
         const int ac = it & 1;
-        const float f0 = nx * nw0, f1 = kSwiglu ? nx * nw1 : f0;
-        if (kb + 1 < blocks_k) {
-          // one block ahead in registers, kScalesAhead in L1
-          if (live) {
-            sx += p.x.group_stride;
-            nx = *sx;
-            if (kb + kScalesAhead < blocks_k) prefetch_l1(sx + (kScalesAhead - 1) * p.x.group_stride);
-          }
-          nw0 = sw0[kb + 1];
-          if (kSwiglu) nw1 = sw1[kb + 1];
-        }
         ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it >> 1) & 1, quit, err));
         if (!ok) break;
         tmem_fence_after();
         // 32 columns are on their way while the 32 before them are added
         uint32_t v[2][32];
         tmem_load32(lanes + ac * kTileN, v[0]);
+        const int slot = it % kScaleSlots;
+        const float fx = s.x_scale[slot][in_tile];  // of a row past the group's end: anything
+        const float f0 = fx * s.w_scale[slot][kSwiglu ? 0 : half], f1 = kSwiglu ? fx * s.w_scale[slot][1] : f0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           tmem_load_wait(v[q & 1]);
