@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
+constexpr int kRowBox = 32;  // rows a load brings
 constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and a scale warp are the third warpgroup
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
+        const int row_boxes = (c.rows + kRowBox - 1) / kRowBox;
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           const int st = it % kStages;
           if (it >= kStages) {
@@ -128,8 +130,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             unsigned char* a = stages + st * kStageBytes;
             unsigned char* b = a + kTileM * kBlockK;
-            mbar_arrive_expect_tx(&s.full[st], kStageBytes);
-            tma_load_2d(a, &map_x, kb * kBlockK, static_cast<int>(c.row), &s.full[st]);
+            // only the rows that are live, 32 at a time: the accumulators of the others
+            // hold anything and are not stored
+            mbar_arrive_expect_tx(&s.full[st], kTileN * kBlockK + row_boxes * kRowBox * kBlockK);
+            for (int q = 0; q < row_boxes; ++q)
+              tma_load_2d(a + q * kRowBox * kBlockK, &map_x, kb * kBlockK, static_cast<int>(c.row) + q * kRowBox, &s.full[st]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int n = kSwiglu ? c.n * 128 + (q >> 1) * 64 + (q & 1) * F : c.n * kTileN + q * 64;
@@ -359,7 +364,7 @@ cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long lo
 
 cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream) {
   CUtensorMap map_x, map_w;
-  cudaError_t e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, kTileM);
+  cudaError_t e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, kRowBox);
   if (e == cudaSuccess) e = make_byte_map(&map_w, p.w, p.K, p.N, p.groups.G, 64);
   if (e != cudaSuccess) return e;
   const bool swiglu = p.act.data != nullptr;
