@@ -37,6 +37,14 @@ __device__ __forceinline__ void latch_status(int* err, int code) {
   if (err) latch_error(err, code);
 }
 
+// Waits until the stream's earlier kernels have ended and their results are
+// visible, then lets a kernel launched the same way start its own preparations
+// (barriers, TMEM) on SMs that become free.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" : : : "memory");
+  asm volatile("griddepcontrol.launch_dependents;" : : : "memory");
+}
+
 // First row and row count of group g.  A group that does not fit its slots or
 // the row buffer is cut to what does (EP_ERR_CAPACITY, latched by `report`).
 __device__ __forceinline__ int group_span(const GroupArgs& a, int g, long long* start, bool report) {
@@ -180,21 +188,26 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
 
 // ------------------------------------------------------------------ launches
 
-// Kernel launch in clusters of two blocks.
+// Launch that may begin while the stream's previous kernel ends: the kernel
+// calls after_previous() before it touches any memory but its own.  `cluster`
+// blocks form a cluster.  Back to back this saves about 2 us a call (one
+// token's product 45.2 -> 43.3 us, a small weight gradient 15.7 -> 14.2 us).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                Args&&... args) {
+inline cudaError_t launch_early(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute pair[1];
-  pair[0].id = cudaLaunchAttributeClusterDimension;
-  pair[0].val.clusterDim.x = 2;
-  pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
-  cfg.attrs = pair;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   const int E = p.E, k = p.k;
   for (int e = tid; e < E; e += blockDim.x) s_count[e] = 0;
   if (tid == 0) s_live = 0, s_bad = 0;
+  after_previous();
   __syncthreads();
 
   float acc[VPL];
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_backward(const Ga
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.k;
   float* chosen = sm + warp * 32 * VPL;
+  after_previous();
   const int tokens = p.count[E];
   // sum_e p_e = 1, so c_e may be counted from any common value; from the mean
   // the difference c_e - sum p c loses fewer digits
@@ -549,8 +551,8 @@ cudaError_t launch_vpl(const GateArgs& p, bool backward, int sms, cudaStream_t s
   const dim3 grid(need < 1 ? 1 : need < most ? need : most), block(kWarps * 32);
   const size_t smem =
       sizeof(float) * (kWarps * 32 * VPL + (backward ? 0 : p.E + (p.groups > 1 ? kWarps * p.groups : 0)));
-  return backward ? launch_kernel(k_gate_backward<T, VPL>, grid, block, smem, s, p)
-                  : launch_kernel(k_gate_forward<T, VPL>, grid, block, smem, s, p);
+  return backward ? launch_early(k_gate_backward<T, VPL>, 1, grid, block, smem, s, p)
+                  : launch_early(k_gate_forward<T, VPL>, 1, grid, block, smem, s, p);
 }
 
 template <typename T>

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(&map_w);
   }
   if (warp == kEpilogueWarps + 1) tmem_alloc(&s.tmem, kTmemColumns);
+  after_previous();
   groups_prefix(p.groups, kTileM, prefix, s.sums);
   tmem_fence_before();
   __syncthreads();
@@ -372,7 +373,7 @@ cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t str
   auto kernel = swiglu ? k_grouped_matmul<true> : k_grouped_matmul<false>;
   static std::atomic<unsigned long long> ready[2];  // devices set up, a bit each
   if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[swiglu], kLaunchRegisters)) != cudaSuccess) return e;
-  return launch_kernel(kernel, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p);
+  return launch_early(kernel, 1, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p);
 }
 
 }  // namespace ep

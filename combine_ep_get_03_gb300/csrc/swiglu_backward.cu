@@ -78,6 +78,7 @@ __device__ __forceinline__ uint4 quant16(const float2* x, float inv) {
 __global__ void __launch_bounds__(kSwigluBackwardThreads, 7) k_swiglu_backward(const SwigluBackwardArgs p) {
   extern __shared__ unsigned prefix[];
   __shared__ unsigned sums[32];
+  after_previous();
   groups_prefix(p.groups, 1, prefix, sums);
   const int lane = threadIdx.x & 31;
   const unsigned total = prefix[p.groups.G];

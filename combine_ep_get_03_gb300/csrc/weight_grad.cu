@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_fence();
   }
   if (warp == kMmaWarp) pair_tmem_alloc(&s.tmem, kTmemColumns);
+  after_previous();
   for (int g = threadIdx.x; g < p.groups.G; g += kThreads) {
     long long start;
     counts[g] = group_span(p.groups, g, &start, blockIdx.x == 0);
@@ -427,7 +428,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t st
   const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
                       sizeof(Shared) + sizeof(int) * p.groups.G;
   // pairs of blocks: an even number of SMs, two at least
-  return launch_pairs(k_weight_grad, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, p);
+  return launch_early(k_weight_grad, 2, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, p);
 }
 
 }  // namespace ep
