@@ -175,13 +175,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-      :
-      : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
 // One lane of a converged warp, the same one every time.  Code that only this
 // lane runs keeps its operands in uniform registers; behind a test of the lane
 // number the same MMAs cost about three times the issue time.
