@@ -227,8 +227,8 @@ ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* gr
 ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_t* grad_out, int N,
                                    const ep_fp8_rows_t* x, int K, void* grad_w, int num_sms, ep_stream_t stream) {
   if (!groups_ok(groups) || N < 128 || N % 128 != 0 || K < 128 || K % 128 != 0) return EP_ERR_INVALID_ARG;
-  if (static_cast<long long>(groups->num_groups) * (N / 128) * ((K + 255) / 256) > INT_MAX / 2 || !grad_w ||
-      !aligned(grad_w, 16))
+  if (static_cast<long long>(groups->num_groups) * (N / 128) * ((K + 255) / 256) > INT_MAX / 2 ||
+      static_cast<long long>(groups->num_groups) * N > INT_MAX || !grad_w || !aligned(grad_w, 16))
     return EP_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (groups->rows == 0)

@@ -18,6 +18,12 @@
 // ties by the first lane of a ballot.  Blocks join their sums as 64-bit fixed
 // point (2^-36), which makes the result independent of their order, and the
 // last block to finish writes counts, P and the loss: one launch.
+//
+// Bound by the half-rate integer and compare pipe (60 % busy forward): hence
+// keys sorted once per lane and shifted, one score kind per row, bf16 logits'
+// exact 32-bit keys.  32 768 tokens of 256 bf16 logits, top-8: 27 us forward,
+// 22 us backward (46 us the pair in a stream); one token 6 us, less than the
+// call's host side.
 #include <math_constants.h>
 
 #include "ep_internal.h"

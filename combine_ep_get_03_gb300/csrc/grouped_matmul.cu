@@ -14,9 +14,18 @@
 // to fp32 registers: 128 a thread.  The scales come with their operands: a
 // fourth warp copies a block's 130 numbers to shared memory, asynchronously,
 // so that the adding warps neither hold pointers nor wait for memory.  Each
-// accumulator has its own issuing warp:
-// a wait on a barrier that is already complete takes some 180 cycles here, two
-// of them and the issue 620, more than the 512 of a stage's MMAs.
+// accumulator has its own issuing warp: a wait on a barrier that is already
+// complete takes some 180 cycles here, two of them and the issue 620, more than
+// the 512 of a stage's MMAs.
+//
+// Many rows: a stage's 48 KB are written to shared memory once and read once,
+// some 750 cycles where the MMAs take 512 (without the loads the same kernel
+// does 3.3 PFLOP/s, without the sums 2.2); 32 768 rows, 7 168 -> 4 096: 905 us,
+// 2.1 PFLOP/s.  Few rows: the weights' stream; 32 experts of 2 048 -> 7 168 for
+// 1 024 rows 77 us, 6.3 TB/s, and one token's eight experts of 7 168 -> 4 096
+// 43 us, 5.4 TB/s (128 tiles on 152 SMs).  Pairs of blocks on a 256 x 256 tile
+// halve the columns' traffic but lengthen the accumulators' round trip: decode
+// 80 -> 113 us, prefill 900 -> 933 us, so blocks work alone.
 //
 // SwiGLU takes its 256 columns as gate 64, up 64, gate 64, up 64 so that a
 // thread holds gate and up of the same channel and the row's 128-channel
@@ -347,20 +356,32 @@ EncodeTiled encode_tiled() {
 
 }  // namespace
 
-cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows) {
+namespace {
+
+cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int width, long long rows,
+                     int planes, int box_rows) {
   EncodeTiled enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;
   const cuuint32_t rank = planes > 0 ? 3 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(planes > 0 ? planes : 1)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(width) * rows};
-  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width) * size, static_cast<cuuint64_t>(width) * size * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(map, type, rank, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, width, rows, planes, box_rows);
+}
+cudaError_t make_bf16_map(CUtensorMap* map, const void* base, int width, long long rows, int box_rows) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, width, rows, 0, box_rows);
 }
 
 cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream) {

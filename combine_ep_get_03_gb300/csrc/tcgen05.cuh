@@ -26,6 +26,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               :
+               : "l"(map), "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+
 // A 4-byte asynchronous copy, 0 instead where `on` is false (src is not read),
 // and an arrival on `bar` (counted in its expected arrivals) when this
 // thread's copies so far have landed.
@@ -39,6 +46,8 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
 // A tensor map over bytes [planes][rows][width] (2-D where planes is 0), box
 // 128 x box_rows, 128-byte swizzle.
 cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
+// The same over bf16 [rows][width], box 64 x box_rows.
+cudaError_t make_bf16_map(CUtensorMap* map, const void* base, int width, long long rows, int box_rows);
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" : : "l"(map) : "memory");

@@ -14,14 +14,20 @@
 // Shared memory is what bounds it: a widened 64-row stage is written once and
 // read once per MMA.  So two blocks on neighbouring SMs share a tile of 256 (n)
 // x 256 (k): each widens its 128 columns of dy and of x, 32 KB a stage instead
-// of the 48 KB of a 128 x 256 tile of its own, for the same MMA time.  Two warps
-// fetch e4m3 rows (TMA) and scales (asynchronous copies) four stages ahead,
-// across tiles; four teams of four warps take a stage each in turn, widen it
-// and store it with the 128-byte swizzle, rows along the long axis (both operands
-// "MN major", so nothing is transposed).  One warp of the first block issues
-// four MMAs a stage; four warps write the previous tile from the other TMEM
-// accumulator; one looks up the next tiles' largest scales.  Rows past the
-// group's end enter as zeros.
+// of the 48 KB of a 128 x 256 tile of its own, for the same MMA time.  Two
+// warps fetch e4m3 rows (TMA) and scales (asynchronous copies) four stages
+// ahead, across tiles; four teams of four warps take a stage each in turn,
+// widen it and store it with the 128-byte swizzle, rows along the long axis
+// (both operands "MN major", so nothing is transposed).  One warp of the first
+// block issues four MMAs a stage; four warps send the previous tile from the
+// other TMEM accumulator out through shared memory; one looks up the next
+// tiles' largest scales.  Rows past the group's end enter as zeros.
+//
+// 16 experts, 16 384 rows, 2 048 x 7 168: 382 us, 1.26 PFLOP/s; the load-store
+// pipe is busy 61 % of the cycles and the tensor cores' operand reads take
+// another 25 % of the same memory.  One block alone on 128 x 256: 614 us; rows
+// by plain loads instead of TMA: 464 us at best; 32-byte stores of the result
+// straight from registers: 410 us.
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "tcgen05.cuh"
@@ -38,6 +44,7 @@ constexpr int kRawStages = 4;  // as fetched; both a multiple of the teams: a st
 constexpr int kChunkBytes = kRows * 128;  // 64 columns of f16
 constexpr int kStageBytes = 2 * kOwn / 64 * kChunkBytes;
 constexpr int kRawBytes = 2 * kOwn * kRows, kScaleBytes = 2 * 4 * kRows;  // dy, x; their scales
+constexpr int kOutBytes = 32 * 128;  // 32 rows of 64 bf16
 constexpr int kTeams = 4, kTeamWarps = 4, kPass = 4 * kTeamWarps, kLoadWarps = kTeams * kTeamWarps, kStoreWarps = 4;
 constexpr int kMmaWarp = kLoadWarps + kStoreWarps, kScaleWarp = kMmaWarp + 1, kFetchWarp = kMmaWarp + 2;
 constexpr int kFetchWarps = 2;
@@ -151,11 +158,12 @@ __device__ __forceinline__ int exponent_of(float m) {
 
 __global__ void __launch_bounds__(kThreads, 1) 
     k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_dw,
                   const __grid_constant__ WeightGradArgs p) {
-  extern __shared__ unsigned char raw[];
-  unsigned char* stages = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) unsigned char stages[];
   unsigned char* raws = stages + kStages * kStageBytes;
-  unsigned char* raw_scales = raws + kRawStages * kRawBytes;
+  unsigned char* outs = raws + kRawStages * kRawBytes;  // what the storing warps have on its way out
+  unsigned char* raw_scales = outs + kStoreWarps * kOutBytes;
   Shared& s = *reinterpret_cast<Shared*>(raw_scales + kRawStages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* quit = &s.quit;
@@ -362,16 +370,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool wide = (reinterpret_cast<uintptr_t>(p.dw) & 31) == 0;
+    // 64 columns of the warp's 32 rows at a time go through shared memory, so
+    // that they leave as whole lines: 32-byte stores into 32 rows cost the
+    // load-store pipe, which bounds the widening, four times as much
+    unsigned char* out = outs + quarter * kOutBytes;
+    auto send = [&](const uint32_t* x, int column, int row) {
+      if (lane == 0) bulk_wait_read<0>();  // the 64 columns before have left
+      __syncwarp();
+      const uint32_t line = smem_u32(out) + lane * 128;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        sts128(line + ((u ^ (lane & 7)) << 4), x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&map_dw, out, column, row);
+        bulk_commit();
+      }
+    };
     uint32_t used = 0;
     for (; w.t < w.tiles; w.t += w.step) {
       w.set();
       const int n = w.n * kPair + rank * kOwn, k = w.k * kPair;
       const int columns = n < p.N ? min(kPair, p.K - k) : 0;
-      uint16_t* o = p.dw + (static_cast<long long>(w.group) * p.N + n + quarter * 32 + lane) * p.K + k;
+      const int row = w.group * p.N + n + quarter * 32;
+      uint32_t x[32];
       if (w.rows == 0) {
-        const uint32_t zero[8] = {};
-        for (int q = 0; q < columns; q += 16) store32(o + q, zero, wide);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = 0u;
+        for (int q = 0; q < columns; q += 64) send(x, k + q, row);
         continue;
       }
       const int ac = used & 1, e = used % kExponents;
@@ -381,32 +408,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_fence_after();
       const float up[2] = {power_of_two(s.exponent[e][0] + s.exponent[e][1]), power_of_two(s.exponent[e][0] + s.exponent[e][2])};
 #pragma unroll
-      for (int q = 0; q < kPair / 32; ++q) {
-        uint32_t v[32];
-        tmem_load32(lanes + ac * kPair + q * 32, v);
-        tmem_load_wait(v);
-        if (q == kPair / 32 - 1) {
+      for (int q = 0; q < kPair / 64; ++q) {
+        const float f = up[q >> 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+          tmem_load32(lanes + ac * kPair + q * 64 + h * 32, v);
+          tmem_load_wait(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            x[h * 16 + j] = pack_bf16x2(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
+        }
+        if (q == kPair / 64 - 1) {
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_first(&s.acc_empty[ac]);
         }
-        const float f = up[q >> 2];
-        if (q * 32 < columns) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              x[j] = pack_bf16x2(__uint_as_float(v[h * 16 + 2 * j]) * f, __uint_as_float(v[h * 16 + 2 * j + 1]) * f);
-            store32(o + q * 32 + h * 16, x, wide);
-          }
-        }
+        if (q * 64 < columns) send(x, k + q * 64, row);
       }
       // the exponents have been used, not only read
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.exp_empty[e]);
       ++used;
     }
+    if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
   tmem_fence_before();
@@ -419,16 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream) {
-  CUtensorMap map_dy, map_x;
+  CUtensorMap map_dy, map_x, map_dw;
   cudaError_t e = make_byte_map(&map_dy, p.dy.data, p.N, p.groups.rows, 0, kRows);
   if (e == cudaSuccess) e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, kRows);
+  if (e == cudaSuccess) e = make_bf16_map(&map_dw, p.dw, p.K, static_cast<long long>(p.groups.G) * p.N, 32);
   static std::atomic<unsigned long long> ready;  // devices set up, a bit each
   if (e == cudaSuccess) e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
   if (e != cudaSuccess) return e;
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
-                      sizeof(Shared) + sizeof(int) * p.groups.G;
+  const size_t smem = static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
+                      kStoreWarps * kOutBytes + sizeof(Shared) + sizeof(int) * p.groups.G;
   // pairs of blocks: an even number of SMs, two at least
-  return launch_early(k_weight_grad, 2, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, p);
+  return launch_early(k_weight_grad, 2, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, map_dw, p);
 }
 
 }  // namespace ep
