@@ -384,8 +384,11 @@ _IDS, _MASK = (torch.int64, torch.int32), (torch.bool, torch.uint8)
 
 def _dev_ptr(t, dtypes, name, dev):
     """Device pointer of a contiguous tensor on the current device."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and t.dtype in dtypes and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev and t.dtype in dtypes and t.is_contiguous():  # a CPU tensor's device is -1
+            return t.data_ptr()
+    except AttributeError:  # not a tensor: refused below
+        pass
     p = _ptr(t, dtypes, name)
     if p is None:
         raise ValueError(f"{name} is required")
@@ -467,24 +470,27 @@ def ep_gate_workspace_bytes(num_experts: int) -> int:
 
 def _logits(t, name, dev):
     """Pointer, type, row stride and shape of [T, E] logits; rows may be strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
-    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+    dtype, shape = t.dtype, t.shape
+    kind = EP_LOGITS_FP32 if dtype is torch.float32 else EP_LOGITS_BF16
+    if len(shape) != 2 or (kind == EP_LOGITS_BF16 and dtype is not torch.bfloat16):
         raise ValueError(f"{name} must be [T, E] fp32 or bf16")
-    T, E = t.shape
+    T, E = shape
     ld, step = t.stride()
     if T <= 1:
         ld = max(E, 1)
     if (step != 1 and E > 1 and T > 0) or ld < E:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), EP_LOGITS_FP32 if t.dtype == torch.float32 else EP_LOGITS_BF16, ld, T, E
+    return t.data_ptr(), kind, ld, T, E
 
 
 def _topk(topk_idx, T, dev):
     p = _dev_ptr(topk_idx, _IDS, "topk_idx", dev)
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx must be [{T}, k], got {list(topk_idx.shape)}")
-    return p, 64 if topk_idx.dtype == torch.int64 else 32, topk_idx.shape[1]
+    shape = topk_idx.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k], got {list(shape)}")
+    return p, 64 if topk_idx.dtype is torch.int64 else 32, shape[1]
 
 
 def ep_gate_forward(logits, topk_idx, topk_weights, expert_count, expert_prob, loss, workspace,

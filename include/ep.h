@@ -414,7 +414,8 @@ ep_status_t ep_check_wait_timeout(ep_handle_t h, ep_stream_t stream);
  * computation on the rows that dispatch leaves.  These calls need no handle
  * and allocate nothing; they run on the current device and work on whatever
  * layout the groups describe.  Sums, softmax statistics and norms are held
- * in fp32.
+ * in fp32.  Their kernels may start their own preparations while the stream's
+ * previous kernel ends; they wait for its results before they read any input.
  * --------------------------------------------------------------------- */
 
 /* Groups of rows, one group per expert.
@@ -531,7 +532,8 @@ ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* gr
 /* Gradient of the experts' weights from 8-bit rows: grad_w[e][n][k] = sum over
  * the rows r of group e of grad_out[r][n] x[r][k], dequantised, rounded once to
  * bf16 (dev [num_groups][N][K], 16-byte aligned; 0 for an empty group).
- * N and K are multiples of 128. */
+ * N and K are multiples of 128.  Runs on pairs of SMs: num_sms is rounded down
+ * to an even number, two at least. */
 ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_t* grad_out, int N,
                                    const ep_fp8_rows_t* x, int K, void* grad_w, int num_sms, ep_stream_t stream);
 
