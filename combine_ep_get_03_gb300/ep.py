@@ -406,51 +406,63 @@ def _optional(t, n, dtypes, name, dev):
     return None if t is None else _vector(t, n, dtypes, name, dev)
 
 
-def _fp8_rows(data, scales, lead, name, dev):
-    """ep_fp8_rows_t of a row buffer with the leading dimensions `lead`, and its width."""
+# `lay` below is the layout of a call's row buffers, (dimensions, first
+# dimension, M or 0), as _groups finds it in the first of them.
+
+def _groups(rows_like, group_count, group_offset, device_status, name, dev):
+    """ep_groups_t of a row buffer, its number of groups, rows and layout."""
+    if not isinstance(rows_like, torch.Tensor):
+        raise ValueError(f"{name} must be a [rows, width] or [E, M, width] tensor")
+    shape = rows_like.shape
+    nd = len(shape)
+    cp = _dev_ptr(group_count, _I32, "group_count", dev)
+    E = group_count.numel()
+    if nd == 2:
+        if group_offset is None:
+            raise ValueError("expert-major rows need group_offset: the first row of each group")
+        op, rows, per = _vector(group_offset, E, _I32, "group_offset", dev), shape[0], 0
+    elif nd == 3:
+        if group_offset is not None:
+            raise ValueError("low-latency rows [E, M, width] take no group_offset")
+        if shape[0] != E:
+            raise ValueError(f"{name} holds {shape[0]} groups, group_count {E}")
+        op, per = 0, shape[1]
+        rows = E * per
+    else:
+        raise ValueError(f"{name} must be [rows, width] or [E, M, width], got {list(shape)}")
+    st = 0 if device_status is None else _vector(device_status, 1, _I32, "device_status", dev)
+    return _GROUPS.pack(cp, op, E, rows, per, st), E, rows, (nd, shape[0], per)
+
+
+def _width(shape, lay, name):
+    """Width of a row buffer that must have the call's layout."""
+    nd, first, per = lay
+    if len(shape) != nd or shape[0] != first or (nd == 3 and shape[1] != per) or shape[-1] == 0:
+        lead = [first] if nd == 2 else [first, per]
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, width], got {list(shape)}")
+    return shape[-1]
+
+
+def _fp8_rows(data, scales, lay, name, dev):
+    """ep_fp8_rows_t of a row buffer with its scales, and its width."""
     p = _dev_ptr(data, _FP8_BYTES, name, dev)
-    shape = data.shape
-    width = shape[-1] if shape else 0
-    if shape[:-1] != lead or width == 0 or width % 128:
-        raise ValueError(f"{name} must be {list(lead)} rows of a positive multiple of 128, got {list(shape)}")
+    width = _width(data.shape, lay, name)
+    if width & 127:
+        raise ValueError(f"{name}'s width must be a multiple of 128, got {width}")
     sp = _dev_ptr(scales, _F32, f"{name}_scales", dev)
     g, have = width >> 7, scales.shape
-    if len(lead) == 1:
-        if len(have) != 2 or have[0] != g or have[1] < lead[0]:
-            raise ValueError(f"{name}_scales must be [{g}, ld >= {lead[0]}] for expert-major rows, got {list(have)}")
+    nd, first, per = lay
+    if nd == 2:
+        if len(have) != 2 or have[0] != g or have[1] < first:
+            raise ValueError(f"{name}_scales must be [{g}, ld >= {first}] for expert-major rows, got {list(have)}")
         return _FP8_ROWS.pack(p, sp, 1, have[1]), width
-    if have != (lead[0], lead[1], g):
-        raise ValueError(f"{name}_scales must be {[*lead, g]} for low-latency rows, got {list(have)}")
+    if have != (first, per, g):
+        raise ValueError(f"{name}_scales must be {[first, per, g]} for low-latency rows, got {list(have)}")
     return _FP8_ROWS.pack(p, sp, g, 1), width
 
 
-def _groups(rows_like, group_count, group_offset, device_status, name, dev):
-    """ep_groups_t of a row buffer, its number of groups, rows and leading dimensions."""
-    if not isinstance(rows_like, torch.Tensor) or rows_like.dim() not in (2, 3):
-        raise ValueError(f"{name} must be a [rows, width] or [E, M, width] tensor")
-    lead = rows_like.shape[:-1]
-    cp = _dev_ptr(group_count, _I32, "group_count", dev)
-    E = group_count.numel()
-    if len(lead) == 1:
-        if group_offset is None:
-            raise ValueError("expert-major rows need group_offset: the first row of each group")
-        op, rows, per = _vector(group_offset, E, _I32, "group_offset", dev), lead[0], 0
-    else:
-        if group_offset is not None:
-            raise ValueError("low-latency rows [E, M, width] take no group_offset")
-        if lead[0] != E:
-            raise ValueError(f"{name} holds {lead[0]} groups, group_count {E}")
-        op, per = 0, lead[1]
-        rows = E * per
-    st = _optional(device_status, 1, _I32, "device_status", dev)
-    return _GROUPS.pack(cp, op, E, rows, per, st or 0), E, rows, lead
-
-
-def _bf16_rows(t, lead, name, dev):
-    p = _dev_ptr(t, _BF16, name, dev)
-    if t.shape[:-1] != lead or t.shape[-1] == 0:
-        raise ValueError(f"{name} must be {list(lead)} rows, got {list(t.shape)}")
-    return p, t.shape[-1]
+def _bf16_rows(t, lay, name, dev):
+    return _dev_ptr(t, _BF16, name, dev), _width(t.shape, lay, name)
 
 
 def _expert_weights(w, w_scales, E, N, K, dev):
@@ -460,6 +472,10 @@ def _expert_weights(w, w_scales, E, N, K, dev):
     if w_scales.shape != (E, (N + 127) >> 7, K >> 7):
         raise ValueError(f"w_scales must be [{E}, {(N + 127) >> 7}, {K >> 7}], got {list(w_scales.shape)}")
     return wp, sp
+
+
+def _stream_on(stream, dev):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def ep_gate_workspace_bytes(num_experts: int) -> int:
@@ -509,7 +525,7 @@ def ep_gate_forward(logits, topk_idx, topk_weights, expert_count, expert_prob, l
         loss_coef, ip, bits, _vector(topk_weights, T * k, _F32, "topk_weights", dev),
         _vector(expert_count, E + 1, _I32, "expert_count", dev), _vector(expert_prob, E, _F32, "expert_prob", dev),
         _vector(loss, 1, _F32, "loss", dev), _dev_ptr(workspace, (workspace.dtype,), "workspace", dev), num_sms,
-        _stream(stream)), "ep_gate_forward")
+        _stream_on(stream, dev)), "ep_gate_forward")
 
 
 def ep_gate_backward(logits, topk_idx, expert_count, grad_topk_weights, grad_loss, grad_logits,
@@ -527,7 +543,7 @@ def ep_gate_backward(logits, topk_idx, expert_count, grad_topk_weights, grad_los
         lp, lt, ld, _optional(token_mask, T, _MASK, "token_mask", dev), T, E, k, score, loss_coef, ip, bits,
         _vector(expert_count, E + 1, _I32, "expert_count", dev),
         _optional(grad_topk_weights, T * k, _F32, "grad_topk_weights", dev),
-        _optional(grad_loss, 1, _F32, "grad_loss", dev), gp, gld, num_sms, _stream(stream)), "ep_gate_backward")
+        _optional(grad_loss, 1, _F32, "grad_loss", dev), gp, gld, num_sms, _stream_on(stream, dev)), "ep_gate_backward")
 
 
 def ep_grouped_matmul(x, x_scales, w, w_scales, out, group_count, group_offset=None, device_status=None,
@@ -535,11 +551,11 @@ def ep_grouped_matmul(x, x_scales, w, w_scales, out, group_count, group_offset=N
     """out = x @ w[e].T for the rows of every group: e4m3 x and w [E, N, K]
     with 128-channel and 128 x 128 scales, bf16 out."""
     dev = torch.cuda.current_device()
-    g, E, _, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
-    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
-    op, N = _bf16_rows(out, lead, "out", dev)
+    g, E, _, lay = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lay, "x", dev)
+    op, N = _bf16_rows(out, lay, "out", dev)
     wp, sp = _expert_weights(w, w_scales, E, N, K, dev)
-    _check(lib().ep_grouped_matmul(g, xr, wp, sp, N, K, op, num_sms, _stream(stream)), "ep_grouped_matmul")
+    _check(lib().ep_grouped_matmul(g, xr, wp, sp, N, K, op, num_sms, _stream_on(stream, dev)), "ep_grouped_matmul")
 
 
 def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_count, group_offset=None,
@@ -548,17 +564,17 @@ def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_co
     """act = row_weights * silu(gate) * up in e4m3 with scales, where (gate, up)
     = x @ w[e].T, w [E, 2F, K]; pre (optional) keeps (gate, up) in e4m3."""
     dev = torch.cuda.current_device()
-    g, E, rows, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
-    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
-    ar, F = _fp8_rows(act, act_scales, lead, "act", dev)
+    g, E, rows, lay = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lay, "x", dev)
+    ar, F = _fp8_rows(act, act_scales, lay, "act", dev)
     pr = None
     if pre is not None:
-        pr, two = _fp8_rows(pre, pre_scales, lead, "pre", dev)
+        pr, two = _fp8_rows(pre, pre_scales, lay, "pre", dev)
         if two != 2 * F:
             raise ValueError(f"pre must be {2 * F} wide, got {two}")
     wp, sp = _expert_weights(w, w_scales, E, 2 * F, K, dev)
     _check(lib().ep_grouped_matmul_swiglu(g, xr, wp, sp, F, K, _optional(row_weights, rows, _F32, "row_weights", dev),
-                                          ar, pr, num_sms, _stream(stream)), "ep_grouped_matmul_swiglu")
+                                          ar, pr, num_sms, _stream_on(stream, dev)), "ep_grouped_matmul_swiglu")
 
 
 def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, group_count, group_offset=None,
@@ -567,15 +583,15 @@ def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_sca
     """Gradient of the pre-activations (e4m3 with scales) and of the row
     weights, from grad_act (bf16) and the 8-bit pre-activations."""
     dev = torch.cuda.current_device()
-    g, _, rows, lead = _groups(grad_act, group_count, group_offset, device_status, "grad_act", dev)
-    dp, F = _bf16_rows(grad_act, lead, "grad_act", dev)
-    pr, two = _fp8_rows(pre, pre_scales, lead, "pre", dev)
-    gr, two_out = _fp8_rows(grad_pre, grad_pre_scales, lead, "grad_pre", dev)
+    g, _, rows, lay = _groups(grad_act, group_count, group_offset, device_status, "grad_act", dev)
+    dp, F = _bf16_rows(grad_act, lay, "grad_act", dev)
+    pr, two = _fp8_rows(pre, pre_scales, lay, "pre", dev)
+    gr, two_out = _fp8_rows(grad_pre, grad_pre_scales, lay, "grad_pre", dev)
     if two != 2 * F or two_out != 2 * F:
         raise ValueError(f"pre and grad_pre must be {2 * F} wide, got {two} and {two_out}")
     _check(lib().ep_grouped_swiglu_backward(
         g, dp, pr, _optional(row_weights, rows, _F32, "row_weights", dev), F, gr,
-        _optional(grad_row_weights, rows, _F32, "grad_row_weights", dev), num_sms, _stream(stream)),
+        _optional(grad_row_weights, rows, _F32, "grad_row_weights", dev), num_sms, _stream_on(stream, dev)),
         "ep_grouped_swiglu_backward")
 
 
@@ -584,13 +600,13 @@ def ep_grouped_weight_grad(grad_out, grad_out_scales, x, x_scales, grad_w, group
     """grad_w[e] = grad_out.T @ x over the rows of group e, both e4m3 with
     scales; bf16 [E, N, K]."""
     dev = torch.cuda.current_device()
-    g, E, _, lead = _groups(x, group_count, group_offset, device_status, "x", dev)
-    yr, N = _fp8_rows(grad_out, grad_out_scales, lead, "grad_out", dev)
-    xr, K = _fp8_rows(x, x_scales, lead, "x", dev)
+    g, E, _, lay = _groups(x, group_count, group_offset, device_status, "x", dev)
+    yr, N = _fp8_rows(grad_out, grad_out_scales, lay, "grad_out", dev)
+    xr, K = _fp8_rows(x, x_scales, lay, "x", dev)
     gp = _dev_ptr(grad_w, _BF16, "grad_w", dev)
     if grad_w.shape != (E, N, K):
         raise ValueError(f"grad_w must be [{E}, {N}, {K}], got {list(grad_w.shape)}")
-    _check(lib().ep_grouped_weight_grad(g, yr, N, xr, K, gp, num_sms, _stream(stream)), "ep_grouped_weight_grad")
+    _check(lib().ep_grouped_weight_grad(g, yr, N, xr, K, gp, num_sms, _stream_on(stream, dev)), "ep_grouped_weight_grad")
 
 
 class Handle:
