@@ -25,7 +25,7 @@ constexpr int kSwigluBackwardThreads = 128;
 namespace {
 
 // Two fp32 operations an instruction: the kernel is bound by issue before
-// memory, 39 instructions a channel without them and 22 with.
+// memory, at 28 instructions a channel (counted on the device).
 __device__ __forceinline__ uint64_t bits(float2 v) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
