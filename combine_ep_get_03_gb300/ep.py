@@ -619,6 +619,7 @@ class Handle:
         self.T = None      # tokens of the last layout
         self.T_ll = None   # tokens of the last low-latency dispatch
         self.T_em = None   # tokens of the last expert-major layout
+        self.em_layouts = 0  # expert-major layouts so far: tells whether the last one is still a caller's own
         self.ptr = ep_handle_create(num_ranks, num_experts, num_topk, hidden, max_tokens_per_rank)
 
     @property
@@ -788,6 +789,7 @@ class Handle:
         ep_em_layout_and_dispatch(self.ptr, topk_idx, x, topk_weights, dtype, expert_alignment, recv_x, recv_scales,
                                   recv_src_idx, recv_weights, num_sms, stream)
         self.T_em = T
+        self.em_layouts += 1
 
     def em_dispatch(self, x, topk_weights, dtype, recv_x, recv_scales=None, recv_src_idx=None, recv_weights=None,
                     num_sms=0, stream=None):

@@ -53,9 +53,11 @@ class ExpertWeights:
 
 
 class MoELayer:
-    """hidden and ffn are multiples of 128.  Buffers are sized once for
-    max_tokens_per_rank; the outputs of forward and backward are overwritten by
-    the next call of the same kind."""
+    """hidden and ffn are multiples of 128.  Every output is a tensor of its
+    own, and what forward saves is all that its backward needs: other forwards
+    and decodes may come between, and backward calls in any order.  The handle
+    and the gate's workspace are the layer's, so its calls go to one stream at a
+    time."""
 
     def __init__(self, num_ranks, num_experts, num_topk, hidden, ffn, max_tokens_per_rank, score=ep.EP_GATE_SOFTMAX,
                  num_groups=1, topk_groups=1, loss_coef=1e-2, expert_alignment=128, device="cuda"):
@@ -69,8 +71,6 @@ class MoELayer:
                                              ep.EP_FP8_E4M3, ep.EP_LAYOUT_EXPERT_MAJOR, expert_alignment)
         self.rows, self.ld = rows, (rows + 3) // 4 * 4
         self.workspace = torch.zeros(ep.ep_gate_workspace_bytes(num_experts), dtype=torch.uint8, device=self.dev)
-        self.offset = torch.empty(num_experts + 1, dtype=torch.int32, device=self.dev)
-        self.count = torch.empty(num_experts, dtype=torch.int32, device=self.dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.dev)
 
     def close(self):
@@ -86,15 +86,15 @@ class MoELayer:
     def _bf16(self, *shape):
         return torch.empty(shape, dtype=torch.bfloat16, device=self.dev)
 
-    def _groups(self):
-        return dict(group_count=self.count, group_offset=self.offset, device_status=self.status)
+    def _i32(self, n):
+        return torch.empty(n, dtype=torch.int32, device=self.dev)
 
     def route(self, logits, token_mask=None):
         """Gate of logits [T, E]: (topk_idx, topk_weights, expert_count, loss)."""
         T = logits.shape[0]
         idx = torch.empty((T, self.k), dtype=torch.int64, device=self.dev)
         w, prob, loss = self._f32(T, self.k), self._f32(self.E), self._f32(1)
-        count = torch.empty(self.E + 1, dtype=torch.int32, device=self.dev)
+        count = self._i32(self.E + 1)
         ep.ep_gate_forward(logits, idx, w, count, prob, loss, self.workspace, token_mask=token_mask, **self.gate,
                            **self.limit)
         return idx, w, count, loss
@@ -107,35 +107,41 @@ class MoELayer:
         xq, xs = self._fp8(self.H)
         row_w = self._f32(self.rows)
         self.h.em_layout_and_dispatch(idx, x, w, ep.EP_FP8_E4M3, self.align, xq, xs, recv_weights=row_w)
-        self.h.em_get_groups(self.offset, self.count)
+        offset, rows = self._i32(self.E + 1), self._i32(self.E)
+        self.h.em_get_groups(offset, rows)
+        groups = dict(group_count=rows, group_offset=offset, device_status=self.status)
         act, act_s = self._fp8(self.F)
         pre, pre_s = self._fp8(2 * self.F)
         ep.ep_grouped_matmul_swiglu(xq, xs, w1.q, w1.s, act, act_s, row_weights=row_w, pre=pre, pre_scales=pre_s,
-                                    **self._groups())
+                                    **groups)
         y = self._bf16(self.rows, self.H)
-        ep.ep_grouped_matmul(act, act_s, w2.q, w2.s, y, **self._groups())
+        ep.ep_grouped_matmul(act, act_s, w2.q, w2.s, y, **groups)
         out = self._bf16(T, self.H)
         self.h.em_combine(y, out)
-        return out, loss, (logits, token_mask, idx, count, xq, xs, row_w, act, act_s, pre, pre_s)
+        return out, loss, (logits, token_mask, idx, count, self.h.em_layouts, groups, xq, xs, row_w, act, act_s, pre,
+                           pre_s)
 
     def backward(self, grad_out, grad_loss, saved, w1: ExpertWeights, w2: ExpertWeights):
         """-> (grad_x bf16 [T, H], grad_logits, grad_w1, grad_w2 bf16)."""
-        logits, token_mask, idx, count, xq, xs, row_w, act, act_s, pre, pre_s = saved
+        logits, token_mask, idx, count, layout, groups, xq, xs, row_w, act, act_s, pre, pre_s = saved
         T = grad_out.shape[0]
         gy, gy_s = self._fp8(self.H)
-        self.h.em_dispatch(grad_out, None, ep.EP_FP8_E4M3, gy, gy_s)
+        if self.h.em_layouts == layout:
+            self.h.em_dispatch(grad_out, None, ep.EP_FP8_E4M3, gy, gy_s)
+        else:  # another forward came between: the same ids give the same rows again
+            self.h.em_layout_and_dispatch(idx, grad_out, None, ep.EP_FP8_E4M3, self.align, gy, gy_s)
         grad_w2 = self._bf16(self.E, self.H, self.F)
-        ep.ep_grouped_weight_grad(gy, gy_s, act, act_s, grad_w2, **self._groups())
+        ep.ep_grouped_weight_grad(gy, gy_s, act, act_s, grad_w2, **groups)
         grad_act = self._bf16(self.rows, self.F)
-        ep.ep_grouped_matmul(gy, gy_s, w2.qt, w2.st, grad_act, **self._groups())
+        ep.ep_grouped_matmul(gy, gy_s, w2.qt, w2.st, grad_act, **groups)
         gp, gp_s = self._fp8(2 * self.F)
         grad_row_w = self._f32(self.rows)
         ep.ep_grouped_swiglu_backward(grad_act, pre, pre_s, gp, gp_s, row_weights=row_w,
-                                      grad_row_weights=grad_row_w, **self._groups())
+                                      grad_row_weights=grad_row_w, **groups)
         grad_w1 = self._bf16(self.E, 2 * self.F, self.H)
-        ep.ep_grouped_weight_grad(gp, gp_s, xq, xs, grad_w1, **self._groups())
+        ep.ep_grouped_weight_grad(gp, gp_s, xq, xs, grad_w1, **groups)
         grad_rows = self._bf16(self.rows, self.H)
-        ep.ep_grouped_matmul(gp, gp_s, w1.qt, w1.st, grad_rows, **self._groups())
+        ep.ep_grouped_matmul(gp, gp_s, w1.qt, w1.st, grad_rows, **groups)
         grad_x = self._bf16(T, self.H)
         self.h.em_combine(grad_rows, grad_x)
         grad_w = self._f32(T, self.k)
@@ -150,11 +156,12 @@ class MoELayer:
         idx, w, _, _ = self.route(logits, token_mask)
         f8 = lambda width: torch.empty((E, M, width), dtype=torch.float8_e4m3fn, device=self.dev)  # noqa: E731
         xq, xs = f8(self.H), self._f32(E, M, self.H // 128)
-        self.h.low_latency_dispatch(x, idx, ep.EP_FP8_E4M3, xq, xs, recv_count=self.count)
+        count = self._i32(E)
+        self.h.low_latency_dispatch(x, idx, ep.EP_FP8_E4M3, xq, xs, recv_count=count)
         act, act_s = f8(self.F), self._f32(E, M, self.F // 128)
-        ep.ep_grouped_matmul_swiglu(xq, xs, w1.q, w1.s, act, act_s, self.count, device_status=self.status)
+        ep.ep_grouped_matmul_swiglu(xq, xs, w1.q, w1.s, act, act_s, count, device_status=self.status)
         y = self._bf16(E, M, self.H)
-        ep.ep_grouped_matmul(act, act_s, w2.q, w2.s, y, self.count, device_status=self.status)
+        ep.ep_grouped_matmul(act, act_s, w2.q, w2.s, y, count, device_status=self.status)
         out = self._bf16(T, self.H)
         self.h.low_latency_combine(y, w, out)
         return out
