@@ -62,14 +62,18 @@ __device__ __forceinline__ int group_span(const GroupArgs& a, int g, long long* 
 }
 
 // prefix[g] = tiles of `tile_rows` rows in the groups before g, prefix[G] =
-// all of them (saturating), for the whole block; `sums` holds 32 words.
+// all of them, for the whole block; `sums` holds 32 words.  Groups that do not
+// overlap have rows / tile_rows + G tiles at most; counts that say more are cut
+// there (EP_ERR_CAPACITY), which also keeps prefix[G] times the column tiles,
+// bounded by the host for that many, within 32 bits.
 __device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows, unsigned* prefix, unsigned* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int per = (a.G + blockDim.x - 1) / blockDim.x;
   const int g0 = tid * per;
-  auto add = [](unsigned x, unsigned y) {
+  const unsigned most = static_cast<unsigned>(a.rows / tile_rows) + a.G;
+  auto add = [most](unsigned x, unsigned y) {
     const unsigned s = x + y;
-    return s < x || s > 0x7fffffffu ? 0x7fffffffu : s;
+    return s < x || s > most ? most + 1 : s;
   };
   unsigned mine = 0;
   for (int g = g0; g < g0 + per && g < a.G; ++g) {
@@ -99,7 +103,10 @@ __device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows,
     prefix[g] = before;
     before = add(before, t);
   }
-  if (tid == 0) prefix[a.G] = all;
+  if (tid == 0) {
+    prefix[a.G] = all;
+    if (all > most && blockIdx.x == 0) latch_status(a.err, kErrCapacity);
+  }
   __syncthreads();
 }
 

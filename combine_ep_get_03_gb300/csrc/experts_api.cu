@@ -37,9 +37,10 @@ bool groups_ok(const ep_groups_t* g) {
                        g->rows_per_group * g->num_groups <= g->rows);
 }
 
-// Tiles of a product over `rows` rows are counted in 32 bits.
+// Tiles of a product over `rows` rows are counted in 32 bits (one more than
+// the groups can have where counts overlap).
 bool tiles_ok(const ep_groups_t* g, int N) {
-  return (g->rows / 128 + g->num_groups) * ((N + 127) / 128) < INT_MAX / 2;
+  return (g->rows / 128 + g->num_groups + 1) * ((N + 127) / 128) < INT_MAX / 2;
 }
 
 ep::GroupArgs groups_of(const ep_groups_t* g) {

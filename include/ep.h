@@ -425,7 +425,10 @@ ep_status_t ep_check_wait_timeout(ep_handle_t h, ep_stream_t stream);
  * Rows outside every group are neither read into a result nor written.  A
  * group that does not fit its rows_per_group slots or the `rows` of the
  * buffers is cut to what does, and EP_ERR_CAPACITY is latched in *status.
- * Groups must not overlap. */
+ * Groups must not overlap: which of two groups' results a row that both hold
+ * gets is not defined, and counts that add up to more tiles of 128 rows than
+ * the buffers have are cut there, with EP_ERR_CAPACITY, by every call that
+ * writes rows. */
 typedef struct {
   const int* count;       /* dev int32 [num_groups]                                  */
   const int* offset;      /* dev int32 [num_groups]: first row of a group, or NULL   */
