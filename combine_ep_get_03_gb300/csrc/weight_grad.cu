@@ -59,6 +59,10 @@ struct Shared {
   int quit;
   int exponent[kExponents][3];  // of the block's dy, of both halves of x
 };
+// Shared memory without the groups' counts, which follow it: 4096 of them fit.
+constexpr size_t kSharedBytes = static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
+                                kStoreWarps * kOutBytes + sizeof(Shared);
+static_assert(kSharedBytes + sizeof(int) * kMaxGroups <= 227 * 1024, "");
 
 // The pair's tiles that have rows, one after another.
 struct Walk {
@@ -451,8 +455,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t st
   static std::atomic<unsigned long long> ready;  // devices set up, a bit each
   if (e == cudaSuccess) e = set_up_kernel(reinterpret_cast<const void*>(k_weight_grad), ready, 0);
   if (e != cudaSuccess) return e;
-  const size_t smem = static_cast<size_t>(kStages) * kStageBytes + kRawStages * (kRawBytes + kScaleBytes) +
-                      kStoreWarps * kOutBytes + sizeof(Shared) + sizeof(int) * p.groups.G;
+  const size_t smem = kSharedBytes + sizeof(int) * p.groups.G;
   // pairs of blocks: an even number of SMs, two at least
   return launch_early(k_weight_grad, 2, dim3(sms < 2 ? 2 : sms & ~1), dim3(kThreads), smem, stream, map_dy, map_x, map_dw, p);
 }

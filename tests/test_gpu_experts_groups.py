@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from combine_ep_get_03_gb300 import ep
-from test_gpu_experts import DEV, Rows, gen, product64, quantize, sum_err, weights, within
+from test_gpu_experts import DEV, Rows, check8, gen, product64, quantize, silu64, sum_err, weights, within
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,51 @@ def test_full_groups_side_by_side_are_not_overlapping():
         y, mag = product64(r, x, w)
         within(r.read16(out), y, y.abs() * 2.0 ** -8 + sum_err(128) * mag, "product")
         assert int(status) == ep.EP_OK
+
+
+@pytest.mark.parametrize("layout", ["em", "ll"])
+@pytest.mark.parametrize("G", [2718, 2719, 4096])
+def test_as_many_groups_as_the_header_allows(G, layout):
+    """Up to 4096 groups, most of them small, some empty, the last one not."""
+    N = K = 128
+    counts = torch.randint(0, 4, (G,), generator=torch.Generator().manual_seed(G)).tolist()
+    counts[5], counts[-1] = 70, 2
+    r = Rows(counts, layout, 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = r.args(device_status=status)
+    xq, xs, x = r.fp8(K, 5)
+    yq, ys, y = r.fp8(N, 6, sigma=1e-2)
+
+    dw = torch.full((G, N, K), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ep.ep_grouped_weight_grad(yq, ys, xq, xs, dw, **args)
+    group = torch.repeat_interleave(torch.arange(G, device=DEV), r.count)
+    slot = torch.cat([torch.arange(c) for c in counts]).to(DEV)
+    py, px = (torch.zeros((G, max(counts), N), dtype=torch.float64, device=DEV) for _ in range(2))
+    py[group, slot], px[group, slot] = y, x
+    ref, mag = py.transpose(1, 2) @ px, py.abs().transpose(1, 2) @ px.abs()
+    within(dw.double(), ref, ref.abs() * 2.0 ** -8 + mag * 2.0 ** -8.9, "weight gradient")
+
+    q, s, w = weights(G, 2 * N, K, 7)
+    out = r.out16(2 * N)
+    ep.ep_grouped_matmul(xq, xs, q, s, out, **args)
+    p, pmag = product64(r, x, w)
+    within(r.read16(out), p, p.abs() * 2.0 ** -8 + sum_err(K) * pmag, "product")
+
+    act, acts = r.out8(N)
+    ep.ep_grouped_matmul_swiglu(xq, xs, q, s, act, acts, **args)
+    (g, u), (eg, eu) = p.chunk(2, 1), (sum_err(K) * pmag).chunk(2, 1)
+    a = silu64(g) * u
+    ea = (1.1 * eg) * u.abs() + (silu64(g).abs() + 1.1 * eg) * eu + (16 + 2 * g.abs()) * 2.0 ** -24 * a.abs()
+    check8(*r.read8(act, acts), a, ea, "activations")
+
+    pq, ps, pre = r.fp8(2 * N, 8, sigma=2.0)
+    d = torch.zeros((r.rows, N), dtype=torch.bfloat16, device=DEV)
+    d[r.live] = torch.randn((len(r.live), N), generator=gen(9), device=DEV).bfloat16()
+    dp, dps = r.out8(2 * N)
+    ep.ep_grouped_swiglu_backward(d.view(r.lead + (N,)), pq, ps, dp, dps, **args)
+    (g, u), d = pre.chunk(2, 1), d[r.live].double()
+    sg = torch.sigmoid(g)
+    grad = torch.cat([d * u * sg * (1 + g * (1 - sg)), d * silu64(g)], 1)
+    eg = torch.cat([(d * u).abs() * sg * (1 + g.abs() + silu64(g).abs()), (d * silu64(g)).abs()], 1)
+    check8(*r.read8(dp, dps), grad, eg * (16 + 2 * g.abs().repeat(1, 2)) * 2.0 ** -24, "gradient")
+    assert int(status) == ep.EP_OK
