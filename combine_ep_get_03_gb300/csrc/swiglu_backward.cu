@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(kSwigluBackwardThreads, 7) k_swiglu_backward(c
           const float2 silu = mul2(gate, s);
           du[j] = mul2(d, silu);
           dw = fma2(du[j], up, dw);
-          // s (1 + g (1 - s)) = s (1 + g - silu)
-          dg[j] = mul2(mul2(d, mul2(up, s)), fma2(silu, minus, add2(gate, one)));
+          // s (1 + g (1 - s)): beyond g = 17 s is 1, so the product is 0 however large g is
+          // (1 + g - silu would be 0 from 2^24 on)
+          dg[j] = mul2(mul2(d, mul2(up, s)), fma2(gate, fma2(s, minus, one), one));
           ag = fmaxf(ag, fmaxf(fabsf(dg[j].x), fabsf(dg[j].y)));
           au = fmaxf(au, fmaxf(fabsf(du[j].x), fabsf(du[j].y)));
         }
