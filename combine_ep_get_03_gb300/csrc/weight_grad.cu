@@ -3,13 +3,17 @@
 // both e4m3 with a scale for every 128 channels of a row.
 //
 // The contraction runs over rows, and both scales change with the row, so they
-// cannot be taken out of the sum: the operands are widened to f16 on the way
-// to shared memory, multiplied by their scales, and go through f16
+// cannot be taken out of the sum: the operands are multiplied by their scales
+// in fp32 on the way to shared memory, rounded once to f16, and go through f16
 // tensor-core instructions with fp32 accumulation.  The scales of an operand's
 // 128 channels are first divided by the power of two that brings the largest
 // of the group's rows to [64, 128) (448 x 128 still fits f16), which is put
-// back on the sums; rows whose scale is 2^-21 of the largest or more keep 11
-// bits.  Two roundings to 11 bits are an eighth of the bf16 result's own.
+// back on the sums.  So a term is off by 2^-10 of itself, a quarter of the bf16
+// result's own 2^-8, as long as both values are 2^-28 of their channels' largest
+// possible (448 times that scale) or more; f16's subnormal step is 2^-39 of it.
+// bf16 operands would keep any range but round to 2^-8 each.  Scale and product
+// both rounded to f16 (no fp32 arithmetic) 386 us, this 413; a scale split in
+// two f16 numbers 412, and with the range above 418.
 //
 // Shared memory is what bounds it: a widened 64-row stage is written once and
 // read once per MMA.  So two blocks on neighbouring SMs share a tile of 256 (n)
@@ -23,7 +27,7 @@
 // other TMEM accumulator out through shared memory; one looks up the next
 // tiles' largest scales.  Rows past the group's end enter as zeros.
 //
-// 16 experts, 16 384 rows, 2 048 x 7 168: 382 us, 1.26 PFLOP/s; the load-store
+// 16 experts, 16 384 rows, 2 048 x 7 168: 413 us, 1.17 PFLOP/s; the load-store
 // pipe is busy 61 % of the cycles and the tensor cores' operand reads take
 // another 25 % of the same memory.  One block alone on 128 x 256: 614 us; rows
 // by plain loads instead of TMA: 464 us at best; 32-byte stores of the result
@@ -120,15 +124,13 @@ struct Cursor {
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
-// Four e4m3 codes as two f16 pairs (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(*lo), "=r"(*hi)
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+// Two products as f16, rounded once (the products in fp32, one instruction for both).
+__device__ __forceinline__ uint32_t scaled_f16x2(float a, float b, float scale) {
   uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("{\n .reg .b64 t, u;\n .reg .f32 x, y;\n mov.b64 t, {%1, %2};\n mov.b64 u, {%3, %3};\n mul.rn.f32x2 t, t, u;\n"
+      " mov.b64 {x, y}, t;\n cvt.rn.f16x2.f32 %0, y, x;\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(scale));
   return r;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -138,14 +140,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // 16 codes times their scale, as f16 at the two shared-memory addresses of
 // their 16-byte units.
 __device__ __forceinline__ void store_chunk(uint32_t lo, uint32_t hi, const uint4& q, float scale) {
-  uint32_t h[8], f;
-  asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(f) : "f"(scale));
+  uint32_t h[8];
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    e4m3x4_to_f16(w[i], &h[2 * i], &h[2 * i + 1]);
-    h[2 * i] = mul_f16x2(h[2 * i], f);
-    h[2 * i + 1] = mul_f16x2(h[2 * i + 1], f);
+    float f[4];
+    e4m3x4_to_f32(w[i], f);
+    h[2 * i] = scaled_f16x2(f[0], f[1], scale);
+    h[2 * i + 1] = scaled_f16x2(f[2], f[3], scale);
   }
   sts128(lo, h[0], h[1], h[2], h[3]);
   sts128(hi, h[4], h[5], h[6], h[7]);

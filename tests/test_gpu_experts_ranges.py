@@ -48,3 +48,62 @@ def test_swiglu_backward_of_large_gates(weighted):
     if weighted:
         terms = (d * silu64(g) * u).abs()
         within(drw.double(), (d * silu64(g) * u).sum(1), (terms * (F / 32 + 24 + 2 * near) * U24).sum(1), "row weights")
+
+
+def weight_grad(r, y, x):
+    dw = torch.full((len(r.counts), y[0].shape[-1], x[0].shape[-1]), math.nan, dtype=torch.bfloat16, device=DEV)
+    ep.ep_grouped_weight_grad(*y, *x, dw, **r.args())
+    return dw
+
+
+def scale_rows(r, scales, values, factor):
+    """Multiplies the live rows' scales (and, in 64 bits, their values)."""
+    r._scales(scales)[r.live] *= factor[:, None].float()
+    return values * factor[:, None]
+
+
+def test_weight_grad_rounds_each_factor_once():
+    """Scales that f16 rounds by almost 2^-11 of themselves: a factor is code *
+    scale rounded once, not the code times a rounded scale, which would be off
+    by 2^-10 on every term.  Against the sum of such factors in 64 bits only the
+    fp32 sum's error and half a unit of the bf16 result (8 bits) remain."""
+    n = 64
+    r = Rows([n], "em")
+    yq, ys, _ = r.fp8(256, 31)
+    xq, xs, _ = r.fp8(384, 32)
+    j = torch.randint(0, 6, (n, 1), generator=gen(33), device=DEV)
+    s = (1 + 2.0 ** -11 - 2.0 ** -20) * torch.exp2(-j.double())
+    factors = []
+    for q, scales in ((yq, ys), (xq, xs)):
+        q.view(torch.uint8)[r.live] &= 0x7F  # all terms of one sign
+        r._scales(scales)[r.live] = s.float().expand(-1, scales.shape[0])
+        e = 2.0 ** (math.floor(math.log2(s.max().item())) - 6)
+        factors.append((q[r.live].double() * s / e).half().double() * e)
+    ref = factors[0].t() @ factors[1]
+    dw = weight_grad(r, (yq, ys), (xq, xs))
+    half_unit = torch.exp2(torch.floor(torch.log2(ref)) - 8)
+    within(dw[0].double(), ref, half_unit + ref * 2 * n * U24, "weight gradient")
+
+
+@pytest.mark.parametrize("spread", [12, 24, 30, 36])
+def test_weight_grad_of_opposed_row_scales(spread):
+    """Row scales over 2^spread in either operand and opposed in the two, so
+    that every row's products are alike: a factor is off by 2^-11 of itself and
+    2^-39 of the largest possible in its channels."""
+    n = 96
+    r = Rows([n, 5], "em")
+    up = torch.exp2(torch.linspace(0, spread, n, device=DEV).round().double())
+    up = torch.cat([up, torch.ones(5, dtype=torch.float64, device=DEV)])
+    yq, ys, y = r.fp8(256, 34)
+    xq, xs, x = r.fp8(128, 35)
+    y, x = scale_rows(r, ys, y, up), scale_rows(r, xs, x, 1 / up)
+    dw = weight_grad(r, (yq, ys), (xq, xs))
+    for e, at in r.spans():
+        ref, mag = y[at].t() @ x[at], y[at].abs().t() @ x[at].abs()
+        lost = []
+        for t, scales in ((y, ys), (x, xs)):
+            top = r._scales(scales)[r.live][at].double().amax(0) * 448.0
+            lost.append((top * 2.0 ** -39).repeat_interleave(128)[None, :].expand(len(t[at]), -1))
+        bound = ref.abs() * 2.0 ** -8 + mag * (2.0 ** -10 * (1 + 2.0 ** -11) + 2 * n * U24)
+        bound += 1.001 * (lost[0].t() @ x[at].abs() + y[at].abs().t() @ lost[1] + lost[0].t() @ lost[1])
+        within(dw[e].double(), ref, bound, f"weight gradient of expert {e}")
