@@ -27,7 +27,7 @@
 // other TMEM accumulator out through shared memory; one looks up the next
 // tiles' largest scales.  Rows past the group's end enter as zeros.
 //
-// 16 experts, 16 384 rows, 2 048 x 7 168: 413 us, 1.17 PFLOP/s; the load-store
+// 16 experts, 16 384 rows, 2 048 x 7 168: 409 us, 1.18 PFLOP/s; the load-store
 // pipe is busy 61 % of the cycles and the tensor cores' operand reads take
 // another 25 % of the same memory.  One block alone on 128 x 256: 614 us; rows
 // by plain loads instead of TMA: 464 us at best; 32-byte stores of the result
@@ -153,11 +153,12 @@ __device__ __forceinline__ void store_chunk(uint32_t lo, uint32_t hi, const uint
   sts128(hi, h[4], h[5], h[6], h[7]);
 }
 
-// 2^e that brings m to [64, 128); a largest scale of 0 or without a finite
-// value leaves the scales as they are.
-__device__ __forceinline__ int exponent_of(float m) {
-  const int e = m > 0.0f && m < 3.0e38f ? ilogbf(m) - 6 : 0;
-  return max(-60, min(60, e));
+// 2^e that brings m to [64, 128) (towards it, where m is subnormal); a largest
+// scale of 0 leaves the scales as they are.
+__device__ __forceinline__ int exponent_of(float m) { return m > 0.0f ? max(-126, ilogbf(m) - 6) : 0; }
+__device__ __forceinline__ float finite_size(float scale) {
+  const float m = fabsf(scale);
+  return m <= 3.402823466e38f ? m : 0.0f;
 }
 
 }  // namespace
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll 8
       for (int r = lane; r < w.rows; r += 32) {
-        if (in_n) m[0] = fmaxf(m[0], fabsf(ys[r * p.dy.row_stride]));
-        m[1] = fmaxf(m[1], fabsf(xs[r * p.x.row_stride]));
-        if (second) m[2] = fmaxf(m[2], fabsf(xs[r * p.x.row_stride + p.x.group_stride]));
+        if (in_n) m[0] = fmaxf(m[0], finite_size(ys[r * p.dy.row_stride]));
+        m[1] = fmaxf(m[1], finite_size(xs[r * p.x.row_stride]));
+        if (second) m[2] = fmaxf(m[2], finite_size(xs[r * p.x.row_stride + p.x.group_stride]));
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1)
@@ -412,10 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      wait_or_quit<true>(&s.acc_full[ac], (used >> 1) & 1, quit, err)))
         break;
       tmem_fence_after();
-      const float up[2] = {power_of_two(s.exponent[e][0] + s.exponent[e][1]), power_of_two(s.exponent[e][0] + s.exponent[e][2])};
+      // each half's 2^(dy's + x's exponent) as two factors: the sum may be beyond
+      // what one fp32 number holds
+      float up[2], rest[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int sum = s.exponent[e][0] + s.exponent[e][1 + h], first = max(-126, min(126, sum));
+        up[h] = power_of_two(first);
+        rest[h] = power_of_two(max(-126, min(126, sum - first)));
+      }
 #pragma unroll
       for (int q = 0; q < kPair / 64; ++q) {
-        const float f = up[q >> 1];
+        const float f = up[q >> 1], f2 = rest[q >> 1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t v[32];
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_load_wait(v);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            x[h * 16 + j] = pack_bf16x2(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
+            x[h * 16 + j] = pack_bf16x2(__uint_as_float(v[2 * j]) * f * f2, __uint_as_float(v[2 * j + 1]) * f * f2);
         }
         if (q == kPair / 64 - 1) {
           tmem_fence_before();

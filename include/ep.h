@@ -536,7 +536,7 @@ ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* gr
  * the rows r of group e of grad_out[r][n] x[r][k], summed in fp32, rounded once
  * to bf16 (dev [num_groups][N][K], 16-byte aligned; 0 for an empty group).
  * The factors are dequantised values rounded once to f16, relative to a power
- * of two near the largest scale of their 128 channels in the group: a factor is
+ * of two near the largest finite scale of their 128 channels in the group: a factor is
  * off by 2^-11 of itself, or, if that is more, by 2^-39 of 448 times that scale.
  * Rows whose values lie within 2^-28 of the group's largest lose nothing more.
  * N and K are multiples of 128.  Runs on pairs of SMs: num_sms is rounded down

@@ -107,3 +107,35 @@ def test_weight_grad_of_opposed_row_scales(spread):
         bound = ref.abs() * 2.0 ** -8 + mag * (2.0 ** -10 * (1 + 2.0 ** -11) + 2 * n * U24)
         bound += 1.001 * (lost[0].t() @ x[at].abs() + y[at].abs().t() @ lost[1] + lost[0].t() @ lost[1])
         within(dw[e].double(), ref, bound, f"weight gradient of expert {e}")
+
+
+@pytest.mark.parametrize("ey,ex", [(-100, 60), (-110, 0), (0, -110), (100, -90), (-70, 100), (116, -116), (60, 60)])
+def test_weight_grad_of_tiny_and_huge_scales(ey, ex):
+    """Scales anywhere in fp32's normal range (2^-8 of the factor here, or more):
+    powers of two change nothing but the result's own exponent."""
+    r = Rows([70, 0, 3], "em", 4)
+    yq, ys, y = r.fp8(256, 36)
+    xq, xs, x = r.fp8(384, 37)
+    plain = weight_grad(r, (yq, ys), (xq, xs))
+    n = len(r.live)
+    scale_rows(r, ys, y, torch.full((n,), 2.0 ** ey, dtype=torch.float64, device=DEV))
+    scale_rows(r, xs, x, torch.full((n,), 2.0 ** ex, dtype=torch.float64, device=DEV))
+    dw = weight_grad(r, (yq, ys), (xq, xs))
+    want = plain.double() * 2.0 ** (ey + ex)
+    assert torch.equal(dw, torch.where(want.abs() < 2.0 ** 127, want, want.sign() * math.inf).bfloat16())
+
+
+def test_weight_grad_beside_an_infinite_row():
+    """A row of infinite scale makes its terms infinite, of the codes' signs;
+    the other rows stay finite beside it."""
+    n = 40
+    r = Rows([n], "em")
+    yq, ys, _ = r.fp8(128, 38)
+    xq, xs, _ = r.fp8(128, 39)
+    for q in (yq, xq):
+        q.view(torch.uint8)[7] = torch.where(torch.arange(128, device=DEV) % 3 == 0, 0x38, 0xB8).to(torch.uint8)  # 1, -1
+    ys[0, :n] *= 2.0 ** 30
+    ys[0, 7] = math.inf
+    dw = weight_grad(r, (yq, ys), (xq, xs))
+    want = yq.double()[7][:, None] * xq.double()[7][None, :] * math.inf
+    assert torch.equal(dw[0].double(), want)
