@@ -244,6 +244,7 @@ struct GateArgs {
   int T, E, k, groups, keep, sigmoid, ids32;
   int vec;  // rows readable as 16-byte words (grad_vec: writable)
   float coef;
+  float fixed;     // 1 / step of the blocks' probability sums
   void* idx;       // [T][k]
   float* weights;  // [T][k]
   int* count;      // [E + 1]

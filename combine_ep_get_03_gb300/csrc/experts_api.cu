@@ -122,6 +122,9 @@ ep_status_t ep_gate_forward(const void* logits, ep_logits_t logits_type, int64_t
   p.prob = expert_prob;
   p.loss = loss;
   p.work = static_cast<unsigned*>(workspace);
+  int log2_T = 0;
+  while ((1LL << log2_T) < T) ++log2_T;
+  p.fixed = static_cast<float>(1ull << (63 - log2_T));
   return status_of(ep::launch_gate(p, logits_type == EP_LOGITS_BF16, false, sms, reinterpret_cast<cudaStream_t>(stream)),
                    "ep_gate_forward launch");
 }

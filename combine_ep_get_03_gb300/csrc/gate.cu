@@ -16,8 +16,9 @@
 // lane's experts are the same for every token and the column sums P stay in
 // registers until the block ends; lane order is index order, which settles
 // ties by the first lane of a ballot.  Blocks join their sums as 64-bit fixed
-// point (2^-36), which makes the result independent of their order, and the
-// last block to finish writes counts, P and the loss: one launch.
+// point, which makes the result independent of their order, and the last block
+// to finish writes counts, P and the loss: one launch.  A sum is at most T, so
+// the step is 2^-(63 - ceil(log2 T)): 2^-48 at 32 768 tokens.
 //
 // Bound by the half-rate integer and compare pipe (60 % busy forward): hence
 // keys sorted once per lane and shifted, one score kind per row, bf16 logits'
@@ -34,7 +35,6 @@ namespace ep {
 // Warps of a block: as many as leave room for a row of floats each.
 __host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 1; }
 __host__ __device__ constexpr int index_bits(int vpl) { return vpl == 1 ? 5 : 1 + index_bits(vpl / 2); }
-constexpr float kFixed = 68719476736.0f;  // 2^36
 
 // work: [0] finished blocks, [1] set if a row had no finite sum, [2] unmasked
 // tokens, [3] unused, then E u64 sums, then E counts
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   if (!alone) {
     for (int e = tid; e < E; e += blockDim.x) {
       const float sum = block_sum(e);
-      if (sum > 0.0f) atomicAdd(&sums[e], __float2ull_rn(sum * kFixed));
+      if (sum > 0.0f) atomicAdd(&sums[e], __float2ull_rn(sum * p.fixed));
       if (s_count[e]) atomicAdd(&counts[e], s_count[e]);
     }
     if (tid == 0) {
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(gate_warps(VPL) * 32) k_gate_forward(const Gat
   float part = 0.0f;
   for (int e = tid; e < E; e += blockDim.x) {
     const int n = alone ? s_count[e] : __ldcg(&counts[e]);
-    const float sum = alone ? block_sum(e) : __ull2float_rn(__ldcg(&sums[e])) * (1.0f / kFixed);
+    const float sum = alone ? block_sum(e) : __ull2float_rn(__ldcg(&sums[e])) * (1.0f / p.fixed);
     const float pe = any_bad ? CUDART_NAN_F : tokens ? sum / tokens : 0.0f;
     p.count[e] = n;
     p.prob[e] = pe;

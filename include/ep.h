@@ -474,6 +474,8 @@ ep_status_t ep_gate_workspace_bytes(int num_experts, int64_t* bytes);
  *      topk_weights dev fp32 [T][k], 0 where topk_idx is -1.
  *      expert_count dev int32 [E + 1]: entries per expert; [E] = unmasked tokens V.
  *      expert_prob  dev fp32 [E]: mean of p over the unmasked tokens (0 if none).
+ *                   Blocks of tokens add their fp32 sums in steps of 2^-(63 -
+ *                   ceil(log2 T)): a sum below half a step counts as 0.
  *      loss         dev fp32 [1]: loss_coef * E / (k V) * sum_e expert_count[e]
  *                   expert_prob[e] (0 if V = 0); NaN, as expert_prob, if a
  *                   row's probabilities are not finite.

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from combine_ep_get_03_gb300 import ep
-from test_gpu_experts import DEV, U24, Rows, check8, gen, silu64, within
+from test_gpu_experts import DEV, U24, Rows, check8, gen, run_gate, silu64, within
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,23 @@ def test_weight_grad_beside_an_infinite_row():
     dw = weight_grad(r, (yq, ys), (xq, xs))
     want = yq.double()[7][:, None] * xq.double()[7][None, :] * math.inf
     assert torch.equal(dw[0].double(), want)
+
+
+@pytest.mark.parametrize("T", [16, 17, 300, 4096, 40000])
+@pytest.mark.parametrize("sms", [0, 1, 7])
+@pytest.mark.parametrize("score", [ep.EP_GATE_SOFTMAX, ep.EP_GATE_SIGMOID])
+def test_gate_mean_probability_of_a_cold_expert(T, sms, score):
+    """An expert that every token gives about 1e-14: its mean comes out to fp32's
+    rounding and half a step of 2^-(63 - ceil(log2 T)) for every block that adds."""
+    E, k = 64, 4
+    l = torch.randn((T, E), generator=gen(41), device=DEV)
+    l[:, 9] -= 28.0
+    o = run_gate(l, k, score=score, num_sms=sms)
+    l64 = l.double()
+    s = torch.exp(l64) if score == ep.EP_GATE_SOFTMAX else torch.sigmoid(l64)
+    prob = (s / s.sum(1, keepdim=True)).mean(0)
+    step = 2.0 ** -(63 - math.ceil(math.log2(T)))
+    blocks = min(-(-T // 16), 2 * (sms or 152))
+    # exponentials to 2^-21 and (|l| + 4) u24, sums over E and over the tokens of a warp
+    tol = (E / 32 + 64 + 40 + T / (16 * blocks)) * U24
+    within(o["prob"].double(), prob, tol * prob + 0.5 * step * blocks / T, "mean probabilities")
