@@ -122,7 +122,13 @@ class MoELayer:
                            pre_s)
 
     def backward(self, grad_out, grad_loss, saved, w1: ExpertWeights, w2: ExpertWeights):
-        """-> (grad_x bf16 [T, H], grad_logits, grad_w1, grad_w2 bf16)."""
+        """-> (grad_x bf16 [T, H], grad_logits, grad_w1, grad_w2 bf16).
+
+        Gradients travel in e4m3 with a scale for 128 channels, whose largest
+        magnitude counts as 1e-4 at least: below that they lose bits, and below
+        2e-10 they are 0.  Every result is linear in (grad_out, grad_loss), so
+        where a mean over many tokens makes gradients that small, scale both up
+        by a power of two (the loss, before its backward) and the results down."""
         logits, token_mask, idx, count, layout, groups, xq, xs, row_w, act, act_s, pre, pre_s = saved
         T = grad_out.shape[0]
         gy, gy_s = self._fp8(self.H)

@@ -528,7 +528,11 @@ ep_status_t ep_grouped_matmul_swiglu(const ep_groups_t* groups, const ep_fp8_row
 /* Backward of that activation from its 8-bit checkpoint.
  * In:  grad_act  dev bf16 [rows][F], the gradient of act;  pre and row_weights as
  *                ep_grouped_matmul_swiglu left and had them.
- * Out: grad_pre  e4m3 rows of width 2F: the gradient of the pre-activations.
+ * Out: grad_pre  e4m3 rows of width 2F: the gradient of the pre-activations,
+ *                quantised as dispatch quantises: 128 channels whose largest
+ *                magnitude is below 1e-4 are stored in steps of 4.4e-10 at best
+ *                and below 2.2e-10 as 0.  The call is linear in grad_act, so
+ *                gradients that small are scaled up first (with the loss).
  *      grad_row_weights  dev fp32 [rows] or NULL. */
 ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* grad_act, const ep_fp8_rows_t* pre,
                                        const float* row_weights, int F, const ep_fp8_rows_t* grad_pre,

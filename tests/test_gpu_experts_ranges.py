@@ -159,3 +159,28 @@ def test_gate_mean_probability_of_a_cold_expert(T, sms, score):
     # exponentials to 2^-21 and (|l| + 4) u24, sums over E and over the tokens of a warp
     tol = (E / 32 + 64 + 40 + T / (16 * blocks)) * U24
     within(o["prob"].double(), prob, tol * prob + 0.5 * step * blocks / T, "mean probabilities")
+
+
+def test_swiglu_backward_of_tiny_gradients():
+    """As the header says: steps of 1e-4 / 448 / 512 for 128 channels below 1e-4,
+    0 below half a step, and every bit back when the gradient is scaled up."""
+    F, n = 256, 20
+    r = Rows([n], "em")
+    pq, ps, p = r.fp8(2 * F, 51)
+    d = torch.randn((n, F), generator=gen(52), device=DEV).bfloat16()
+    g, u = p.chunk(2, 1)
+    sg = torch.sigmoid(g)
+    slope = torch.cat([u * sg * (1 + g * (1 - sg)), silu64(g)], 1)
+    rel = torch.cat([u.abs() * sg * (1 + g.abs() + silu64(g).abs()), silu64(g).abs()], 1) * (16 + 2 * g.abs().repeat(1, 2)) * U24
+    for e in (-27, -3):
+        da = (d.double() * 2.0 ** e).bfloat16()
+        dp, dps = r.out8(2 * F)
+        ep.ep_grouped_swiglu_backward(da, pq, ps, dp, dps, **r.args())
+        v, sc = r.read8(dp, dps)
+        da2 = da.double().repeat(1, 2)
+        check8(v, sc, da2 * slope, da2.abs() * rel, "gradient")
+        if e == -27:  # the floor's scale everywhere
+            assert (sc == sc.flatten()[0]).all() and (v != 0).any()
+            assert (v[(da2 * slope).abs() < 2.1e-10] == 0).all()
+        else:  # no group at the floor
+            assert (sc > 1.01e-4 / 448).all()

@@ -93,3 +93,15 @@ def test_layout_made_outside_the_layer(layer, weights):
     layer.h.em_layout_and_dispatch(other, a["x"], None, ep.EP_BF16, 1,
                                    torch.empty((rows, H), dtype=torch.bfloat16, device=DEV))
     same(backward(layer, a, saved, weights), want)
+
+
+def test_backward_is_linear_in_its_gradients(layer, weights):
+    """Both gradients times 2^10: every result is 2^10 times what it was, bit for
+    bit, since no 128 channels are at the quantisation's floor here.  That is how
+    small gradients are scaled up."""
+    a = batch(31)
+    _, _, saved = forward(layer, a, weights)
+    one = backward(layer, a, saved, weights)
+    big = layer.backward((a["go"].float() * 1024).bfloat16(), a["gl"] * 1024, saved, *weights)
+    for x, y in zip(big, one):
+        assert torch.equal(x, y * 1024)
