@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from combine_ep_get_03_gb300 import ep
-from test_gpu_experts import DEV, U24, Rows, check8, gen, run_gate, silu64, within
+from test_gpu_experts import (DEV, F8, U24, Rows, check8, gen, quantize, run_gate, silu64, sum_err, weights,
+                              within)
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +185,102 @@ def test_swiglu_backward_of_tiny_gradients():
             assert (v[(da2 * slope).abs() < 2.1e-10] == 0).all()
         else:  # no group at the floor
             assert (sc > 1.01e-4 / 448).all()
+
+
+def test_swiglu_and_its_backward_read_64_bit_offsets():
+    """The only live rows lie past 2^31 elements of x, of both outputs and of the
+    gradients."""
+    M, G, K, F, n = 45000, 8, 6016, 6144, 5
+    f8 = lambda w: torch.empty((G, M, w), dtype=torch.uint8, device=DEV)  # noqa: E731
+    f32 = lambda w: torch.empty((G, M, w), device=DEV)  # noqa: E731
+    x, xs, act, acts, pre, pres = f8(K), f32(K // 128), f8(F), f32(F // 128), f8(2 * F), f32(2 * F // 128)
+    assert min(x.numel(), act.numel()) > 2 ** 31
+    q, s = quantize(torch.randn((n, K), generator=gen(61), device=DEV))
+    x[G - 1, :n], xs[G - 1, :n] = q.view(torch.uint8), s
+    count = torch.tensor([0] * (G - 1) + [n], dtype=torch.int32, device=DEV)
+    wq, ws, w = weights(1, 2 * F, K, 62)
+    w8 = wq.view(torch.uint8).expand(G, -1, -1).contiguous()
+    ep.ep_grouped_matmul_swiglu(x, xs, w8, ws.expand(G, -1, -1).contiguous(), act, acts, count, pre=pre, pre_scales=pres)
+    del w8
+    xd = q.double() * s.double().repeat_interleave(128, 1)
+    y, err = xd @ w[0].t(), sum_err(K) * (xd.abs() @ w[0].abs().t())
+    read = lambda t, sc: t[G - 1, :n].view(F8).double() * sc[G - 1, :n].double().repeat_interleave(128, 1)  # noqa: E731
+    check8(read(pre, pres), pres[G - 1, :n].double(), y, err, "pre-activations")
+    g, u = y.chunk(2, 1)
+    eg, eu = err.chunk(2, 1)
+    a = silu64(g) * u
+    ea = 1.1 * eg * u.abs() + (silu64(g).abs() + 1.1 * eg) * eu + (16 + 2 * g.abs()) * U24 * a.abs()
+    check8(read(act, acts), acts[G - 1, :n].double(), a, ea, "activations")
+
+    del x, xs, act, acts
+    da = torch.empty((G, M, F), dtype=torch.bfloat16, device=DEV)
+    da[G - 1, :n] = torch.randn((n, F), generator=gen(63), device=DEV).bfloat16()
+    dp, dps = f8(2 * F), f32(2 * F // 128)
+    ep.ep_grouped_swiglu_backward(da, pre, pres, dp, dps, count)
+    g, u = read(pre, pres).chunk(2, 1)
+    d, sg = da[G - 1, :n].double(), torch.sigmoid(g)
+    mag = torch.cat([(d * u).abs() * sg * (1 + g.abs() + silu64(g).abs()), (d * silu64(g)).abs()], 1)
+    check8(read(dp, dps), dps[G - 1, :n].double(), torch.cat([d * u * sg * (1 + g * (1 - sg)), d * silu64(g)], 1),
+           mag * (16 + 2 * g.abs().repeat(1, 2)) * U24, "gradient")
+
+
+def test_weight_grad_and_product_of_weights_beyond_2_31_elements():
+    """The last group's weights, and their gradient, lie past 2^31 elements."""
+    G, N, K, n = 66, 4096, 8192, 70
+    r = Rows([0] * (G - 1) + [n], "em")
+    yq, ys, y = r.fp8(N, 64, sigma=1e-2)
+    xq, xs, x = r.fp8(K, 65)
+    dw = torch.full((G, N, K), math.nan, dtype=torch.bfloat16, device=DEV)
+    assert (G - 1) * N * K > 2 ** 31
+    ep.ep_grouped_weight_grad(yq, ys, xq, xs, dw, **r.args())
+    ref, mag = y.t() @ x, y.abs().t() @ x.abs()
+    within(dw[G - 1].double(), ref, ref.abs() * 2.0 ** -8 + mag * 2.0 ** -8.9, "weight gradient")
+    assert all((dw[e] == 0).all() for e in range(G - 1))
+    del dw
+    w8 = torch.empty((G, N, K), dtype=torch.uint8, device=DEV)
+    wq, ws, w = weights(1, N, K, 66)
+    w8[G - 1] = wq[0].view(torch.uint8)
+    scales = torch.empty((G, N // 128, K // 128), device=DEV)
+    scales[G - 1] = ws[0]
+    out = r.out16(N)
+    ep.ep_grouped_matmul(xq, xs, w8, scales, out, **r.args())
+    p, pmag = x @ w[0].t(), x.abs() @ w[0].abs().t()
+    within(r.read16(out), p, p.abs() * 2.0 ** -8 + sum_err(K) * pmag, "product")
+
+
+def test_weight_grad_of_rows_beyond_2_31_elements():
+    M, G, N, K, n = 1400000, 4, 128, 512, 90
+    y, x = (torch.empty((G, M, w), dtype=torch.uint8, device=DEV) for w in (N, K))
+    ys, xs = (torch.empty((G, M, w // 128), device=DEV) for w in (N, K))
+    assert (G - 1) * M * K > 2 ** 31
+    vals = []
+    for q, s, w in ((y, ys, N), (x, xs, K)):
+        c, sc = quantize(torch.randn((n, w), generator=gen(w), device=DEV))
+        q[G - 1, :n], s[G - 1, :n] = c.view(torch.uint8), sc
+        vals.append(c.double() * sc.double().repeat_interleave(128, 1))
+    dw = torch.empty((G, N, K), dtype=torch.bfloat16, device=DEV)
+    ep.ep_grouped_weight_grad(y, ys, x, xs, dw, torch.tensor([0] * (G - 1) + [n], dtype=torch.int32, device=DEV))
+    ref, mag = vals[0].t() @ vals[1], vals[0].abs().t() @ vals[1].abs()
+    within(dw[G - 1].double(), ref, ref.abs() * 2.0 ** -8 + mag * 2.0 ** -8.9, "weight gradient")
+    assert (dw[:G - 1] == 0).all()
+
+
+def test_gate_reads_64_bit_offsets():
+    """The only unmasked tokens lie past 2^31 logits."""
+    T, E, k, n = 560000, 4000, 5, 6
+    l = torch.empty((T, E), dtype=torch.bfloat16, device=DEV)
+    assert (T - n) * E > 2 ** 31
+    l[T - n:] = torch.randn((n, E), generator=gen(67), device=DEV).bfloat16()
+    mask = torch.zeros(T, dtype=torch.bool, device=DEV)
+    mask[T - n:] = True
+    o = run_gate(l, k, mask=mask)
+    tail = l[T - n:].contiguous()
+    small = run_gate(tail, k)
+    assert torch.equal(o["idx"][T - n:], small["idx"]) and torch.equal(o["w"][T - n:], small["w"])
+    assert (o["idx"][:T - n] == -1).all() and torch.equal(o["count"], small["count"])
+    dw = torch.randn((T, k), generator=gen(68), device=DEV)
+    one = torch.ones(1, device=DEV)
+    grad, want = torch.full_like(l, 7.0), torch.empty_like(tail)
+    ep.ep_gate_backward(l, o["idx"], o["count"], dw, one, grad, loss_coef=0.5, token_mask=mask)
+    ep.ep_gate_backward(tail, small["idx"], small["count"], dw[T - n:].contiguous(), one, want, loss_coef=0.5)
+    assert torch.equal(grad[T - n:], want) and not grad[:T - n].any()
