@@ -106,7 +106,8 @@ class MoELayer:
         idx, w, count, loss = self.route(logits, token_mask)
         xq, xs = self._fp8(self.H)
         row_w = self._f32(self.rows)
-        self.h.em_layout_and_dispatch(idx, x, w, ep.EP_FP8_E4M3, self.align, xq, xs, recv_weights=row_w)
+        # no tokens, no weights: an empty tensor has no address to give with recv_weights
+        self.h.em_layout_and_dispatch(idx, x, w, ep.EP_FP8_E4M3, self.align, xq, xs, recv_weights=row_w if T else None)
         offset, rows = self._i32(self.E + 1), self._i32(self.E)
         self.h.em_get_groups(offset, rows)
         groups = dict(group_count=rows, group_offset=offset, device_status=self.status)

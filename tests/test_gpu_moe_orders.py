@@ -105,3 +105,19 @@ def test_backward_is_linear_in_its_gradients(layer, weights):
     big = layer.backward((a["go"].float() * 1024).bfloat16(), a["gl"] * 1024, saved, *weights)
     for x, y in zip(big, one):
         assert torch.equal(x, y * 1024)
+
+
+def test_no_tokens_and_one_token_per_rank(layer, weights):
+    """A micro-batch without tokens has gradients of zero; one of a token for each
+    rank agrees with itself inside a larger batch's buffers."""
+    empty = batch(41, 0)
+    out, loss, saved = forward(layer, empty, weights)
+    gx, gl, gw1, gw2 = backward(layer, empty, saved, weights)
+    assert out.shape == (0, H) and gx.shape == (0, H) and gl.shape == (0, E) and loss.item() == 0.0
+    assert not gw1.any() and not gw2.any()
+    assert layer.decode(empty["x"], empty["logits"], *weights).shape == (0, H)
+    few = batch(42, R)
+    _, _, want = straight(layer, few, weights)
+    forward(layer, batch(43), weights)
+    same(straight(layer, few, weights)[2], want)
+    layer.check()
