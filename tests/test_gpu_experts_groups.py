@@ -100,3 +100,22 @@ def test_as_many_groups_as_the_header_allows(G, layout):
     eg = torch.cat([(d * u).abs() * sg * (1 + g.abs() + silu64(g).abs()), (d * silu64(g)).abs()], 1)
     check8(*r.read8(dp, dps), grad, eg * (16 + 2 * g.abs().repeat(1, 2)) * 2.0 ** -24, "gradient")
     assert int(status) == ep.EP_OK
+
+
+@pytest.mark.parametrize("lead", [(0,), (3, 0)])
+def test_buffers_without_rows(lead):
+    """No rows at all: nothing to write, and weight gradients of zero."""
+    G, N, K = 3, 128, 256
+    f8 = lambda w: torch.empty(lead + (w,), dtype=torch.uint8, device=DEV)  # noqa: E731
+    f32 = lambda w: torch.empty((w // 128, 4) if len(lead) == 1 else lead + (w // 128,), device=DEV)  # noqa: E731
+    bf = lambda w: torch.empty(lead + (w,), dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    zero = torch.zeros(G, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = dict(group_count=zero, group_offset=zero if len(lead) == 1 else None, device_status=status)
+    q, s, _ = weights(G, 2 * N, K, 1)
+    ep.ep_grouped_matmul(f8(K), f32(K), q, s, bf(2 * N), **args)
+    ep.ep_grouped_matmul_swiglu(f8(K), f32(K), q, s, f8(N), f32(N), pre=f8(2 * N), pre_scales=f32(2 * N), **args)
+    ep.ep_grouped_swiglu_backward(bf(N), f8(2 * N), f32(2 * N), f8(2 * N), f32(2 * N), **args)
+    dw = torch.full((G, N, K), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ep.ep_grouped_weight_grad(f8(N), f32(N), f8(K), f32(K), dw, **args)
+    assert not dw.any() and int(status) == ep.EP_OK
