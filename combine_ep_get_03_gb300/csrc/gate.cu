@@ -20,9 +20,10 @@
 // to finish writes counts, P and the loss: one launch.  A sum is at most T, so
 // the step is 2^-(63 - ceil(log2 T)): 2^-48 at 32 768 tokens.
 //
-// Bound by the half-rate integer and compare pipe (60 % busy forward): hence
-// keys sorted once per lane and shifted, one score kind per row, bf16 logits'
-// exact 32-bit keys.  32 768 tokens of 256 bf16 logits, top-8: 27 us forward,
+// No pipe is full: the half-rate integer and compare pipe is 60 % busy forward
+// (hence keys sorted once per lane and shifted, one score kind per row, bf16
+// logits' exact 32-bit keys), and each token begins with a load that it waits
+// for.  32 768 tokens of 256 bf16 logits, top-8: 27 us forward,
 // 22 us backward (46 us the pair in a stream); one token 6 us, less than the
 // call's host side.
 #include <math_constants.h>
@@ -32,7 +33,10 @@
 
 namespace ep {
 
-// Warps of a block: as many as leave room for a row of floats each.
+// Warps of a block: as many as leave room for a row of floats each.  Beyond 1 024
+// experts (VPL = 128) a row does not fit the registers (1.6-1.9 KB of spill stores
+// a thread): fp32, 8 192 tokens, top-8, forward and backward 53 and 79 us at 1 024
+// experts, 257 and 312 at 1 025, 513 and 379 at 4 096.
 __host__ __device__ constexpr int gate_warps(int vpl) { return vpl <= 8 ? 16 : vpl <= 32 ? 8 : 1; }
 __host__ __device__ constexpr int index_bits(int vpl) { return vpl == 1 ? 5 : 1 + index_bits(vpl / 2); }
 

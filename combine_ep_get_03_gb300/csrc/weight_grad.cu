@@ -12,8 +12,8 @@
 // result's own 2^-8, as long as both values are 2^-28 of their channels' largest
 // possible (448 times that scale) or more; f16's subnormal step is 2^-39 of it.
 // bf16 operands would keep any range but round to 2^-8 each.  Scale and product
-// both rounded to f16 (no fp32 arithmetic) 386 us, this 413; a scale split in
-// two f16 numbers 412, and with the range above 418.
+// both rounded to f16 (no fp32 arithmetic) 386 us, this 409-414; a scale split
+// in two f16 numbers 412, and with the range above 418.
 //
 // Shared memory is what bounds it: a widened 64-row stage is written once and
 // read once per MMA.  So two blocks on neighbouring SMs share a tile of 256 (n)
@@ -27,11 +27,11 @@
 // other TMEM accumulator out through shared memory; one looks up the next
 // tiles' largest scales.  Rows past the group's end enter as zeros.
 //
-// 16 experts, 16 384 rows, 2 048 x 7 168: 409 us, 1.18 PFLOP/s; the load-store
-// pipe is busy 61 % of the cycles and the tensor cores' operand reads take
-// another 25 % of the same memory.  One block alone on 128 x 256: 614 us; rows
-// by plain loads instead of TMA: 464 us at best; 32-byte stores of the result
-// straight from registers: 410 us.
+// 16 experts, 16 384 rows, 2 048 x 7 168: 409-414 us, 1.17 PFLOP/s; 61 % of the
+// issue slots are taken, the load-store pipe is busy 52 % of the cycles and the
+// tensor cores' operand reads take about another quarter of the same memory.  With two f16 roundings instead (386 us):
+// one block alone on 128 x 256 614 us; rows by plain loads instead of TMA 464 us
+// at best; 32-byte stores of the result straight from registers 410 us.
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "tcgen05.cuh"
