@@ -21,7 +21,7 @@
 // Many rows: a stage's 48 KB are written to shared memory once and read once,
 // some 750 cycles where the MMAs take 512 (without the loads the same kernel
 // does 3.3 PFLOP/s, without the sums 2.2; a library product of 8 192^3 with one
-// scale does 3.9); 32 768 rows, 7 168 -> 4 096: 922 us, 2.09 PFLOP/s, the tensor
+// scale does 3.9); 32 768 rows, 7 168 -> 4 096: 897-923 us, 2.1 PFLOP/s, the tensor
 // pipe 53 % active.  Few rows: the weights' stream; 32 experts of 2 048 -> 7 168 for
 // 1 024 rows 77 us, 6.3 TB/s, and one token's eight experts of 7 168 -> 4 096
 // 43 us, 5.4 TB/s (128 tiles on 152 SMs).  Pairs of blocks on a 256 x 256 tile

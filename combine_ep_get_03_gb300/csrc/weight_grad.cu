@@ -29,9 +29,10 @@
 //
 // 16 experts, 16 384 rows, 2 048 x 7 168: 409-414 us, 1.17 PFLOP/s; 61 % of the
 // issue slots are taken, the load-store pipe is busy 52 % of the cycles and the
-// tensor cores' operand reads take about another quarter of the same memory.  With two f16 roundings instead (386 us):
-// one block alone on 128 x 256 614 us; rows by plain loads instead of TMA 464 us
-// at best; 32-byte stores of the result straight from registers 410 us.
+// tensor cores' operand reads take about another quarter of the same memory.
+// Measured with two f16 roundings (386 us): one block alone on 128 x 256 614 us;
+// rows by plain loads instead of TMA 464 us at best; 32-byte stores of the result
+// straight from registers 410 us.
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "tcgen05.cuh"
