@@ -10,6 +10,7 @@
 namespace ep {
 
 constexpr int kMaxGroups = 4096;
+constexpr int kTile4Rows = 112;  // rows of a tile of the products on 4-bit weights
 
 // Groups of rows: group g holds count[g] rows from offset[g], or from
 // g * rows_per_group where offset is null.
@@ -282,6 +283,18 @@ struct MatmulArgs {
   const float* row_weights; // [rows] or null
 };
 
+// The same products on 4-bit weights; act.data selects the SwiGLU epilogue.
+struct Matmul4Args {
+  GroupArgs groups;
+  Fp8Rows x;                      // [rows][K]
+  const void* w;                  // e2m1 [G][N][K/2], two codes a byte
+  const unsigned char* w_scales;  // [G][ceil(N/128)][K/128][512]
+  int N, K;
+  uint16_t* out;            // bf16 [rows][N], or null
+  Fp8Rows act;              // [rows][F]
+  const float* row_weights; // [rows] or null
+};
+
 // dw[g] = sum over the group's rows of dy^T x.
 struct WeightGradArgs {
   GroupArgs groups;
@@ -294,6 +307,7 @@ struct WeightGradArgs {
 cudaError_t launch_gate(const GateArgs& p, bool bf16, bool backward, int sms, cudaStream_t stream);
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& p, int sms, cudaStream_t stream);
 cudaError_t launch_grouped_matmul(const MatmulArgs& p, int sms, cudaStream_t stream);
+cudaError_t launch_grouped_matmul_w4(const Matmul4Args& p, int sms, cudaStream_t stream);
 cudaError_t launch_weight_grad(const WeightGradArgs& p, int sms, cudaStream_t stream);
 size_t gate_work_bytes(int E);
 // out[i] = row_weights[the expert-major row of entry i], 0 where masked.

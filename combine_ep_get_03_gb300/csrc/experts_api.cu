@@ -206,6 +206,55 @@ ep_status_t ep_grouped_matmul_swiglu(const ep_groups_t* groups, const ep_fp8_row
                    "ep_grouped_matmul_swiglu launch");
 }
 
+static bool w4_ok(const ep_groups_t* g, const void* w, const void* w_scales, int N, int K) {
+  return groups_ok(g) && K >= 128 && K % 128 == 0 && static_cast<long long>(g->num_groups) * N <= INT_MAX &&
+         (g->rows / ep::kTile4Rows + g->num_groups + 1) * ((N + 127) / 128) < INT_MAX / 2 && w && w_scales &&
+         aligned(w, 32) && aligned(w_scales, 16);
+}
+
+ep_status_t ep_grouped_matmul_w4(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                                 const uint8_t* w_scales, int N, int K, void* out, int num_sms, ep_stream_t stream) {
+  if (N < 8 || N % 8 != 0 || !w4_ok(groups, w, w_scales, N, K)) return EP_ERR_INVALID_ARG;
+  if (groups->rows == 0) return EP_OK;
+  if (!rows_ok(x) || !out || !aligned(out, 16)) return EP_ERR_INVALID_ARG;
+  int sms = 0;
+  ep_status_t st = sm_count(num_sms, &sms);
+  if (st != EP_OK) return st;
+  ep::Matmul4Args p{};
+  p.groups = groups_of(groups);
+  p.x = rows_of(x);
+  p.w = w;
+  p.w_scales = w_scales;
+  p.N = N;
+  p.K = K;
+  p.out = static_cast<uint16_t*>(out);
+  return status_of(ep::launch_grouped_matmul_w4(p, sms, reinterpret_cast<cudaStream_t>(stream)),
+                   "ep_grouped_matmul_w4 launch");
+}
+
+ep_status_t ep_grouped_matmul_w4_swiglu(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                                        const uint8_t* w_scales, int F, int K, const float* row_weights,
+                                        const ep_fp8_rows_t* act, int num_sms, ep_stream_t stream) {
+  if (F < 128 || F % 128 != 0 || F > INT_MAX / 2 || !w4_ok(groups, w, w_scales, 2 * F, K) || !aligned(row_weights, 4))
+    return EP_ERR_INVALID_ARG;
+  if (groups->rows == 0) return EP_OK;
+  if (!rows_ok(x) || !rows_ok(act)) return EP_ERR_INVALID_ARG;
+  int sms = 0;
+  ep_status_t st = sm_count(num_sms, &sms);
+  if (st != EP_OK) return st;
+  ep::Matmul4Args p{};
+  p.groups = groups_of(groups);
+  p.x = rows_of(x);
+  p.w = w;
+  p.w_scales = w_scales;
+  p.N = 2 * F;
+  p.K = K;
+  p.act = rows_of(act);
+  p.row_weights = row_weights;
+  return status_of(ep::launch_grouped_matmul_w4(p, sms, reinterpret_cast<cudaStream_t>(stream)),
+                   "ep_grouped_matmul_w4_swiglu launch");
+}
+
 ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* grad_act, const ep_fp8_rows_t* pre,
                                        const float* row_weights, int F, const ep_fp8_rows_t* grad_pre,
                                        float* grad_row_weights, int num_sms, ep_stream_t stream) {

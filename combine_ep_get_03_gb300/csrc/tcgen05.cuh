@@ -46,6 +46,11 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
 // A tensor map over bytes [planes][rows][width] (2-D where planes is 0), box
 // 128 x box_rows, 128-byte swizzle.
 cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
+// The same over 4-bit codes [planes][rows][width], two a byte, box 128 x
+// box_rows: shared memory gets 8 bytes of codes and 8 unused bytes for every 16
+// channels, as the tensor cores take 4-bit operands beside 8-bit ones.  The
+// transaction counts the codes' bytes.  base is 32-byte aligned.
+cudaError_t make_e2m1_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
 // The same over bf16 [rows][width], box 64 x box_rows.
 cudaError_t make_bf16_map(CUtensorMap* map, const void* base, int width, long long rows, int box_rows);
 
@@ -136,6 +141,26 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
       : "r"(addr)
       : "memory");
 }
+// The same for 16 and for 8 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr)
+               : "memory");
+}
+// One word to four consecutive columns of the warp's 32 lanes, and the wait for it.
+__device__ __forceinline__ void tmem_fill4(uint32_t addr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" : : "r"(addr), "r"(v) : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" : : : "memory");
+}
 // Waits for this thread's loads; `v` are registers that one of them fills, so
 // that nothing reads them before.
 __device__ __forceinline__ void tmem_load_wait(uint32_t* v) {
@@ -145,6 +170,14 @@ __device__ __forceinline__ void tmem_load_wait(uint32_t* v) {
                  "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
                  "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
                  "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_load_wait16(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
 }
@@ -182,6 +215,37 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
       :
       : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ MMA with scales in TMEM
+//
+// e2m1 x e4m3 with a power of two for every 32 channels of an operand's row,
+// eight bits each (2^(b - 127)).  Scales of 128 rows and 128 channels are 512
+// bytes in shared memory, byte 16 (row % 32) + 4 (row / 32) + channels / 32; a
+// copy lays them into four TMEM columns, and the descriptor picks the byte that
+// an MMA of 32 channels takes.
+
+// Operand descriptor of such a block of scales (no swizzle, rows of 16 bytes).
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
+}
+__device__ __forceinline__ void tmem_copy_scales(uint32_t addr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" : : "r"(addr), "l"(desc) : "memory");
+}
+// A e2m1 (a byte each, see the 4-bit tensor map), B e4m3, both with their long
+// axis along the contraction; `step`: the byte of both scales' words.
+__device__ __forceinline__ uint32_t mma_mx_desc(int M, int N, int step) {
+  return (static_cast<uint32_t>(step) << 4) | (5u << 7) | (static_cast<uint32_t>(N / 8) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(M / 16) << 24) | (static_cast<uint32_t>(step) << 29);
+}
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t a_scales,
+                                       uint32_t b_scales, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}\n"
+      :
+      : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u), "r"(a_scales), "r"(b_scales)
       : "memory");
 }
 // One lane of a converged warp, the same one every time.  Code that only this

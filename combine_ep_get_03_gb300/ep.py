@@ -83,6 +83,8 @@ def lib() -> ctypes.CDLL:
             L.ep_gate_backward.argtypes = [P, I, I64, P, I, I, I, I, F32, P, I, P, P, P, P, I64, I, P]
             L.ep_grouped_matmul.argtypes = [GP, RP, P, P, I, I, P, I, P]
             L.ep_grouped_matmul_swiglu.argtypes = [GP, RP, P, P, I, I, P, RP, RP, I, P]
+            L.ep_grouped_matmul_w4.argtypes = [GP, RP, P, P, I, I, P, I, P]
+            L.ep_grouped_matmul_w4_swiglu.argtypes = [GP, RP, P, P, I, I, P, RP, I, P]
             L.ep_grouped_swiglu_backward.argtypes = [GP, P, RP, P, I, RP, P, I, P]
             L.ep_grouped_weight_grad.argtypes = [GP, RP, I, RP, I, P, I, P]
             L.ep_status_str.argtypes = [I]
@@ -93,7 +95,7 @@ def lib() -> ctypes.CDLL:
                       "ep_em_layout_and_dispatch", "ep_em_dispatch", "ep_em_get_layout", "ep_em_combine",
                       "ep_get_buffer_size_hint", "ep_em_get_groups", "ep_em_combine_weights", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
                       "ep_grouped_matmul", "ep_grouped_matmul_swiglu", "ep_grouped_swiglu_backward",
-                      "ep_grouped_weight_grad",
+                      "ep_grouped_weight_grad", "ep_grouped_matmul_w4", "ep_grouped_matmul_w4_swiglu",
                       "ep_get_device_status", "ep_check_wait_timeout", "ep_get_dispatch_layout_noalloc"):
                 getattr(L, n).restype = I
             _lib = L
@@ -379,6 +381,7 @@ def ep_get_dispatch_layout_noalloc(num_ranks, num_experts, num_topk, topk_idx, n
 # These calls are short, so their checks are written for few attribute reads.
 
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_U8 = (torch.uint8,)
 _IDS, _MASK = (torch.int64, torch.int32), (torch.bool, torch.uint8)
 
 
@@ -575,6 +578,41 @@ def ep_grouped_matmul_swiglu(x, x_scales, w, w_scales, act, act_scales, group_co
     wp, sp = _expert_weights(w, w_scales, E, 2 * F, K, dev)
     _check(lib().ep_grouped_matmul_swiglu(g, xr, wp, sp, F, K, _optional(row_weights, rows, _F32, "row_weights", dev),
                                           ar, pr, num_sms, _stream_on(stream, dev)), "ep_grouped_matmul_swiglu")
+
+
+def _expert_weights4(w, w_scales, E, N, K, dev):
+    wp, sp = _dev_ptr(w, _U8, "w", dev), _dev_ptr(w_scales, _U8, "w_scales", dev)
+    if w.shape != (E, N, K >> 1):
+        raise ValueError(f"w must be [{E}, {N}, {K >> 1}] for 4-bit codes, got {list(w.shape)}")
+    if w_scales.shape != (E, (N + 127) >> 7, K >> 7, 512):
+        raise ValueError(f"w_scales must be [{E}, {(N + 127) >> 7}, {K >> 7}, 512], got {list(w_scales.shape)}")
+    return wp, sp
+
+
+def ep_grouped_matmul_w4(x, x_scales, w, w_scales, out, group_count, group_offset=None, device_status=None,
+                         num_sms: int = 0, stream=None) -> None:
+    """out = x @ w[e].T for the rows of every group: e4m3 x with 128-channel
+    scales, w [E, N, K/2] bytes of two e2m1 codes with an exponent for every 32
+    channels, w_scales [E, ceil(N/128), K/128, 512] bytes; bf16 out."""
+    dev = torch.cuda.current_device()
+    g, E, _, lay = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lay, "x", dev)
+    op, N = _bf16_rows(out, lay, "out", dev)
+    wp, sp = _expert_weights4(w, w_scales, E, N, K, dev)
+    _check(lib().ep_grouped_matmul_w4(g, xr, wp, sp, N, K, op, num_sms, _stream_on(stream, dev)), "ep_grouped_matmul_w4")
+
+
+def ep_grouped_matmul_w4_swiglu(x, x_scales, w, w_scales, act, act_scales, group_count, group_offset=None,
+                                row_weights=None, device_status=None, num_sms: int = 0, stream=None) -> None:
+    """act = row_weights * silu(gate) * up in e4m3 with scales, where (gate, up)
+    = x @ w[e].T, w [E, 2F, K/2] 4-bit codes with their exponents."""
+    dev = torch.cuda.current_device()
+    g, E, rows, lay = _groups(x, group_count, group_offset, device_status, "x", dev)
+    xr, K = _fp8_rows(x, x_scales, lay, "x", dev)
+    ar, F = _fp8_rows(act, act_scales, lay, "act", dev)
+    wp, sp = _expert_weights4(w, w_scales, E, 2 * F, K, dev)
+    _check(lib().ep_grouped_matmul_w4_swiglu(g, xr, wp, sp, F, K, _optional(row_weights, rows, _F32, "row_weights", dev),
+                                             ar, num_sms, _stream_on(stream, dev)), "ep_grouped_matmul_w4_swiglu")
 
 
 def ep_grouped_swiglu_backward(grad_act, pre, pre_scales, grad_pre, grad_pre_scales, group_count, group_offset=None,

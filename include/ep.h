@@ -525,7 +525,30 @@ ep_status_t ep_grouped_matmul_swiglu(const ep_groups_t* groups, const ep_fp8_row
                                      const ep_fp8_rows_t* act, const ep_fp8_rows_t* pre, int num_sms,
                                      ep_stream_t stream);
 
-/* Backward of that activation from its 8-bit checkpoint.
+/* The same products on 4-bit weights, for serving: out[r][n] = sum_k x[r][k]
+ * w[e][n][k] with w[e][n][k] = e2m1 code * 2^(its 32 channels' exponent - 127),
+ * summed in fp32.
+ * In:  w         dev [num_groups][N][K/2], 32-byte aligned: two e2m1 codes a byte,
+ *                the even channel in the low four bits; a code's bit 3 is the
+ *                sign, codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6.  N a multiple
+ *                of 8, K of 128.
+ *      w_scales  dev [num_groups][ceil(N/128)][K/128][512], 16-byte aligned: the
+ *                8-bit exponents of 128 rows and 128 channels together, that of
+ *                row n, channels [32 c, 32 c + 32) at byte 16 (n % 32) +
+ *                4 (n % 128 / 32) + c % 4 of block (n / 128, c / 4).  255 stands for
+ *                NaN.  Bytes of rows past N may hold anything.
+ * Out: out       dev bf16 [rows][N]. */
+ep_status_t ep_grouped_matmul_w4(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                                 const uint8_t* w_scales, int N, int K, void* out, int num_sms, ep_stream_t stream);
+
+/* The experts' first product on 4-bit weights with the activation in its
+ * epilogue: w as above with N = 2F (the gate's F rows, then the up projection's;
+ * F, K multiples of 128), row_weights and act as ep_grouped_matmul_swiglu. */
+ep_status_t ep_grouped_matmul_w4_swiglu(const ep_groups_t* groups, const ep_fp8_rows_t* x, const void* w,
+                                        const uint8_t* w_scales, int F, int K, const float* row_weights,
+                                        const ep_fp8_rows_t* act, int num_sms, ep_stream_t stream);
+
+/* Backward of the 8-bit product's activation from its 8-bit checkpoint.
  * In:  grad_act  dev bf16 [rows][F], the gradient of act;  pre and row_weights as
  *                ep_grouped_matmul_swiglu left and had them.
  * Out: grad_pre  e4m3 rows of width 2F: the gradient of the pre-activations,
