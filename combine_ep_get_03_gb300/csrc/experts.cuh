@@ -66,8 +66,11 @@ __device__ __forceinline__ int group_span(const GroupArgs& a, int g, long long* 
 // all of them, for the whole block; `sums` holds 32 words.  Groups that do not
 // overlap have rows / tile_rows + G tiles at most; counts that say more are cut
 // there (EP_ERR_CAPACITY), which also keeps prefix[G] times the column tiles,
-// bounded by the host for that many, within 32 bits.
-__device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows, unsigned* prefix, unsigned* sums) {
+// bounded by the host for that many, within 32 bits.  `each` sees every group's
+// row count, in some thread.
+template <typename Each>
+__device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows, unsigned* prefix, unsigned* sums,
+                                              Each each) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int per = (a.G + blockDim.x - 1) / blockDim.x;
   const int g0 = tid * per;
@@ -80,6 +83,7 @@ __device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows,
   for (int g = g0; g < g0 + per && g < a.G; ++g) {
     long long first;
     const int n = group_span(a, g, &first, blockIdx.x == 0);
+    each(n);
     const unsigned t = static_cast<unsigned>((static_cast<long long>(n) + tile_rows - 1) / tile_rows);
     prefix[g] = t;
     mine = add(mine, t);
@@ -109,6 +113,10 @@ __device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows,
     if (all > most && blockIdx.x == 0) latch_status(a.err, kErrCapacity);
   }
   __syncthreads();
+}
+
+__device__ __forceinline__ void groups_prefix(const GroupArgs& a, int tile_rows, unsigned* prefix, unsigned* sums) {
+  groups_prefix(a, tile_rows, prefix, sums, [](int) {});
 }
 
 // The group that item i (< prefix[G]) belongs to.

@@ -31,26 +31,27 @@ namespace {
 
 constexpr int kTileT = kTile4Rows, kBlockK = 128;
 constexpr int kChunks = kTileT / 16;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 8, kMaxAcc = 4;
 constexpr int kHalfBytes = 128 * kBlockK;  // codes of 128 weight rows, a byte each
 constexpr int kHalfLoad = kHalfBytes / 2;  // ... as the transaction counts them
 constexpr int kScaleBytes = 512;           // exponents of 128 weight rows
-constexpr int kTokenBytes = kTileT * kBlockK;
-constexpr int kStageBytes = 2 * kHalfBytes + kTokenBytes + 2 * kScaleBytes;
-static_assert(kStageBytes % 1024 == 0 && kTokenBytes % 1024 == 0, "swizzled operands start at 1024-byte boundaries");
+// a stage: both halves, their exponents, the tokens; swizzled operands start at 1024-byte boundaries
+constexpr int kTokens = 2 * kHalfBytes + 2 * kScaleBytes;
+static_assert(kTokens % 1024 == 0 && 16 * kBlockK % 1024 == 0, "");
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and a scale warp are the third warpgroup
 constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 232, kOtherRegisters = 40;
 static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegisters <= kThreads * kLaunchRegisters, "");
 constexpr uint32_t kTmemColumns = 512;
-constexpr uint32_t kAccColumns = 2 * kTileT, kWeightScales = 2 * kAccColumns, kTokenScales = kWeightScales + 16;
+constexpr uint32_t kWeightScales = 4 * kTileT, kTokenScales = kWeightScales + 16;
 static_assert(kTokenScales + 4 <= kTmemColumns, "");
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 16;  // blocks of k whose scales are kept: more than stages and accumulators together
+static_assert(kMaxStages + kMaxAcc < kScaleSlots, "");
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], amax_full[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kMaxAcc], acc_empty[kMaxAcc], amax_full[2];
   uint32_t tmem;
-  int quit;
+  int quit, columns;
   unsigned sums[32];
   alignas(16) float x_scale[kScaleSlots][kTileT];
   float amax[2][2][4][kTileT / 2];  // [tile parity][half][warp][token]
@@ -63,7 +64,12 @@ struct Tile {
   int columns;    // ... rounded up to 16
 };
 
-// A group's tiles have about as many rows each.
+// Rows of the tiles of a group of `count` rows (the last may have fewer): about
+// as many in each, a multiple of 16, which an MMA's columns are.
+__device__ __forceinline__ int rows_per_tile(int count, int tiles_m) {
+  return tiles_m ? ((count + tiles_m - 1) / tiles_m + 15) & ~15 : 16;
+}
+
 __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* prefix, int tiles_n, unsigned t) {
   const int g = find_group(prefix, a.G, t / static_cast<unsigned>(tiles_n));
   Tile r;
@@ -74,7 +80,7 @@ __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* pref
   r.group = g;
   r.n = tiles_m ? static_cast<int>(local / static_cast<unsigned>(tiles_m)) : 0;
   const int m = static_cast<int>(local) - r.n * tiles_m;
-  const int per = tiles_m ? ((count + tiles_m - 1) / tiles_m + 15) / 16 * 16 : 0;
+  const int per = rows_per_tile(count, tiles_m);
   r.row = start + static_cast<long long>(m) * per;
   r.rows = tiles_m ? max(0, min(per, count - m * per)) : 0;
   r.columns = max(16, (r.rows + 15) & ~15);  // an MMA has 16 at least
@@ -86,28 +92,32 @@ __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* pref
 template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grouped_matmul_w4(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const Matmul4Args p) {
+                        const Matmul4Args p, uint32_t smem_bytes) {
   extern __shared__ unsigned char raw[];
-  unsigned char* stages = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared& s = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  Shared& s = *reinterpret_cast<Shared*>(raw);
   unsigned* prefix = reinterpret_cast<unsigned*>(&s + 1);
+  unsigned char* stages = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(prefix + p.groups.G + 1) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* quit = &s.quit;
   int* err = p.groups.err;
 
   if (threadIdx.x == 0) {
     // the loading thread's arrival and one of each of the scale warp's lanes
-    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1 + 32), mbar_init(&s.empty[i], 1);
-    for (int i = 0; i < 2; ++i)
-      mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kEpilogueWarps), mbar_init(&s.amax_full[i], 4);
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&s.full[i], 1 + 32), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < kMaxAcc; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kEpilogueWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.amax_full[i], 4);
     s.quit = 0;
+    s.columns = 16;
     mbar_init_fence();
     prefetch_map(&map_x);
     prefetch_map(&map_w);
   }
   if (warp == kEpilogueWarps + 1) tmem_alloc(&s.tmem, kTmemColumns);
+  __syncthreads();
   after_previous();
-  groups_prefix(p.groups, kTileT, prefix, s.sums);
+  groups_prefix(p.groups, kTileT, prefix, s.sums,
+                [&](int n) { if (n) atomicMax(&s.columns, rows_per_tile(n, (n + kTileT - 1) / kTileT)); });
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -118,6 +128,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
 
+  // As many stages as fit beside the largest tile's tokens, and four accumulators
+  // where it has few.
+  const uint32_t widest = s.columns;
+  const uint32_t stage_bytes = kTokens + widest * kBlockK;
+  const uint32_t num_stages = min(static_cast<uint32_t>(kMaxStages),
+                                  (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
+  const uint32_t num_acc = widest * 2 * kMaxAcc <= kWeightScales ? kMaxAcc : 2;
+
   const int F = p.N >> 1;
   const int blocks_n = (p.N + 127) >> 7;
   const int tiles_n = kSwiglu ? F >> 7 : (blocks_n + 1) >> 1;
@@ -127,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kEpilogueWarps) {
     registers_down<kOtherRegisters>();
     if (warp == kEpilogueWarps) {
-      uint32_t it = 0;
+      uint32_t it = 0, st = 0, phase = 0;  // stage and its round
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
@@ -136,15 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned char* scales = p.w_scales + (static_cast<long long>(c.group) * blocks_n + block0) * blocks_k * kScaleBytes;
         const long long second = static_cast<long long>(block1 - block0) * blocks_k * kScaleBytes;
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-          const int st = it % kStages;
-          if (it >= kStages) {
-            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
+          if (it >= num_stages) {
+            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], phase ^ 1, quit, err));
             if (!ok) break;
           }
           if (elect_one()) {
-            unsigned char* a = stages + st * kStageBytes;
-            unsigned char* b = a + 2 * kHalfBytes;
-            unsigned char* f = b + kTokenBytes;
+            unsigned char* a = stages + st * stage_bytes;
+            unsigned char* f = a + 2 * kHalfBytes;
+            unsigned char* b = a + kTokens;
             mbar_arrive_expect_tx(&s.full[st], halves * (kHalfLoad + kScaleBytes) + c.columns * kBlockK);
             tma_load_3d(a, &map_w, kb * kBlockK, block0 * 128, c.group, &s.full[st]);
             if (halves == 2) tma_load_3d(a + kHalfBytes, &map_w, kb * kBlockK, block1 * 128, c.group, &s.full[st]);
@@ -155,76 +172,82 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(b + q * kBlockK, &map_x, kb * kBlockK, static_cast<int>(c.row) + q, &s.full[st]);
           }
           __syncwarp();
+          if (++st == num_stages) st = 0, phase ^= 1;
         }
       }
       // no load may outlive the block: wait for the last fill of every stage
-      for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) {
+      for (uint32_t i = it < num_stages ? 0 : it - num_stages; i < it; ++i) {
         int none = 0;
-        wait_or_quit(&s.full[i % kStages], (i / kStages) & 1, &none, err);
+        wait_or_quit(&s.full[i % num_stages], (i / num_stages) & 1, &none, err);
       }
     } else if (warp <= kEpilogueWarps + 2) {
-      const int ac = warp - kEpilogueWarps - 1;  // the warp's accumulator: even or odd blocks of k
+      const uint32_t odd = warp - kEpilogueWarps - 1;  // the warp issues the even or the odd blocks of k
       const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
-      const uint64_t first_scales = scale_desc(smem_u32(stages) + 2 * kHalfBytes + kTokenBytes);
-      const uint32_t a_scales = tmem + kWeightScales + ac * 8, b_scales = tmem + kTokenScales;
-      uint32_t it = 0, used = 0;  // blocks of k, and those of this warp
+      const uint64_t first_scales = scale_desc(smem_u32(stages) + 2 * kHalfBytes);
+      const uint32_t a_scales = tmem + kWeightScales + odd * 8, b_scales = tmem + kTokenScales;
+      uint32_t it = 0, st = 0, phase = 0, last = 0, last_phase = 0;
+      bool used = false;
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
         const int halves = kSwiglu || 2 * c.n + 1 < blocks_n ? 2 : 1;
         const uint32_t desc = mma_mx_desc(128, c.columns, 0);
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-          if ((it & 1) != static_cast<uint32_t>(ac)) continue;
-          const int st = it % kStages;
-          ok = __all_sync(kFullMask, (it < 2 || wait_or_quit(&s.acc_empty[ac], ((it >> 1) & 1) ^ 1, quit, err)) &&
-                                         wait_or_quit(&s.full[st], (it / kStages) & 1, quit, err));
+          const uint32_t at = st, round = phase;
+          if (++st == num_stages) st = 0, phase ^= 1;
+          if ((it & 1) != odd) continue;
+          const uint32_t ac = it & (num_acc - 1), turn = (it / num_acc) & 1;
+          ok = __all_sync(kFullMask, (it < num_acc || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err)) &&
+                                         wait_or_quit(&s.full[at], round, quit, err));
           if (!ok) break;
           tmem_fence_after();
           if (elect_one()) {
             // descriptors count 16-byte units; 32 channels are two
-            const uint64_t a = first + st * (kStageBytes >> 4), b = a + (2 * kHalfBytes >> 4);
-            const uint64_t f = first_scales + st * (kStageBytes >> 4);
-            const uint32_t d = tmem + ac * kAccColumns;
+            const uint64_t a = first + at * (stage_bytes >> 4), b = a + (kTokens >> 4);
+            const uint64_t f = first_scales + at * (stage_bytes >> 4);
+            const uint32_t d = tmem + ac * 2 * widest;
             for (int h = 0; h < halves; ++h) {
               tmem_copy_scales(a_scales + 4 * h, f + h * (kScaleBytes >> 4));
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_mx(d + h * kTileT, a + h * (kHalfBytes >> 4) + 2 * j, b + 2 * j,
+                mma_mx(d + h * widest, a + h * (kHalfBytes >> 4) + 2 * j, b + 2 * j,
                        desc | (static_cast<uint32_t>(j) << 4) | (static_cast<uint32_t>(j) << 29), a_scales + 4 * h,
                        b_scales, j > 0);
             }
             mma_commit(&s.acc_full[ac]);
-            mma_commit(&s.empty[st]);
+            mma_commit(&s.empty[at]);
           }
           __syncwarp();
-          ++used;
+          used = true;
+          last = ac;
+          last_phase = turn;
         }
       }
       // nor may an MMA: its last accumulator is complete before TMEM goes back
       if (used) {
         int none = 0;
-        wait_or_quit(&s.acc_full[ac], (used - 1) & 1, &none, err);
+        wait_or_quit(&s.acc_full[last], last_phase, &none, err);
       }
     } else {
       // the tokens' scales of every block of k, with its operands
-      uint32_t it = 0;
+      uint32_t it = 0, st = 0, phase = 0;
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
         const float* sx = p.x.scales + (c.row + lane) * p.x.row_stride;
         const long long step = 32 * p.x.row_stride;
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-          const int st = it % kStages, slot = it % kScaleSlots;
-          if (it >= kStages) {
-            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], ((it / kStages) & 1) ^ 1, quit, err));
+          if (it >= num_stages) {
+            ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], phase ^ 1, quit, err));
             if (!ok) break;
           }
-          const uint32_t dst = smem_u32(&s.x_scale[slot][lane]);
+          const uint32_t dst = smem_u32(&s.x_scale[it % kScaleSlots][lane]);
 #pragma unroll
           for (int j = 0; j < (kTileT + 31) / 32; ++j)
             if (32 * j + lane < c.rows) copy_async4(dst + j * 128, sx + j * step, true);
           copy_async_arrive(&s.full[st]);
           sx += p.x.group_stride;
+          if (++st == num_stages) st = 0, phase ^= 1;
         }
       }
       asm volatile("cp.async.wait_all;" : : : "memory");
@@ -247,39 +270,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kTileT; ++j) acc[j] = 0.0f;
       for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-        const int ac = it & 1;
-        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it >> 1) & 1, quit, err));
+        const uint32_t ac = it & (num_acc - 1);
+        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it / num_acc) & 1, quit, err));
         if (!ok) break;
         tmem_fence_after();
-        const uint32_t d = lanes + ac * kAccColumns + (kSwiglu ? first : half * kTileT);
-        uint32_t v[2][16];
-        auto load = [&](int q, uint32_t* to) {
+        const uint32_t d = lanes + ac * 2 * widest + (kSwiglu ? first : half * widest);
+        const float* fx = s.x_scale[it % kScaleSlots] + first;  // of a row past the group's end: anything
+        // 64 columns are on their way at a time; the accumulator goes back as soon as
+        // the last are here
+        uint32_t v[4][16];
+        auto load = [&](int q) {
+          if (q >= chunks) return;
           if constexpr (kSwiglu) {
-            tmem_load8(d + 8 * q, to);
-            tmem_load8(d + kTileT + 8 * q, to + 8);
+            tmem_load8(d + 8 * q, v[q & 3]);
+            tmem_load8(d + widest + 8 * q, v[q & 3] + 8);
           } else {
-            tmem_load16(d + 16 * q, to);
+            tmem_load16(d + 16 * q, v[q & 3]);
           }
         };
-        const float* fx = s.x_scale[it % kScaleSlots] + first;  // of a row past the group's end: anything
-        load(0, v[0]);
+        auto release = [&]() {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
+        };
+        auto add = [&](int q) {
+          if (q >= chunks) return;
 #pragma unroll
-        for (int q = 0; q < kChunks; ++q) {
-          if (q < chunks) {
-            tmem_load_wait16(v[q & 1]);
-            if (q + 1 < chunks) {
-              load(q + 1, v[(q + 1) & 1]);
-            } else {
-              tmem_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float f = fx[kSwiglu ? 8 * q + (j & 7) : 16 * q + j];
-              acc[16 * q + j] = fmaf(__uint_as_float(v[q & 1][j]), f, acc[16 * q + j]);
-            }
+          for (int j = 0; j < 16; ++j) {
+            const float f = fx[kSwiglu ? 8 * q + (j & 7) : 16 * q + j];
+            acc[16 * q + j] = fmaf(__uint_as_float(v[q & 3][j]), f, acc[16 * q + j]);
           }
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load(q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_load_wait16(v[q]);
+        if (chunks <= 4) {
+          release();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) add(q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) add(q), load(q + 4);
+          add(3);
+#pragma unroll
+          for (int q = 4; q < kChunks; ++q) tmem_load_wait16(v[q & 3]);
+          release();
+#pragma unroll
+          for (int q = 4; q < kChunks; ++q) add(q);
         }
       }
       if (!ok) break;
@@ -344,11 +382,17 @@ cudaError_t launch_grouped_matmul_w4(const Matmul4Args& p, int sms, cudaStream_t
   if (e == cudaSuccess) e = make_e2m1_map(&map_w, p.w, p.K, p.N, p.groups.G, 128);
   if (e != cudaSuccess) return e;
   const bool swiglu = p.act.data != nullptr;
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared) + sizeof(unsigned) * (p.groups.G + 1);
+  int device = 0, smem = 0;  // all of it: the kernel decides on the stages
+  if ((e = cudaGetDevice(&device)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
+    return e;
+  const size_t least = sizeof(Shared) + sizeof(unsigned) * (p.groups.G + 1) + 1023 + 2 * (kTokens + kTileT * kBlockK);
+  if (least > static_cast<size_t>(smem)) return cudaErrorInvalidValue;
   auto kernel = swiglu ? k_grouped_matmul_w4<true> : k_grouped_matmul_w4<false>;
   static std::atomic<unsigned long long> ready[2];  // devices set up, a bit each
   if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[swiglu], kLaunchRegisters)) != cudaSuccess) return e;
-  return launch_early(kernel, 1, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p);
+  return launch_early(kernel, 1, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p,
+                      static_cast<uint32_t>(smem));
 }
 
 }  // namespace ep
