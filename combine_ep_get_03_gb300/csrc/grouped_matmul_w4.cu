@@ -27,11 +27,16 @@
 
 namespace ep {
 
+// Both halves' codes, their exponents; 16, 32 and 64 rows of tokens.
+struct Matmul4Maps {
+  CUtensorMap w, scales, x[3];
+};
+
 namespace {
 
 constexpr int kTileT = kTile4Rows, kBlockK = 128;
 constexpr int kChunks = kTileT / 16;
-constexpr int kMaxStages = 8, kMaxAcc = 4;
+constexpr int kMaxStages = 8;
 constexpr int kHalfBytes = 128 * kBlockK;  // codes of 128 weight rows, a byte each
 constexpr int kHalfLoad = kHalfBytes / 2;  // ... as the transaction counts them
 constexpr int kScaleBytes = 512;           // exponents of 128 weight rows
@@ -45,15 +50,18 @@ static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegister
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kWeightScales = 4 * kTileT, kTokenScales = kWeightScales + 16;
 static_assert(kTokenScales + 4 <= kTmemColumns, "");
-constexpr int kScaleSlots = 16;  // blocks of k whose scales are kept: more than stages and accumulators together
-static_assert(kMaxStages + kMaxAcc < kScaleSlots, "");
+// Blocks of k whose token scales are kept, and words for them.  A slot is filled
+// again when the MMAs of `kept - stages` blocks later are done; the warps that
+// add may then be reading those of three hand-overs before.
+constexpr int kScaleWords = 1792;
+static_assert(16 * kTileT <= kScaleWords && 32 * 48 <= kScaleWords, "");
 
 struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kMaxAcc], acc_empty[kMaxAcc], amax_full[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], amax_full[2], drained[2];
   uint32_t tmem;
   int quit, columns;
   unsigned sums[32];
-  alignas(16) float x_scale[kScaleSlots][kTileT];
+  alignas(16) float x_scale[kScaleWords];
   float amax[2][2][4][kTileT / 2];  // [tile parity][half][warp][token]
 };
 
@@ -87,12 +95,174 @@ __device__ __forceinline__ Tile tile_at(const GroupArgs& a, const unsigned* pref
   return r;
 }
 
+// What the warps that add take over: the TMEM address of the thread's first
+// column, the distance of the halves, the tokens' scales of block of k `it` (a
+// ring of `kept`), the barrier that gives the accumulator back.
+struct Handover {
+  uint32_t from, widest;
+  const float* scales;
+  uint32_t it, kept;
+  uint64_t* empty;
+};
+
+// Item m of a hand-over is chunk m % kOf, 16 columns, of its (m / kOf)th block of k.
+template <bool kSwiglu, int kOf>
+__device__ __forceinline__ void load_item(uint32_t (&v)[4][16], const Handover& h, int m, int items) {
+  if (m >= items) return;
+  const uint32_t from = h.from + (m / kOf) * 2 * h.widest;
+  if constexpr (kSwiglu) {
+    tmem_load8(from + 8 * (m % kOf), v[m & 3]);
+    tmem_load8(from + h.widest + 8 * (m % kOf), v[m & 3] + 8);
+  } else {
+    tmem_load16(from + 16 * (m % kOf), v[m & 3]);
+  }
+}
+
+template <bool kSwiglu, int kOf>
+__device__ __forceinline__ void add_item(float (&acc)[16 * kOf], const uint32_t (&v)[4][16], const Handover& h, int m,
+                                         int items) {
+  if (m >= items) return;
+  // scales of rows past the group's end are anything
+  const float4* f = reinterpret_cast<const float4*>(h.scales + ((h.it + m / kOf) % h.kept) * h.widest) +
+                    (m % kOf) * (kSwiglu ? 2 : 4);
+#pragma unroll
+  for (int j = 0; j < (kSwiglu ? 2 : 4); ++j) {
+    const float4 s4 = f[j];
+    const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 16 * (m % kOf) + 4 * j + i;
+      acc[at] = fmaf(__uint_as_float(v[m & 3][4 * j + i]), sc[i], acc[at]);
+      if constexpr (kSwiglu) acc[at + 8] = fmaf(__uint_as_float(v[m & 3][8 + 4 * j + i]), sc[i], acc[at + 8]);
+    }
+  }
+}
+
+__device__ __forceinline__ void release(const Handover& h) {
+  tmem_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(h.empty);
+}
+
+// Adds a hand-over's items, `kMost` at most: 64 columns are on their way at a
+// time, and the accumulator goes back as soon as the last are here.
+template <bool kSwiglu, int kOf, int kMost>
+__device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, int items) {
+  uint32_t v[4][16];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) load_item<kSwiglu, kOf>(v, h, m, items);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) tmem_load_wait16(v[m]);
+  if (kMost <= 4 || items <= 4) {
+    release(h);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) add_item<kSwiglu, kOf>(acc, v, h, m, items);
+  } else {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      add_item<kSwiglu, kOf>(acc, v, h, m, items);
+      if (m + 4 < kMost) load_item<kSwiglu, kOf>(v, h, m + 4, items);
+    }
+#pragma unroll
+    for (int m = 4; m < kMost; ++m) tmem_load_wait16(v[m & 3]);
+    release(h);
+#pragma unroll
+    for (int m = 4; m < kMost; ++m) add_item<kSwiglu, kOf>(acc, v, h, m, items);
+  }
+}
+
+// What all warps know of the launch.
+struct Launch {
+  uint32_t tmem, widest, acc_columns, kept;
+  int per, tiles_n, blocks_k;
+  unsigned tiles;
+};
+
+// The warps that add, in a launch whose tiles have up to kOf chunks of 16 tokens.
+template <bool kSwiglu, int kOf>
+__device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const unsigned* prefix, const Launch& l) {
+  constexpr int kColumns = 16 * kOf;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2, quarter = warp & 3;
+  const int in_half = quarter * 32 + lane;  // the thread's weight row in its half
+  volatile int* quit = &s.quit;
+  int* err = p.groups.err;
+  const int F = p.N >> 1;
+  uint32_t it = 0, group = 0;  // blocks of k and hand-overs of all tiles
+  int turn = 0;
+  bool ok;
+  for (unsigned t = blockIdx.x; t < l.tiles; t += gridDim.x, turn ^= 1) {
+    const Tile c = tile_at(p.groups, prefix, l.tiles_n, t);
+    // a warp's columns: all of its half's, or half of both halves' (SwiGLU: 8
+    // tokens' gates, then their up projections)
+    const int first = kSwiglu ? half * (c.columns >> 1) : 0;
+    const uint32_t from = l.tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kSwiglu ? first : half * l.widest);
+    float acc[kColumns];
+#pragma unroll
+    for (int j = 0; j < kColumns; ++j) acc[j] = 0.0f;
+    for (int kb = 0; kb < l.blocks_k; ++group) {
+      const uint32_t ac = group & 1;
+      const int n = min(l.per, l.blocks_k - kb);
+      ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (group >> 1) & 1, quit, err));
+      if (!ok) return;
+      tmem_fence_after();
+      const Handover h{from + ac * l.acc_columns, l.widest, s.x_scale + first, it, l.kept, &s.acc_empty[ac]};
+      take<kSwiglu, kOf, kOf == 3 ? 6 : kOf < 3 ? 4 : kOf>(acc, h, kOf == kChunks ? c.columns >> 4 : n * kOf);
+      kb += n;
+      it += n;
+    }
+    if constexpr (!kSwiglu) {
+      const int n = c.n * 256 + half * 128 + in_half;
+      uint16_t* o = p.out + c.row * p.N + n;
+      if (n < p.N) {
+#pragma unroll
+        for (int j = 0; j < kColumns; ++j)
+          if (j < c.rows) o[static_cast<long long>(j) * p.N] = static_cast<uint16_t>(pack_bf16x2(acc[j], 0.0f));
+      }
+    } else {
+      const int mine = max(0, min(c.columns >> 1, c.rows - first));  // live tokens of this warp
+      const long long row = c.row + first;
+      float (*amax)[kTileT / 2] = s.amax[turn][half];
+      float w[2] = {1.0f, 1.0f};
+      if (p.row_weights) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (32 * i + lane < mine) w[i] = p.row_weights[row + 32 * i + lane];
+      }
+#pragma unroll
+      for (int j = 0; j < kColumns / 2; ++j) {
+        if (j < mine) {
+          const float g = acc[16 * (j >> 3) + (j & 7)], u = acc[16 * (j >> 3) + 8 + (j & 7)];
+          const float a = __fdividef(g, 1.0f + __expf(-g)) * u * __shfl_sync(kFullMask, w[j >> 5], j & 31);
+          acc[16 * (j >> 3) + (j & 7)] = a;
+          // a NaN does not enter the maximum
+          const unsigned most = __reduce_max_sync(kFullMask, __float_as_uint(fmaxf(fabsf(a), 0.0f)));
+          if (lane == 0) amax[quarter][j] = __uint_as_float(most);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.amax_full[half]);
+      ok = __all_sync(kFullMask, wait_or_quit(&s.amax_full[half], turn, quit, err));
+      if (!ok) return;
+      unsigned char* o = p.act.data + row * F + c.n * 128 + in_half;
+#pragma unroll
+      for (int j = 0; j < kColumns / 2; ++j) {
+        if (j < mine) {
+          float inv;
+          const float sc = group_scale(fmaxf(fmaxf(amax[0][j], amax[1][j]), fmaxf(amax[2][j], amax[3][j])), &inv);
+          if (quarter == 0 && lane == (j & 31)) *p.act.scale(row + j, c.n) = sc;
+          o[static_cast<long long>(j) * F] = static_cast<unsigned char>(pack_e4m3x2(acc[16 * (j >> 3) + (j & 7)] * inv, 0.0f));
+        }
+      }
+    }
+  }
+}
+
 }  // namespace
 
 template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_grouped_matmul_w4(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const Matmul4Args p, uint32_t smem_bytes) {
+    k_grouped_matmul_w4(const __grid_constant__ Matmul4Maps maps, const Matmul4Args p, uint32_t smem_bytes) {
   extern __shared__ unsigned char raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
   unsigned* prefix = reinterpret_cast<unsigned*>(&s + 1);
@@ -105,13 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     // the loading thread's arrival and one of each of the scale warp's lanes
     for (int i = 0; i < kMaxStages; ++i) mbar_init(&s.full[i], 1 + 32), mbar_init(&s.empty[i], 1);
-    for (int i = 0; i < kMaxAcc; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], kEpilogueWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(&s.amax_full[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.acc_empty[i], kEpilogueWarps), mbar_init(&s.amax_full[i], 4), mbar_init(&s.drained[i], 1);
     s.quit = 0;
     s.columns = 16;
     mbar_init_fence();
-    prefetch_map(&map_x);
-    prefetch_map(&map_w);
+    prefetch_map(&maps.x[0]);
+    prefetch_map(&maps.scales);
+    prefetch_map(&maps.w);
   }
   if (warp == kEpilogueWarps + 1) tmem_alloc(&s.tmem, kTmemColumns);
   __syncthreads();
@@ -122,19 +292,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
+  // As many stages as fit beside the largest tile's tokens; an accumulator holds
+  // several blocks of k where the tiles have few.
+  const uint32_t widest = s.columns;
+  const uint32_t stage_bytes = kTokens + widest * kBlockK;
+  const uint32_t num_stages = min(static_cast<uint32_t>(kMaxStages),
+                                  (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
+  const int per = widest <= 16 ? 4 : widest <= 48 ? 2 : 1;
+  const uint32_t acc_columns = per * 2 * widest;
+  const uint32_t kept = per == 1 ? 16 : 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&s.acc_full[i], per);
+    mbar_init_fence();
+  }
   // the tokens' scales inside the MMA are 2^0: theirs are applied behind it
   if (warp < 4) tmem_fill4(tmem + (static_cast<uint32_t>(warp * 32) << 16) + kTokenScales, 0x7f7f7f7fu);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-
-  // As many stages as fit beside the largest tile's tokens, and four accumulators
-  // where it has few.
-  const uint32_t widest = s.columns;
-  const uint32_t stage_bytes = kTokens + widest * kBlockK;
-  const uint32_t num_stages = min(static_cast<uint32_t>(kMaxStages),
-                                  (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
-  const uint32_t num_acc = widest * 2 * kMaxAcc <= kWeightScales ? kMaxAcc : 2;
 
   const int F = p.N >> 1;
   const int blocks_n = (p.N + 127) >> 7;
@@ -149,10 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
-        const int block0 = kSwiglu ? c.n : 2 * c.n, block1 = kSwiglu ? c.n + (F >> 7) : 2 * c.n + 1;
-        const int halves = block1 < blocks_n ? 2 : 1;
-        const unsigned char* scales = p.w_scales + (static_cast<long long>(c.group) * blocks_n + block0) * blocks_k * kScaleBytes;
-        const long long second = static_cast<long long>(block1 - block0) * blocks_k * kScaleBytes;
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           if (it >= num_stages) {
             ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], phase ^ 1, quit, err));
@@ -162,14 +333,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* a = stages + st * stage_bytes;
             unsigned char* f = a + 2 * kHalfBytes;
             unsigned char* b = a + kTokens;
-            mbar_arrive_expect_tx(&s.full[st], halves * (kHalfLoad + kScaleBytes) + c.columns * kBlockK);
-            tma_load_3d(a, &map_w, kb * kBlockK, block0 * 128, c.group, &s.full[st]);
-            if (halves == 2) tma_load_3d(a + kHalfBytes, &map_w, kb * kBlockK, block1 * 128, c.group, &s.full[st]);
-            bulk_load(f, scales + static_cast<long long>(kb) * kScaleBytes, kScaleBytes, &s.full[st]);
-            if (halves == 2)
-              bulk_load(f + kScaleBytes, scales + second + static_cast<long long>(kb) * kScaleBytes, kScaleBytes, &s.full[st]);
-            for (int q = 0; q < c.columns; q += 16)
-              tma_load_2d(b + q * kBlockK, &map_x, kb * kBlockK, static_cast<int>(c.row) + q, &s.full[st]);
+            uint64_t* bar = &s.full[st];
+            mbar_arrive_expect_tx(bar, 2 * (kHalfLoad + kScaleBytes) + c.columns * kBlockK);
+            if constexpr (kSwiglu) {
+              tma_load_4d(a, &maps.w, kb * kBlockK, c.n * 128, 0, c.group, bar);
+              tma_load_3d(f, &maps.scales, kb * (kScaleBytes / 4), c.n, c.group * 2, bar);
+            } else {
+              tma_load_3d(a, &maps.w, kb * kBlockK, c.n * 256, c.group, bar);
+              tma_load_2d(f, &maps.scales, kb * (kScaleBytes / 4), c.group * blocks_n + 2 * c.n, bar);
+            }
+            int y = static_cast<int>(c.row);
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {
+              if (c.columns & (16 << i)) {
+                tma_load_2d(b, &maps.x[i], kb * kBlockK, y, bar);
+                b += (16 << i) * kBlockK;
+                y += 16 << i;
+              }
+            }
           }
           __syncwarp();
           if (++st == num_stages) st = 0, phase ^= 1;
@@ -185,19 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
       const uint64_t first_scales = scale_desc(smem_u32(stages) + 2 * kHalfBytes);
       const uint32_t a_scales = tmem + kWeightScales + odd * 8, b_scales = tmem + kTokenScales;
-      uint32_t it = 0, st = 0, phase = 0, last = 0, last_phase = 0;
-      bool used = false;
+      uint32_t it = 0, st = 0, phase = 0, group = 0;  // of all tiles: blocks of k, their stage, hand-overs
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
-        const int halves = kSwiglu || 2 * c.n + 1 < blocks_n ? 2 : 1;
         const uint32_t desc = mma_mx_desc(128, c.columns, 0);
-        for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-          const uint32_t at = st, round = phase;
+        for (int kb = 0, in = 0; kb < blocks_k; ++kb, ++it) {
+          const uint32_t at = st, round = phase, ac = group & 1, turn = (group >> 1) & 1, slot = in;
+          const bool first_turn = group < 2, last = kb + 1 == blocks_k;
           if (++st == num_stages) st = 0, phase ^= 1;
+          if (++in == per || last) in = 0, ++group;
           if ((it & 1) != odd) continue;
-          const uint32_t ac = it & (num_acc - 1), turn = (it / num_acc) & 1;
-          ok = __all_sync(kFullMask, (it < num_acc || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err)) &&
+          ok = __all_sync(kFullMask, (first_turn || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err)) &&
                                          wait_or_quit(&s.full[at], round, quit, err));
           if (!ok) break;
           tmem_fence_after();
@@ -205,29 +385,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             // descriptors count 16-byte units; 32 channels are two
             const uint64_t a = first + at * (stage_bytes >> 4), b = a + (kTokens >> 4);
             const uint64_t f = first_scales + at * (stage_bytes >> 4);
-            const uint32_t d = tmem + ac * 2 * widest;
-            for (int h = 0; h < halves; ++h) {
-              tmem_copy_scales(a_scales + 4 * h, f + h * (kScaleBytes >> 4));
+            const uint32_t d = tmem + ac * acc_columns + slot * 2 * widest;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) tmem_copy_scales(a_scales + 4 * h, f + h * (kScaleBytes >> 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 mma_mx(d + h * widest, a + h * (kHalfBytes >> 4) + 2 * j, b + 2 * j,
                        desc | (static_cast<uint32_t>(j) << 4) | (static_cast<uint32_t>(j) << 29), a_scales + 4 * h,
                        b_scales, j > 0);
-            }
+            // the last hand-over of a tile may hold fewer blocks than the barrier counts
+            if (last)
+              for (int i = slot + 1; i < per; ++i) mbar_arrive(&s.acc_full[ac]);
             mma_commit(&s.acc_full[ac]);
             mma_commit(&s.empty[at]);
           }
           __syncwarp();
-          used = true;
-          last = ac;
-          last_phase = turn;
         }
       }
-      // nor may an MMA: its last accumulator is complete before TMEM goes back
-      if (used) {
-        int none = 0;
-        wait_or_quit(&s.acc_full[last], last_phase, &none, err);
-      }
+      // nor may an MMA: all are done before TMEM goes back
+      int none = 0;
+      if (elect_one()) mma_commit(&s.drained[odd]);
+      __syncwarp();
+      wait_or_quit(&s.drained[odd], 0, &none, err);
     } else {
       // the tokens' scales of every block of k, with its operands
       uint32_t it = 0, st = 0, phase = 0;
@@ -241,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], phase ^ 1, quit, err));
             if (!ok) break;
           }
-          const uint32_t dst = smem_u32(&s.x_scale[it % kScaleSlots][lane]);
+          const uint32_t dst = smem_u32(&s.x_scale[(it % kept) * widest + lane]);
 #pragma unroll
           for (int j = 0; j < (kTileT + 31) / 32; ++j)
             if (32 * j + lane < c.rows) copy_async4(dst + j * 128, sx + j * step, true);
@@ -254,118 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     registers_up<kEpilogueRegisters>();
-    const int half = warp >> 2, quarter = warp & 3;
-    const int in_half = quarter * 32 + lane;  // the thread's weight row in its half
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint32_t it = 0;
-    int turn = 0;
-    bool ok = true;
-    for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x, turn ^= 1) {
-      const Tile c = tile_at(p.groups, prefix, tiles_n, t);
-      const int chunks = c.columns >> 4;
-      // a warp's columns: all of its half's, or half of both halves' (SwiGLU: 8
-      // tokens' gates, then their up projections)
-      const int first = kSwiglu ? half * (c.columns >> 1) : 0;
-      float acc[kTileT];
-#pragma unroll
-      for (int j = 0; j < kTileT; ++j) acc[j] = 0.0f;
-      for (int kb = 0; kb < blocks_k; ++kb, ++it) {
-        const uint32_t ac = it & (num_acc - 1);
-        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (it / num_acc) & 1, quit, err));
-        if (!ok) break;
-        tmem_fence_after();
-        const uint32_t d = lanes + ac * 2 * widest + (kSwiglu ? first : half * widest);
-        const float* fx = s.x_scale[it % kScaleSlots] + first;  // of a row past the group's end: anything
-        // 64 columns are on their way at a time; the accumulator goes back as soon as
-        // the last are here
-        uint32_t v[4][16];
-        auto load = [&](int q) {
-          if (q >= chunks) return;
-          if constexpr (kSwiglu) {
-            tmem_load8(d + 8 * q, v[q & 3]);
-            tmem_load8(d + widest + 8 * q, v[q & 3] + 8);
-          } else {
-            tmem_load16(d + 16 * q, v[q & 3]);
-          }
-        };
-        auto release = [&]() {
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
-        };
-        auto add = [&](int q) {
-          if (q >= chunks) return;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float f = fx[kSwiglu ? 8 * q + (j & 7) : 16 * q + j];
-            acc[16 * q + j] = fmaf(__uint_as_float(v[q & 3][j]), f, acc[16 * q + j]);
-          }
-        };
-#pragma unroll
-        for (int q = 0; q < 4; ++q) load(q);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_load_wait16(v[q]);
-        if (chunks <= 4) {
-          release();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) add(q);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 3; ++q) add(q), load(q + 4);
-          add(3);
-#pragma unroll
-          for (int q = 4; q < kChunks; ++q) tmem_load_wait16(v[q & 3]);
-          release();
-#pragma unroll
-          for (int q = 4; q < kChunks; ++q) add(q);
-        }
-      }
-      if (!ok) break;
-      if constexpr (!kSwiglu) {
-        const int n = c.n * 256 + half * 128 + in_half;
-        uint16_t* o = p.out + c.row * p.N + n;
-        if (n < p.N) {
-#pragma unroll
-          for (int j = 0; j < kTileT; ++j)
-            if (j < c.rows) o[static_cast<long long>(j) * p.N] = static_cast<uint16_t>(pack_bf16x2(acc[j], 0.0f));
-        }
-      } else {
-        const int mine = max(0, min(c.columns >> 1, c.rows - first));  // live tokens of this warp
-        const long long row = c.row + first;
-        float (*amax)[kTileT / 2] = s.amax[turn][half];
-        float w[2] = {1.0f, 1.0f};
-        if (p.row_weights) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (32 * i + lane < mine) w[i] = p.row_weights[row + 32 * i + lane];
-        }
-#pragma unroll
-        for (int j = 0; j < kTileT / 2; ++j) {
-          if (j < mine) {
-            const float g = acc[16 * (j >> 3) + (j & 7)], u = acc[16 * (j >> 3) + 8 + (j & 7)];
-            const float a = __fdividef(g, 1.0f + __expf(-g)) * u * __shfl_sync(kFullMask, w[j >> 5], j & 31);
-            acc[16 * (j >> 3) + (j & 7)] = a;
-            // a NaN does not enter the maximum
-            const unsigned most = __reduce_max_sync(kFullMask, __float_as_uint(fmaxf(fabsf(a), 0.0f)));
-            if (lane == 0) amax[quarter][j] = __uint_as_float(most);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.amax_full[half]);
-        ok = __all_sync(kFullMask, wait_or_quit(&s.amax_full[half], turn, quit, err));
-        if (!ok) break;
-        unsigned char* o = p.act.data + row * F + c.n * 128 + in_half;
-#pragma unroll
-        for (int j = 0; j < kTileT / 2; ++j) {
-          if (j < mine) {
-            float inv;
-            const float sc = group_scale(fmaxf(fmaxf(amax[0][j], amax[1][j]), fmaxf(amax[2][j], amax[3][j])), &inv);
-            if (quarter == 0 && lane == (j & 31)) *p.act.scale(row + j, c.n) = sc;
-            o[static_cast<long long>(j) * F] = static_cast<unsigned char>(pack_e4m3x2(acc[16 * (j >> 3) + (j & 7)] * inv, 0.0f));
-          }
-        }
-      }
-    }
+    const Launch l{tmem, widest, acc_columns, kept, per, tiles_n, blocks_k, tiles};
+    if (widest <= 16)
+      add_tiles<kSwiglu, 1>(p, s, prefix, l);
+    else if (widest <= 32)
+      add_tiles<kSwiglu, 2>(p, s, prefix, l);
+    else if (widest <= 48)
+      add_tiles<kSwiglu, 3>(p, s, prefix, l);
+    else
+      add_tiles<kSwiglu, kChunks>(p, s, prefix, l);
   }
   __syncwarp();
   tmem_fence_before();
@@ -377,11 +455,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 cudaError_t launch_grouped_matmul_w4(const Matmul4Args& p, int sms, cudaStream_t stream) {
-  CUtensorMap map_x, map_w;
-  cudaError_t e = make_byte_map(&map_x, p.x.data, p.K, p.groups.rows, 0, 16);
-  if (e == cudaSuccess) e = make_e2m1_map(&map_w, p.w, p.K, p.N, p.groups.G, 128);
-  if (e != cudaSuccess) return e;
   const bool swiglu = p.act.data != nullptr;
+  Matmul4Maps maps;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; e == cudaSuccess && i < 3; ++i) e = make_byte_map(&maps.x[i], p.x.data, p.K, p.groups.rows, 0, 16 << i);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t K = p.K, N = p.N, G = p.groups.G, blocks_n = (N + 127) / 128, row = K / 128 * kScaleBytes;
+  if (swiglu) {
+    // both halves at once: the gate's rows, then the up projection's
+    const cuuint64_t dims[4] = {K, N / 2, 2, G}, strides[3] = {K / 2, N / 2 * (K / 2), N * (K / 2)};
+    const cuuint32_t box[4] = {kBlockK, 128, 2, 1};
+    e = make_tensor_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.w, 4, dims, strides, box, true);
+    const cuuint64_t sdims[3] = {row / 4, blocks_n / 2, 2 * G}, sstrides[2] = {row, row * (blocks_n / 2)};
+    const cuuint32_t sbox[3] = {kScaleBytes / 4, 1, 2};
+    if (e == cudaSuccess)
+      e = make_tensor_map(&maps.scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.w_scales, 3, sdims, sstrides, sbox, false);
+  } else {
+    const cuuint64_t dims[3] = {K, N, G}, strides[2] = {K / 2, N * (K / 2)};
+    const cuuint32_t box[3] = {kBlockK, 256, 1};
+    e = make_tensor_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.w, 3, dims, strides, box, true);
+    const cuuint64_t sdims[2] = {row / 4, blocks_n * G}, sstrides[1] = {row};
+    const cuuint32_t sbox[2] = {kScaleBytes / 4, 2};
+    if (e == cudaSuccess)
+      e = make_tensor_map(&maps.scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.w_scales, 2, sdims, sstrides, sbox, false);
+  }
+  if (e != cudaSuccess) return e;
   int device = 0, smem = 0;  // all of it: the kernel decides on the stages
   if ((e = cudaGetDevice(&device)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
@@ -391,7 +489,7 @@ cudaError_t launch_grouped_matmul_w4(const Matmul4Args& p, int sms, cudaStream_t
   auto kernel = swiglu ? k_grouped_matmul_w4<true> : k_grouped_matmul_w4<false>;
   static std::atomic<unsigned long long> ready[2];  // devices set up, a bit each
   if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[swiglu], kLaunchRegisters)) != cudaSuccess) return e;
-  return launch_early(kernel, 1, dim3(sms), dim3(kThreads), smem, stream, map_x, map_w, p,
+  return launch_early(kernel, 1, dim3(sms), dim3(kThreads), smem, stream, maps, p,
                       static_cast<uint32_t>(smem));
 }
 

@@ -26,6 +26,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int u, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :
+      : "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                :
@@ -46,11 +54,10 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
 // A tensor map over bytes [planes][rows][width] (2-D where planes is 0), box
 // 128 x box_rows, 128-byte swizzle.
 cudaError_t make_byte_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
-// The same over 4-bit codes [planes][rows][width], two a byte, box 128 x
-// box_rows: shared memory gets 8 bytes of codes and 8 unused bytes for every 16
-// channels, as the tensor cores take 4-bit operands beside 8-bit ones.  The
-// transaction counts the codes' bytes.  base is 32-byte aligned.
-cudaError_t make_e2m1_map(CUtensorMap* map, const void* base, int width, long long rows, int planes, int box_rows);
+// A tensor map with any type, sizes (elements) and strides (bytes, of every
+// dimension but the first); `swizzle`: 128-byte swizzle.
+cudaError_t make_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                            const cuuint64_t* strides, const cuuint32_t* box, bool swizzle);
 // The same over bf16 [rows][width], box 64 x box_rows.
 cudaError_t make_bf16_map(CUtensorMap* map, const void* base, int width, long long rows, int box_rows);
 
