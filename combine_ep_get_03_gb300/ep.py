@@ -67,6 +67,8 @@ def lib() -> ctypes.CDLL:
             L.ep_em_dispatch.argtypes = [P, P, P, I, P, P, I64, I64, P, P, I, P]
             L.ep_em_get_layout.argtypes = [P, P, P, P]
             L.ep_em_combine.argtypes = [P, P, I64, P, I, P]
+            L.ep_em_combine_weighted.argtypes = [P, P, I64, P, P, I, P]
+            L.ep_em_combine_weighted_backward.argtypes = [P, P, P, I64, P, I, P, P, I64, P, I, P]
             L.ep_em_get_groups.argtypes = [P, P, P, P]
             L.ep_em_combine_weights.argtypes = [P, P, I64, P, P]
             L.ep_get_buffer_size_hint.argtypes = [I, I, I, I, I, I, I, I, P, P]
@@ -93,7 +95,8 @@ def lib() -> ctypes.CDLL:
                       "ep_dispatch", "ep_combine", "ep_layout_and_dispatch", "ep_low_latency_dispatch",
                       "ep_low_latency_combine", "ep_combine_ex", "ep_handle_set_topk_idx_bits",
                       "ep_em_layout_and_dispatch", "ep_em_dispatch", "ep_em_get_layout", "ep_em_combine",
-                      "ep_get_buffer_size_hint", "ep_em_get_groups", "ep_em_combine_weights", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
+                      "ep_get_buffer_size_hint", "ep_em_get_groups", "ep_em_combine_weights", "ep_em_combine_weighted",
+                      "ep_em_combine_weighted_backward", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
                       "ep_grouped_matmul", "ep_grouped_matmul_swiglu", "ep_grouped_swiglu_backward",
                       "ep_grouped_weight_grad", "ep_grouped_matmul_w4", "ep_grouped_matmul_w4_swiglu",
                       "ep_get_device_status", "ep_check_wait_timeout", "ep_get_dispatch_layout_noalloc"):
@@ -303,6 +306,34 @@ def ep_em_get_layout(h, num_experts: int, stream=None, check: bool = True):
 def ep_em_combine(h, y, out, num_sms: int = 0, stream=None) -> None:
     _check(lib().ep_em_combine(h, _ptr(y, (torch.bfloat16,), "y"), y.shape[0], _ptr(out, (torch.bfloat16,), "out"),
                                int(num_sms), _stream(stream)), "ep_em_combine")
+
+
+def ep_em_combine_weighted(h, y, topk_weights, out, num_sms: int = 0, stream=None) -> None:
+    """out[t] = the sum of topk_weights[t, j] y[row of (t, j)] over the unmasked entries."""
+    _check(lib().ep_em_combine_weighted(h, _ptr(y, (torch.bfloat16,), "y"), y.shape[0],
+                                        _ptr(topk_weights, (torch.float32,), "topk_weights"),
+                                        _ptr(out, (torch.bfloat16,), "out"), int(num_sms), _stream(stream)),
+           "ep_em_combine_weighted")
+
+
+def ep_em_combine_weighted_backward(h, grad_out, y, topk_weights, dtype: int, grad_y=None, grad_y_scales=None,
+                                    grad_topk_weights=None, num_sms: int = 0, stream=None) -> None:
+    """Gradients of ep_em_combine_weighted: of the rows (bf16, or e4m3 with
+    scales [H/128, scales_ld]) and of the weights; either may be None."""
+    fp8 = dtype == EP_FP8_E4M3
+    like = grad_y if grad_y is not None else y
+    if like is None:
+        raise ValueError("grad_y or y is required")
+    if fp8 and grad_y is not None and (grad_y_scales is None or grad_y_scales.dim() != 2):
+        raise ValueError("grad_y_scales must be a contiguous [H/128, scales_ld] tensor")
+    _check(lib().ep_em_combine_weighted_backward(
+        h, _ptr(grad_out, (torch.bfloat16,), "grad_out"), _ptr(y, (torch.bfloat16,), "y"), like.shape[0],
+        _ptr(topk_weights, (torch.float32,), "topk_weights"), int(dtype),
+        _ptr(grad_y, _FP8_BYTES if fp8 else (torch.bfloat16,), "grad_y"),
+        _ptr(grad_y_scales, (torch.float32,), "grad_y_scales") if fp8 else None,
+        grad_y_scales.shape[1] if fp8 and grad_y_scales is not None else 0,
+        _ptr(grad_topk_weights, (torch.float32,), "grad_topk_weights"), int(num_sms), _stream(stream)),
+        "ep_em_combine_weighted_backward")
 
 
 def ep_em_get_groups(h, group_offset=None, group_count=None, stream=None) -> None:
@@ -849,6 +880,39 @@ class Handle:
             raise ValueError(f"y must be [rows, {self.H}]")
         self._need(out, self.T_em * self.H, "out")
         ep_em_combine(self.ptr, y, out, num_sms, stream)
+
+    def em_combine_weighted(self, y, topk_weights, out, num_sms=0, stream=None):
+        if self.T_em is None:
+            raise RuntimeError("expert-major combine before any expert-major layout")
+        if y.dim() != 2 or y.shape[1] != self.H:
+            raise ValueError(f"y must be [rows, {self.H}]")
+        self._need(topk_weights, self.T_em * self.k, "topk_weights")
+        self._need(out, self.T_em * self.H, "out")
+        ep_em_combine_weighted(self.ptr, y, topk_weights, out, num_sms, stream)
+
+    def em_combine_weighted_backward(self, grad_out, y, topk_weights, dtype, grad_y=None, grad_y_scales=None,
+                                     grad_topk_weights=None, num_sms=0, stream=None):
+        if self.T_em is None:
+            raise RuntimeError("expert-major combine before any expert-major layout")
+        rows = None
+        for t, name in ((y, "y"), (grad_y, "grad_y")):
+            if t is None:
+                continue
+            if t.dim() != 2 or t.shape[1] != self.H:
+                raise ValueError(f"{name} must be [rows, {self.H}]")
+            if rows is not None and t.shape[0] != rows:
+                raise ValueError(f"y has {rows} rows, grad_y {t.shape[0]}")
+            rows = t.shape[0]
+        self._need(grad_out, self.T_em * self.H, "grad_out")
+        self._need(topk_weights, self.T_em * self.k, "topk_weights")
+        self._need(grad_topk_weights, self.T_em * self.k, "grad_topk_weights")
+        if dtype == EP_FP8_E4M3 and grad_y is not None:
+            if grad_y_scales is None or grad_y_scales.dim() != 2 or grad_y_scales.shape[0] != self.G:
+                raise ValueError(f"e4m3 rows need grad_y_scales [{self.G}, scales_ld]")
+            if grad_y_scales.shape[1] < rows:
+                raise ValueError("scales_ld must be >= the rows")
+        ep_em_combine_weighted_backward(self.ptr, grad_out, y, topk_weights, dtype, grad_y, grad_y_scales,
+                                        grad_topk_weights, num_sms, stream)
 
     def em_get_groups(self, group_offset=None, group_count=None, stream=None):
         self._need(group_offset, self.E + 1, "group_offset")

@@ -316,6 +316,34 @@ ep_status_t ep_em_get_layout(ep_handle_t h, int* num_recv_tokens_per_expert, int
 ep_status_t ep_em_combine(ep_handle_t h, const void* y, int64_t y_rows, void* out, int num_sms,
                           ep_stream_t stream);
 
+/* The same with the routing weights applied on the way back: for each token
+ * acc = fmaf(w, y, acc) over its unmasked entries in ascending expert id (k-index
+ * breaks ties), from +0.0, rounded to bf16 (nearest-even), as
+ * ep_low_latency_combine.  topk_weights dev fp32 [T][k]; those of masked entries
+ * are not used.  For experts whose rows do not carry their weight already
+ * (ep_em_combine with a weight in the first product's epilogue is the other way). */
+ep_status_t ep_em_combine_weighted(ep_handle_t h, const void* y, int64_t y_rows, const float* topk_weights, void* out,
+                                   int num_sms, ep_stream_t stream);
+
+/* Its gradient, through the handle's last expert-major layout.
+ * In:  grad_out      dev bf16 [T][H];  y  dev bf16 [rows][H] and topk_weights dev
+ *                    fp32 [T][k] as the forward call had them (y may be NULL
+ *                    without grad_topk_weights, topk_weights without grad_y).
+ * Out (either may be NULL):
+ *      grad_y        [rows][H] bf16, or e4m3 (dtype) with grad_y_scales dev fp32
+ *                    [H/128][scales_ld] as ep_em_dispatch lays them out: the
+ *                    entry's weight times its token's grad_out, multiplied in
+ *                    fp32 and quantised from there as dispatch quantises.
+ *                    Padding rows are not written.  Must not overlap y.
+ *      grad_topk_weights  dev fp32 [T][k]: the products of grad_out and y summed
+ *                    over the channels in fp32, 0 where masked.
+ * Entries whose row is at or past `rows` are skipped (gradient of the weight 0)
+ * and latch EP_ERR_CAPACITY. */
+ep_status_t ep_em_combine_weighted_backward(ep_handle_t h, const void* grad_out, const void* y, int64_t rows,
+                                            const float* topk_weights, ep_dtype_t dtype, void* grad_y,
+                                            float* grad_y_scales, int64_t scales_ld, float* grad_topk_weights,
+                                            int num_sms, ep_stream_t stream);
+
 /* Copy the last expert-major layout's groups to device memory, on `stream`
  * and without synchronising: what the grouped calls below take.
  * Out (each may be NULL): group_offset dev int32 [E+1] (first row of each
