@@ -5,6 +5,7 @@
 #include <cstdio>
 #include <cstdlib>
 
+#include "block_norm.cuh"
 #include "ep.h"
 #include "ep_internal.h"
 #include "experts.cuh"
@@ -67,6 +68,28 @@ bool gate_ok(const void* logits, ep_logits_t type, int64_t ld, int T, int E, int
 bool words16(const void* p, ep_logits_t type, int64_t ld, int E) {
   const int per = type == EP_LOGITS_FP32 ? 4 : 8;
   return E % per == 0 && ld % per == 0 && aligned(p, 16);
+}
+
+bool norm_ok(const ep_block_norm_t* n) {
+  return n && n->num_tokens >= 0 && n->hidden >= 8 && n->hidden % 8 == 0 && n->hidden <= ep::kBlockNormMaxHidden &&
+         (n->residual_type == EP_REAL_FP32 || n->residual_type == EP_REAL_BF16) &&
+         (n->weight_type == EP_REAL_FP32 || n->weight_type == EP_REAL_BF16) && aligned(n->post_weight, 16) &&
+         aligned(n->pre_weight, 16) && aligned(n->gate, 16);
+}
+
+ep::BlockNormArgs norm_args(const ep_block_norm_t* n) {
+  ep::BlockNormArgs a{};
+  a.T = n->num_tokens;
+  a.H = n->hidden;
+  a.eps = n->eps;
+  a.scale = n->residual_scale;
+  a.weight32 = n->weight_type == EP_REAL_FP32;
+  a.gate_per_token = n->gate && n->gate_per_token;
+  a.post = n->post_weight;
+  a.pre = n->pre_weight;
+  a.gate = n->gate;
+  a.mask = n->token_mask;
+  return a;
 }
 
 ep::GateArgs gate_args(const void* logits, ep_logits_t type, int64_t ld, const uint8_t* mask, int T, int E, int k,
@@ -298,6 +321,83 @@ ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_
   p.K = K;
   p.dw = static_cast<uint16_t*>(grad_w);
   return status_of(ep::launch_weight_grad(p, sms, s), "ep_grouped_weight_grad launch");
+}
+
+ep_status_t ep_block_norm_forward(const ep_block_norm_t* norm, const void* residual, const void* y, void* new_residual,
+                                  void* x, float* rstd, int num_sms, ep_stream_t stream) {
+  if (!norm_ok(norm)) return EP_ERR_INVALID_ARG;
+  const bool any = norm->num_tokens > 0;  // tensors without tokens have no address
+  if ((norm->pre_weight && any && !x) || (!norm->pre_weight && x)) return EP_ERR_INVALID_ARG;
+  if (any && (!residual || (y ? !new_residual : norm->post_weight || norm->gate || !x))) return EP_ERR_INVALID_ARG;
+  if (!aligned(residual, 16) || !aligned(y, 16) || !aligned(new_residual, 16) || !aligned(x, 16) || !aligned(rstd, 4))
+    return EP_ERR_INVALID_ARG;
+  if (!any) return EP_OK;
+  int sms = 0;
+  ep_status_t st = sm_count(num_sms, &sms);
+  if (st != EP_OK) return st;
+  ep::BlockNormArgs a = norm_args(norm);
+  a.residual = residual;
+  a.y = y;
+  a.new_residual = new_residual;
+  a.x = x;
+  a.rstd = rstd;
+  return status_of(ep::launch_block_norm(a, norm->residual_type == EP_REAL_FP32, sms, reinterpret_cast<cudaStream_t>(stream)),
+                   "ep_block_norm_forward launch");
+}
+
+ep_status_t ep_block_norm_workspace_bytes(int hidden, int64_t* bytes) {
+  if (hidden < 8 || hidden % 8 != 0 || hidden > ep::kBlockNormMaxHidden || !bytes) return EP_ERR_INVALID_ARG;
+  *bytes = static_cast<int64_t>(ep::kBlockNormMaxBlocks) * 3 * sizeof(float) * hidden;
+  return EP_OK;
+}
+
+ep_status_t ep_block_norm_backward(const ep_block_norm_t* norm, const void* new_residual, const void* y,
+                                   const float* rstd, const void* grad_new_residual, const void* grad_x,
+                                   void* grad_residual, void* grad_y, void* grad_gate, float* grad_post_weight,
+                                   float* grad_pre_weight, void* workspace, int num_sms, ep_stream_t stream) {
+  if (!norm_ok(norm)) return EP_ERR_INVALID_ARG;
+  const bool any = norm->num_tokens > 0;
+  const bool per_token = norm->gate && norm->gate_per_token;
+  if ((grad_gate && !norm->gate) || (grad_post_weight && !norm->post_weight) ||
+      (grad_pre_weight && (!norm->pre_weight || (any && !grad_x))) || (grad_x && !norm->pre_weight))
+    return EP_ERR_INVALID_ARG;
+  const bool block = grad_y || grad_gate || grad_post_weight;
+  if (any && ((grad_x && (!new_residual || !rstd)) || (block && norm->post_weight && (!y || !rstd)) || (grad_gate && !y)))
+    return EP_ERR_INVALID_ARG;
+  const bool sums = grad_pre_weight || grad_post_weight || (grad_gate && !per_token);
+  if (sums && any && !workspace) return EP_ERR_INVALID_ARG;
+  for (const void* p : {new_residual, y, grad_new_residual, grad_x, static_cast<const void*>(grad_residual),
+                        static_cast<const void*>(grad_y), static_cast<const void*>(grad_gate),
+                        static_cast<const void*>(grad_post_weight), static_cast<const void*>(grad_pre_weight),
+                        static_cast<const void*>(workspace)})
+    if (!aligned(p, 16)) return EP_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4)) return EP_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!any) {
+    cudaError_t e = cudaSuccess;
+    for (float* p : {grad_pre_weight, grad_post_weight, per_token ? nullptr : static_cast<float*>(grad_gate)})
+      if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(float) * norm->hidden, s);
+    return status_of(e, "ep_block_norm_backward memset");
+  }
+  if (!block && !grad_residual && !grad_pre_weight) return EP_OK;
+  int sms = 0;
+  ep_status_t st = sm_count(num_sms, &sms);
+  if (st != EP_OK) return st;
+  ep::BlockNormBackwardArgs a{};
+  a.n = norm_args(norm);
+  a.n.new_residual = const_cast<void*>(new_residual);
+  a.n.y = y;
+  a.n.rstd = const_cast<float*>(rstd);
+  a.grad_new = grad_new_residual;
+  a.grad_x = grad_x;
+  a.grad_residual = grad_residual;
+  a.grad_y = grad_y;
+  a.grad_gate = grad_gate;
+  a.grad_post = grad_post_weight;
+  a.grad_pre = grad_pre_weight;
+  a.partial = static_cast<float*>(workspace);
+  return status_of(ep::launch_block_norm_backward(a, norm->residual_type == EP_REAL_FP32, sms, s),
+                   "ep_block_norm_backward launch");
 }
 
 }  // extern "C"

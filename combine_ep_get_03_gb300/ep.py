@@ -24,6 +24,7 @@ EP_BF16, EP_FP8_E4M3 = 0, 1
 EP_LAYOUT_RANK_MAJOR, EP_LAYOUT_LOW_LATENCY, EP_LAYOUT_EXPERT_MAJOR = 0, 1, 2
 EP_LOGITS_FP32, EP_LOGITS_BF16 = 0, 1
 EP_GATE_SOFTMAX, EP_GATE_SIGMOID = 0, 1
+EP_REAL_FP32, EP_REAL_BF16 = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -35,9 +36,10 @@ class EPError(RuntimeError):
         self.status = status
 
 
-# ep_groups_t and ep_fp8_rows_t of include/ep.h, as the bytes of one struct
+# ep_groups_t, ep_fp8_rows_t and ep_block_norm_t of include/ep.h, as the bytes of one struct
 _GROUPS = struct.Struct("@PPiqqP")
 _FP8_ROWS = struct.Struct("@PPqq")
+_BLOCK_NORM = struct.Struct("@PPPPiiiiiff4x")
 
 
 def lib() -> ctypes.CDLL:
@@ -89,6 +91,9 @@ def lib() -> ctypes.CDLL:
             L.ep_grouped_matmul_w4_swiglu.argtypes = [GP, RP, P, P, I, I, P, RP, I, P]
             L.ep_grouped_swiglu_backward.argtypes = [GP, P, RP, P, I, RP, P, I, P]
             L.ep_grouped_weight_grad.argtypes = [GP, RP, I, RP, I, P, I, P]
+            L.ep_block_norm_forward.argtypes = [GP, P, P, P, P, P, I, P]
+            L.ep_block_norm_workspace_bytes.argtypes = [I, P]
+            L.ep_block_norm_backward.argtypes = [GP, P, P, P, P, P, P, P, P, P, P, P, I, P]
             L.ep_status_str.argtypes = [I]
             L.ep_status_str.restype = ctypes.c_char_p
             for n in ("ep_handle_create", "ep_handle_destroy", "ep_get_dispatch_layout", "ep_get_num_recv",
@@ -99,6 +104,7 @@ def lib() -> ctypes.CDLL:
                       "ep_em_combine_weighted_backward", "ep_gate_workspace_bytes", "ep_gate_forward", "ep_gate_backward",
                       "ep_grouped_matmul", "ep_grouped_matmul_swiglu", "ep_grouped_swiglu_backward",
                       "ep_grouped_weight_grad", "ep_grouped_matmul_w4", "ep_grouped_matmul_w4_swiglu",
+                      "ep_block_norm_forward", "ep_block_norm_workspace_bytes", "ep_block_norm_backward",
                       "ep_get_device_status", "ep_check_wait_timeout", "ep_get_dispatch_layout_noalloc"):
                 getattr(L, n).restype = I
             _lib = L
@@ -677,6 +683,108 @@ def ep_grouped_weight_grad(grad_out, grad_out_scales, x, x_scales, grad_w, group
     if grad_w.shape != (E, N, K):
         raise ValueError(f"grad_w must be [{E}, {N}, {K}], got {list(grad_w.shape)}")
     _check(lib().ep_grouped_weight_grad(g, yr, N, xr, K, gp, num_sms, _stream_on(stream, dev)), "ep_grouped_weight_grad")
+
+
+# ------------------------------------------------ the norms around a block
+
+_REALS = (torch.float32, torch.bfloat16)
+
+
+def _tokens(t, T, H, dtypes, name, dev):
+    """Device pointer of a contiguous [T, H] tensor."""
+    p = _dev_ptr(t, dtypes, name, dev)
+    if t.shape != (T, H):
+        raise ValueError(f"{name} must be [{T}, {H}], got {list(t.shape)}")
+    return p
+
+
+def _block_norm(residual, name, post_weight, pre_weight, gate, token_mask, eps, residual_scale, dev):
+    """ep_block_norm_t of a call on [T, H] tensors, T, H, whether the gate comes per token."""
+    if not isinstance(residual, torch.Tensor) or residual.dim() != 2 or residual.dtype not in _REALS:
+        raise ValueError(f"{name} must be a [T, H] fp32 or bf16 tensor")
+    T, H = residual.shape
+    per_token = gate is not None and gate.dim() == 2
+    kind, weights = None, []
+    for t, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (None if per_token else gate, "gate")):
+        if t is None:
+            weights.append(None)
+            continue
+        weights.append(_dev_ptr(t, _REALS, what, dev))
+        if t.shape != (H,):
+            raise ValueError(f"{what} must be [{H}]{' or [T, H]' if what == 'gate' else ''}, got {list(t.shape)}")
+        if kind is not None and t.dtype is not kind:
+            raise ValueError("post_weight, pre_weight and a gate [H] must have one dtype")
+        kind = t.dtype
+    if per_token:
+        weights[2] = _tokens(gate, T, H, _BF16, "gate", dev)
+    real = lambda d: EP_REAL_BF16 if d is torch.bfloat16 else EP_REAL_FP32  # noqa: E731
+    return _BLOCK_NORM.pack(*(w or 0 for w in weights), _optional(token_mask, T, _MASK, "token_mask", dev) or 0, T, H,
+                            per_token, real(residual.dtype), real(kind), eps, residual_scale), T, H, per_token
+
+
+def ep_block_norm_forward(residual, y, new_residual, x, rstd=None, post_weight=None, pre_weight=None, gate=None,
+                          eps: float = 1e-6, residual_scale: float = 1.0, token_mask=None, num_sms: int = 0,
+                          stream=None) -> None:
+    """new_residual = residual + residual_scale * gate * (norm(y) * post_weight)
+    and x = norm(new_residual) * pre_weight, norm(v) = v / sqrt(mean(v^2) + eps).
+
+    residual and new_residual [T, H] fp32 or bf16 (they may be one tensor); y
+    and x [T, H] bf16; weights [H] fp32 or bf16; gate [H], or [T, H] bf16.
+    post_weight, gate and pre_weight (with x) may be None; y None: no block
+    behind, x is the norm of residual.  rstd [2, T] fp32 keeps what the
+    backward pass needs."""
+    dev = torch.cuda.current_device()
+    n, T, H, _ = _block_norm(residual, "residual", post_weight, pre_weight, gate, token_mask, eps, residual_scale, dev)
+    if (x is None) != (pre_weight is None):
+        raise ValueError("x and pre_weight come together")
+    if y is None and (post_weight is not None or gate is not None or new_residual is not None):
+        raise ValueError("post_weight, gate and new_residual need y")
+    if y is None and x is None:
+        raise ValueError("y or x is required")
+    tokens = lambda t, dt, name: None if t is None else _tokens(t, T, H, dt, name, dev)  # noqa: E731
+    if y is not None and new_residual is None:
+        raise ValueError("new_residual is required")
+    _check(lib().ep_block_norm_forward(
+        n, _tokens(residual, T, H, _REALS, "residual", dev), tokens(y, _BF16, "y"),
+        tokens(new_residual, (residual.dtype,), "new_residual"), tokens(x, _BF16, "x"),
+        _optional(rstd, 2 * T, _F32, "rstd", dev), num_sms, _stream_on(stream, dev)), "ep_block_norm_forward")
+
+
+def ep_block_norm_workspace_bytes(hidden: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().ep_block_norm_workspace_bytes(hidden, ctypes.byref(n)), "ep_block_norm_workspace_bytes")
+    return n.value
+
+
+def ep_block_norm_backward(new_residual, y, rstd, grad_new_residual, grad_x, grad_residual, grad_y, workspace,
+                           post_weight=None, pre_weight=None, gate=None, grad_post_weight=None, grad_pre_weight=None,
+                           grad_gate=None, residual_scale: float = 1.0, token_mask=None, num_sms: int = 0,
+                           stream=None) -> None:
+    """Gradients of ep_block_norm_forward from those of new_residual and x
+    (either may be None), on what it left: new_residual, rstd, and its y.
+
+    grad_residual [T, H] has the residual's dtype (and may be
+    grad_new_residual); grad_y [T, H] bf16; grad_post_weight, grad_pre_weight
+    and grad_gate [H] fp32 (grad_gate [T, H] bf16 for a gate per token); each
+    may be None.  workspace: ep_block_norm_workspace_bytes(H) bytes."""
+    dev = torch.cuda.current_device()
+    like = new_residual if new_residual is not None else grad_residual if grad_residual is not None else grad_new_residual
+    n, T, H, per_token = _block_norm(like, "new_residual", post_weight, pre_weight, gate, token_mask, 0.0, residual_scale,
+                                     dev)
+    tokens = lambda t, dt, name: None if t is None else _tokens(t, T, H, dt, name, dev)  # noqa: E731
+    real = (like.dtype,)
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or
+                                  workspace.numel() * workspace.element_size() < 3072 * H):
+        raise ValueError(f"workspace must be a tensor of at least {3072 * H} bytes")
+    _check(lib().ep_block_norm_backward(
+        n, tokens(new_residual, real, "new_residual"), tokens(y, _BF16, "y"), _optional(rstd, 2 * T, _F32, "rstd", dev),
+        tokens(grad_new_residual, real, "grad_new_residual"), tokens(grad_x, _BF16, "grad_x"),
+        tokens(grad_residual, real, "grad_residual"), tokens(grad_y, _BF16, "grad_y"),
+        tokens(grad_gate, _BF16, "grad_gate") if per_token else _optional(grad_gate, H, _F32, "grad_gate", dev),
+        _optional(grad_post_weight, H, _F32, "grad_post_weight", dev),
+        _optional(grad_pre_weight, H, _F32, "grad_pre_weight", dev),
+        None if workspace is None else _dev_ptr(workspace, (workspace.dtype,), "workspace", dev), num_sms,
+        _stream_on(stream, dev)), "ep_block_norm_backward")
 
 
 class Handle:

@@ -601,6 +601,68 @@ ep_status_t ep_grouped_swiglu_backward(const ep_groups_t* groups, const void* gr
 ep_status_t ep_grouped_weight_grad(const ep_groups_t* groups, const ep_fp8_rows_t* grad_out, int N,
                                    const ep_fp8_rows_t* x, int K, void* grad_w, int num_sms, ep_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * The norms around a block of a model (the attention or the experts), its gate
+ * and its residual scale, in one pass over the tokens.  No handle; the calls run
+ * on the current device, on the caller's stream, and allocate nothing.
+ * --------------------------------------------------------------------- */
+
+typedef enum { EP_REAL_FP32 = 0, EP_REAL_BF16 = 1 } ep_real_t;
+
+/* With norm(v) = v / sqrt(mean over the channels of v^2 + eps):
+ *   new_residual = residual + residual_scale * gate . (norm(y) . post_weight)
+ *   x            = norm(new_residual) . pre_weight
+ * y is the output of the block behind, x the input of the one in front. */
+typedef struct {
+  const void* post_weight; /* dev [H] weight_type, or NULL: y is taken as it is         */
+  const void* pre_weight;  /* dev [H] weight_type, or NULL: no norm in front             */
+  const void* gate;        /* dev [H] weight_type, or (gate_per_token) dev bf16 [T][H],
+                              or NULL: 1                                                 */
+  const uint8_t* token_mask; /* dev [T] or NULL: 0 marks a padding token, whose rows are
+                                not read and whose results are 0                        */
+  int num_tokens;          /* T >= 0                                                     */
+  int hidden;              /* H, a multiple of 8, 8..16384                               */
+  int gate_per_token;
+  ep_real_t residual_type; /* of the residual, the new one and their gradients          */
+  ep_real_t weight_type;
+  float eps, residual_scale;
+} ep_block_norm_t;
+
+/* In:  residual      dev [T][H];  y  dev bf16 [T][H], or NULL: no block behind
+ *                    (post_weight and gate NULL too), x = norm(residual) . pre_weight.
+ * Out: new_residual  dev [T][H] (with y; it may be residual itself).
+ *      x             dev bf16 [T][H] (exactly with pre_weight), from the new residual
+ *                    before it is rounded.
+ *      rstd          dev fp32 [2][T] or NULL: 1 / sqrt(mean + eps) of y (with
+ *                    post_weight) and of the new residual (with pre_weight), for the
+ *                    backward pass; the other entries are left as they are.
+ * 16-byte aligned; one launch. */
+ep_status_t ep_block_norm_forward(const ep_block_norm_t* norm, const void* residual, const void* y, void* new_residual,
+                                  void* x, float* rstd, int num_sms, ep_stream_t stream);
+
+/* Bytes of the backward pass's workspace for a hidden size. */
+ep_status_t ep_block_norm_workspace_bytes(int hidden, int64_t* bytes);
+
+/* Gradients, from those of the forward call's results.
+ * In:  new_residual, y, rstd  as the forward call left and had them (new_residual
+ *                    with grad_x, y with post_weight or grad_gate, rstd with either norm).
+ *      grad_new_residual  dev [T][H], or NULL: 0;  grad_x  dev bf16 [T][H], or NULL: x
+ *                    took no part (pre_weight is then not used).
+ * Out (each may be NULL):
+ *      grad_residual dev [T][H] (it may be grad_new_residual itself).
+ *      grad_y        dev bf16 [T][H].
+ *      grad_gate     with gate: dev fp32 [H], or (gate_per_token) bf16 [T][H].
+ *      grad_post_weight, grad_pre_weight  dev fp32 [H]; the first with post_weight, the
+ *                    second with grad_x.
+ * The sums over tokens are fp32 and always in the same order for the same num_sms.
+ * workspace: dev, ep_block_norm_workspace_bytes, 16-byte aligned, needs no
+ * preparation; one call at a time may use it.  Two launches where a sum over
+ * tokens is asked for, else one. */
+ep_status_t ep_block_norm_backward(const ep_block_norm_t* norm, const void* new_residual, const void* y,
+                                   const float* rstd, const void* grad_new_residual, const void* grad_x,
+                                   void* grad_residual, void* grad_y, void* grad_gate, float* grad_post_weight,
+                                   float* grad_pre_weight, void* workspace, int num_sms, ep_stream_t stream);
+
 /* Static, NUL-terminated name of a status. */
 const char* ep_status_str(ep_status_t s);
 
