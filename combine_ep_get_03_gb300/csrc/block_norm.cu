@@ -78,7 +78,7 @@ __device__ __forceinline__ float team_sum(float v, float* part, int team, int wa
 
 // kWords: 16-byte words of bf16 that a thread holds of each row.
 template <int kWords, bool kRes32>
-__global__ void k_block_norm(const BlockNormArgs a, int warps) {
+__global__ void __launch_bounds__(512) k_block_norm(const BlockNormArgs a, int warps) {
   __shared__ float part[2][32];
   after_previous();
   const int per_team = warps * 32, teams = blockDim.x / per_team;
@@ -100,6 +100,14 @@ __global__ void k_block_norm(const BlockNormArgs a, int warps) {
         if (a.x) a.rstd[a.T + t] = 0.0f;
       }
       continue;
+    }
+    if (tid == 0 && t + gridDim.x * teams < a.T) {
+      // the team's next rows on their way to L2
+      const long long next = (t + gridDim.x * teams) * a.H;
+      constexpr int kR = kRes32 ? 4 : 2;
+      prefetch_l2_bulk(static_cast<const char*>(a.residual) + next * kR, a.H * kR);
+      if (a.y) prefetch_l2_bulk(static_cast<const uint16_t*>(a.y) + next, a.H * 2);
+      if (a.gate_per_token) prefetch_l2_bulk(static_cast<const uint16_t*>(a.gate) + next, a.H * 2);
     }
     uint4 y[kWords];
     float h[kWords][8];
@@ -181,13 +189,253 @@ __global__ void k_block_norm(const BlockNormArgs a, int warps) {
 namespace {
 
 constexpr int kBackThreads = 512, kBackWarps = kBackThreads / 32;
+constexpr int kWordsEach = 2;                                       // 8-channel words of a row that a thread owns
+constexpr int kBackHidden = kBackThreads * kWordsEach * 8;          // beyond: k_block_norm_backward_long
+constexpr int kMaxStages = 4;
+
+struct BackShared {
+  uint64_t full[kBackWarps][kMaxStages], empty[kBackWarps][kMaxStages];
+  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team]
+  int quit;
+};
 
 }  // namespace
 
-// Partial sums of the weights' gradients in shared memory, [3][H] (pre, post,
-// gate), a thread's channels its own.
+// A team of warps takes a row at a time; its tensors' rows arrive by bulk copies in
+// a ring of stages in shared memory, read twice: for the sums, and for the results.
+// kPre: x's gradient takes part; kY: y is needed (a norm behind the block or its
+// gate's gradient); kToken: the gate comes per token.
+template <bool kRes32, bool kPre, bool kY, bool kToken>
+__global__ void __launch_bounds__(kBackThreads, 1)
+    k_block_norm_backward(const BlockNormBackwardArgs a, int warps, int num_stages) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ BackShared s;
+  const BlockNormArgs& n = a.n;
+  const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
+  const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads;
+  const int words = n.H >> 3;
+  constexpr int kR = kRes32 ? 4 : 2;
+  const int o_h = a.grad_new ? kR * n.H : 0, o_x = o_h + (kPre ? kR * n.H : 0), o_y = o_x + (kPre ? 2 * n.H : 0);
+  const int o_g = o_y + (kY ? 2 * n.H : 0), stage_bytes = o_g + (kToken ? 2 * n.H : 0);
+  unsigned char* stages = ring + static_cast<size_t>(team) * num_stages * stage_bytes;
+  uint64_t *full = s.full[team], *empty = s.empty[team];
+  if (tid == 0) {
+    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], warps);
+    s.quit = 0;
+    mbar_init_fence();
+  }
+  after_previous();
+  __syncthreads();
+  const long long step = static_cast<long long>(gridDim.x) * teams;
+  const long long first = static_cast<long long>(blockIdx.x) * teams + team;
+  auto fetch = [&](long long t, int st) {
+    unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
+    const long long at = t * n.H;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    if (a.grad_new) bulk_load(d, static_cast<const char*>(a.grad_new) + at * kR, kR * n.H, &full[st]);
+    if (kPre) bulk_load(d + o_h, static_cast<const char*>(n.new_residual) + at * kR, kR * n.H, &full[st]);
+    if (kPre) bulk_load(d + o_x, static_cast<const char*>(a.grad_x) + at * 2, 2 * n.H, &full[st]);
+    if (kY) bulk_load(d + o_y, static_cast<const char*>(n.y) + at * 2, 2 * n.H, &full[st]);
+    if (kToken) bulk_load(d + o_g, static_cast<const char*>(n.gate) + at * 2, 2 * n.H, &full[st]);
+  };
+  if (tid == 0 && stage_bytes)
+    for (int i = 0; i < num_stages && first + i * step < n.T; ++i) fetch(first + i * step, i);
+
+  // the channels' constants: pre, and q = scale post (times gate where it is a vector)
+  const bool post = kY && n.post, reduce = kPre || post;
+  const float inv_h = 1.0f / static_cast<float>(n.H);
+  float wp[kPre ? kWordsEach : 1][8], q[kWordsEach][8];
+  float sum_pre[kPre ? kWordsEach : 1][8], sum_y[kY ? kWordsEach : 1][8];
+#pragma unroll
+  for (int k = 0; k < kWordsEach; ++k) {
+    const int c = tid + k * threads;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q[k][j] = n.scale;
+      if (kPre) wp[k][j] = sum_pre[k][j] = 0.0f;
+      if (kY) sum_y[k][j] = 0.0f;
+    }
+    if (c < words) {
+      float v[8];
+      if (kPre) load8(n.pre, n.weight32, c, wp[k]);
+      if (n.post && kY) {
+        load8(n.post, n.weight32, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[k][j] *= v[j];
+      }
+      if (n.gate && !n.gate_per_token) {
+        load8(n.gate, n.weight32, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[k][j] *= v[j];
+      }
+    }
+  }
+
+  int st = 0, phase = 0, turn = 0;
+  float next1 = 1.0f, next2 = 0.0f;
+  bool next_live = true;
+  if (first < n.T) {
+    if (n.mask) next_live = n.mask[first];
+    if (post) next1 = n.rstd[first];
+    if (kPre) next2 = n.rstd[n.T + first];
+  }
+  for (long long t = first; t < n.T; t += step) {
+    const float r1 = next1, r2 = next2;
+    const bool live = next_live;
+    if (t + step < n.T) {
+      if (n.mask) next_live = n.mask[t + step];
+      if (post) next1 = n.rstd[t + step];
+      if (kPre) next2 = n.rstd[n.T + t + step];
+    }
+    const unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
+    const bool landed = !stage_bytes || wait_or_quit(&full[st], phase, &s.quit, nullptr);
+    float g[kWordsEach][8];
+    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWordsEach; ++k) {
+      const int c = tid + k * threads;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[k][j] = 0.0f;
+      if (c < words && live) {
+        float hn[8];
+        if (a.grad_new) load8(d, kRes32, c, g[k]);
+        if (kPre) {
+          float x[8];
+          load8(d + o_h, kRes32, c, hn);
+          load8(d + o_x, false, c, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            hn[j] *= r2;
+            x[j] *= wp[k][j];
+            s1 = fmaf(x[j], hn[j], s1);
+            g[k][j] = fmaf(r2, x[j], g[k][j]);
+          }
+        }
+        if (kY) {
+          float y[8], u[8];
+          load8(d + o_y, false, c, y);
+          if (kToken) load8(d + o_g, false, c, u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            y[j] *= r1 * q[k][j];
+            if (kToken) y[j] *= u[j];
+            s2 = fmaf(y[j], g[k][j], s2);
+            if (kPre) s3 = fmaf(y[j], hn[j], s3);
+          }
+        }
+      }
+    }
+    if (!landed) {  // a copy that never came: NaN, not old values
+#pragma unroll
+      for (int k = 0; k < kWordsEach; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[k][j] = __int_as_float(0x7fc00000);
+    }
+    float m1 = 0.0f, m2 = 0.0f;
+    if (reduce) {
+      if (kPre) s1 = warp_sum(s1);
+      if (kY) s2 = warp_sum(s2);
+      if (kPre && kY) s3 = warp_sum(s3);
+      if (warps > 1) {
+        float4* part = s.part[team][turn];
+        if (lane == 0) part[tid >> 5] = make_float4(s1, s2, s3, 0.0f);
+        team_barrier(team, threads);
+        s1 = s2 = s3 = 0.0f;
+        for (int w = 0; w < warps; ++w) {
+          const float4 p = part[w];
+          s1 += p.x, s2 += p.y, s3 += p.z;
+        }
+        turn ^= 1;
+      }
+      m1 = s1 * inv_h * r2;
+      if (post) m2 = inv_h * fmaf(-m1, s3, s2);
+    }
+    const long long row = t * words;
+#pragma unroll
+    for (int k = 0; k < kWordsEach; ++k) {
+      const int c = tid + k * threads;
+      if (c >= words) continue;
+      if (!live) {
+        const float zero[8] = {};
+        if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, zero);
+        if (a.grad_y) store8(a.grad_y, false, row + c, zero);
+        if (kToken && a.grad_gate) store8(a.grad_gate, false, row + c, zero);
+        continue;
+      }
+      if (kPre) {
+        float hn[8], x[8];
+        load8(d + o_h, kRes32, c, hn);
+        load8(d + o_x, false, c, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          hn[j] *= r2;
+          sum_pre[k][j] = fmaf(x[j], hn[j], sum_pre[k][j]);
+          g[k][j] = fmaf(-hn[j], m1, g[k][j]);
+        }
+      }
+      if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g[k]);
+      float u[8];
+      if (kToken) load8(d + o_g, false, c, u);
+      if (kY) {
+        float y[8], dg[8];
+        load8(d + o_y, false, c, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          y[j] *= r1;
+          const float v = g[k][j] * y[j];
+          if (kToken) {
+            dg[j] = q[k][j] * v;
+            sum_y[k][j] = fmaf(u[j], v, sum_y[k][j]);
+          } else {
+            sum_y[k][j] += v;
+          }
+          const float b = (kToken ? q[k][j] * u[j] : q[k][j]) * g[k][j];
+          g[k][j] = r1 * fmaf(-y[j], m2, b);
+        }
+        if (kToken && a.grad_gate) store8(a.grad_gate, false, row + c, dg);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[k][j] *= kToken ? q[k][j] * u[j] : q[k][j];
+      }
+      if (a.grad_y) store8(a.grad_y, false, row + c, g[k]);
+    }
+    __syncwarp();
+    if (stage_bytes) {
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (tid == 0 && t + num_stages * step < n.T) {
+        wait_or_quit(&empty[st], phase, &s.quit, nullptr);
+        fetch(t + num_stages * step, st);
+      }
+    }
+    __syncwarp();
+    if (++st == num_stages) st = 0, phase ^= 1;
+  }
+
+  // the block's sums: its teams', in their order
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int k = 0; k < kWordsEach; ++k) {
+    const int c = tid + k * threads;
+    if (c >= words) continue;
+    float* to = teams == 1 ? a.partial + static_cast<long long>(blockIdx.x) * 2 * n.H : sums + team * 2 * n.H;
+    if (kPre && a.grad_pre) store8(to, true, c, sum_pre[k]);
+    if (kY && a.sum_y) store8(to + n.H, true, c, sum_y[k]);
+  }
+  if (teams == 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * n.H; i += blockDim.x) {
+    if (i < n.H ? !(kPre && a.grad_pre) : !(kY && a.sum_y)) continue;
+    float v = sums[i];
+    for (int k = 1; k < teams; ++k) v += sums[k * 2 * n.H + i];
+    a.partial[static_cast<long long>(blockIdx.x) * 2 * n.H + i] = v;
+  }
+}
+
+// The same for rows too long for a thread's registers: read from memory twice,
+// sums in shared memory, [2][H], a thread's channels its own.
 template <bool kRes32>
-__global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward(const BlockNormBackwardArgs a) {
+__global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward_long(const BlockNormBackwardArgs a) {
   extern __shared__ float4 own4[];
   float* own = reinterpret_cast<float*>(own4);
   __shared__ float part[2][3][kBackWarps];
@@ -196,11 +444,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward(const B
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = n.H >> 3;
   const float inv_h = 1.0f / static_cast<float>(n.H);
-  const bool pre = a.grad_x != nullptr, block = a.grad_y || a.grad_gate || a.grad_post;
-  const bool post = block && n.post, vector = a.grad_gate && !n.gate_per_token;
-  for (int c = tid; c < words; c += kBackThreads)
-    for (int k = 0; k < 3; ++k)
-      for (int j = 0; j < 8; ++j) own[k * n.H + 8 * c + j] = 0.0f;
+  const bool pre = a.grad_x != nullptr, post = a.need_y && n.post;
+  for (int i = tid; i < 2 * n.H; i += kBackThreads) own[i] = 0.0f;
+  __syncthreads();
   int turn = 0;
   for (long long t = blockIdx.x; t < n.T; t += gridDim.x) {
     const long long row = t * words;
@@ -215,35 +461,45 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward(const B
     }
     const float r1 = post ? n.rstd[t] : 1.0f, r2 = pre ? n.rstd[n.T + t] : 0.0f;
     float m1 = 0.0f, m2 = 0.0f;
-    if (pre || (post && a.grad_y)) {
+    // word c: g = grad_h + rstd2 a, hn, x, yn, q = scale gate post, u the token's gate
+    auto fetch = [&](int c, float* g, float* hn, float* x, float* w, float* y, float* q, float* u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = hn[j] = x[j] = w[j] = y[j] = 0.0f, q[j] = n.scale, u[j] = 1.0f;
+      if (a.grad_new) load8(a.grad_new, kRes32, row + c, g);
+      if (pre) {
+        load8(n.new_residual, kRes32, row + c, hn);
+        load8(a.grad_x, false, row + c, x);
+        load8(n.pre, n.weight32, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) hn[j] *= r2, g[j] = fmaf(r2 * x[j], w[j], g[j]);
+      }
+      float v[8];
+      if (a.need_y) {
+        load8(n.y, false, row + c, y);
+        if (n.post) load8(n.post, n.weight32, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          y[j] *= r1;
+          if (n.post) q[j] *= v[j];
+        }
+      }
+      if (n.gate) {
+        load8(n.gate, n.weight32 && !n.gate_per_token, n.gate_per_token ? row + c : c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) (n.gate_per_token ? u : q)[j] *= v[j];
+      }
+    };
+    if (pre || post) {
       float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
       for (int c = tid; c < words; c += kBackThreads) {
-        float g[8] = {}, hn[8] = {};
-        if (a.grad_new) load8(a.grad_new, kRes32, row + c, g);
-        if (pre) {
-          float x[8], w[8];
-          load8(n.new_residual, kRes32, row + c, hn);
-          load8(a.grad_x, false, row + c, x);
-          load8(n.pre, n.weight32, c, w);
+        float g[8], hn[8], x[8], w[8], y[8], q[8], u[8];
+        fetch(c, g, hn, x, w, y, q, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            hn[j] *= r2;
-            x[j] *= w[j];
-            s1 = fmaf(x[j], hn[j], s1);
-            g[j] = fmaf(r2, x[j], g[j]);
-          }
-        }
-        if (post) {
-          float y[8], w[8], q[8];
-          load8(n.y, false, row + c, y);
-          load8(n.post, n.weight32, c, w);
-          if (n.gate) load8(n.gate, n.weight32 && !n.gate_per_token, n.gate_per_token ? row + c : c, q);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float u = (n.gate ? q[j] : 1.0f) * w[j] * (y[j] * r1);
-            s2 = fmaf(u, g[j], s2);
-            s3 = fmaf(u, hn[j], s3);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float b = q[j] * u[j] * y[j];
+          s1 = fmaf(x[j] * w[j], hn[j], s1);
+          s2 = fmaf(b, g[j], s2);
+          s3 = fmaf(b, hn[j], s3);
         }
       }
       s1 = warp_sum(s1), s2 = warp_sum(s2), s3 = warp_sum(s3);
@@ -253,76 +509,75 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward(const B
 #pragma unroll
       for (int w = 0; w < kBackWarps; ++w) s1 += part[turn][0][w], s2 += part[turn][1][w], s3 += part[turn][2][w];
       turn ^= 1;
-      m1 = s1 * inv_h;
-      m2 = n.scale * inv_h * fmaf(-m1 * r2, s3, s2);
+      m1 = s1 * inv_h * r2;
+      if (post) m2 = inv_h * fmaf(-m1, s3, s2);
     }
     for (int c = tid; c < words; c += kBackThreads) {
-      float g[8] = {};
-      if (a.grad_new) load8(a.grad_new, kRes32, row + c, g);
-      if (pre) {
-        float x[8], w[8], hn[8];
-        load8(n.new_residual, kRes32, row + c, hn);
-        load8(a.grad_x, false, row + c, x);
-        load8(n.pre, n.weight32, c, w);
-        float* o = own + 8 * c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          hn[j] *= r2;
-          if (a.grad_pre) o[j] = fmaf(x[j], hn[j], o[j]);
-          g[j] = fmaf(r2, fmaf(-hn[j], m1, x[j] * w[j]), g[j]);
-        }
-      }
-      if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g);
-      if (!block) continue;
-      float y[8] = {}, w[8], q[8];
-      if (post || a.grad_gate) load8(n.y, false, row + c, y);
-      if (post) load8(n.post, n.weight32, c, w);
-      if (n.gate) load8(n.gate, n.weight32 && !n.gate_per_token, n.gate_per_token ? row + c : c, q);
-      float dg[8];
+      float g[8], hn[8], x[8], w[8], y[8], q[8], u[8], dg[8];
+      fetch(c, g, hn, x, w, y, q, u);
+      float *op = own + 8 * c, *oy = op + n.H;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float yn = y[j] * r1, gn = n.scale * g[j];
-        dg[j] = gn * (post ? yn * w[j] : yn);
-        const float u = n.gate ? gn * q[j] : gn;
-        if (post && a.grad_post) own[n.H + 8 * c + j] = fmaf(u, yn, own[n.H + 8 * c + j]);
-        if (vector) own[2 * n.H + 8 * c + j] += dg[j];
-        g[j] = post ? r1 * fmaf(-yn, m2, u * w[j]) : u;
+        if (a.grad_pre) op[j] = fmaf(x[j], hn[j], op[j]);
+        g[j] = fmaf(-hn[j], m1, g[j]);
+      }
+      if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = g[j] * y[j];
+        dg[j] = q[j] * v;
+        if (a.sum_y) oy[j] = fmaf(u[j], v, oy[j]);
+        g[j] = r1 * fmaf(-y[j], m2, q[j] * u[j] * g[j]);
       }
       if (a.grad_gate && n.gate_per_token) store8(a.grad_gate, false, row + c, dg);
       if (a.grad_y) store8(a.grad_y, false, row + c, g);
     }
   }
   for (int c = tid; c < words; c += kBackThreads)
-    for (int k = 0; k < 3; ++k)
-      if (k == 0 ? a.grad_pre != nullptr : k == 1 ? a.grad_post != nullptr : vector)
+    for (int k = 0; k < 2; ++k)
+      if (k == 0 ? a.grad_pre != nullptr : a.sum_y)
         for (int j = 0; j < 8; ++j)
-          a.partial[(static_cast<long long>(blockIdx.x) * 3 + k) * n.H + 8 * c + j] = own[k * n.H + 8 * c + j];
+          a.partial[(static_cast<long long>(blockIdx.x) * 2 + k) * n.H + 8 * c + j] = own[k * n.H + 8 * c + j];
 }
 
-// out[k][i] = sum over blocks of partial[block][k][i], eight runs of blocks side by side.
-__global__ void __launch_bounds__(256) k_block_norm_sums(const float* partial, int blocks, int H, float* pre, float* post,
-                                                         float* gate) {
+// Sums of the blocks' partial [block][2][H], eight runs of blocks side by side:
+// pre's gradient, and sum(gh yn), which times scale and the gate is post's
+// gradient and times scale and post the gate's.
+__global__ void __launch_bounds__(256) k_block_norm_sums(const BlockNormBackwardArgs a, int blocks) {
   __shared__ float4 runs[8][32];
   after_previous();
-  float* out = blockIdx.y == 0 ? pre : blockIdx.y == 1 ? post : gate;
+  const BlockNormArgs& n = a.n;
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int i = (blockIdx.x * 32 + lane) * 4;
+  const bool on = i < n.H && (blockIdx.y ? a.sum_y : a.grad_pre != nullptr);
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (out && i < H) {
+  if (on) {
 #pragma unroll 4
     for (int b = run; b < blocks; b += 8) {
-      const float4 v = *reinterpret_cast<const float4*>(partial + (static_cast<long long>(b) * 3 + blockIdx.y) * H + i);
+      const float4 v = *reinterpret_cast<const float4*>(a.partial + (static_cast<long long>(b) * 2 + blockIdx.y) * n.H + i);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
   }
   runs[run][lane] = s;
   __syncthreads();
-  if (run == 0 && out && i < H) {
-    for (int r = 1; r < 8; ++r) {
-      const float4 v = runs[r][lane];
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    *reinterpret_cast<float4*>(out + i) = s;
+  if (run || !on) return;
+  for (int r = 1; r < 8; ++r) {
+    const float4 v = runs[r][lane];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  if (blockIdx.y == 0) {
+    *reinterpret_cast<float4*>(a.grad_pre + i) = s;
+    return;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  auto weight = [&](const void* p, int at) {
+    return n.weight32 ? static_cast<const float*>(p)[at] : bf16_lo(static_cast<const uint16_t*>(p)[at]);
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float scaled = n.scale * v[j];
+    if (a.grad_post) a.grad_post[i + j] = n.gate && !n.gate_per_token ? scaled * weight(n.gate, i + j) : scaled;
+    if (a.grad_gate && !n.gate_per_token) static_cast<float*>(a.grad_gate)[i + j] = n.post ? scaled * weight(n.post, i + j) : scaled;
   }
 }
 
@@ -336,24 +591,75 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
   static const Kernel kernels[2][4] = {
       {k_block_norm<1, false>, k_block_norm<2, false>, k_block_norm<3, false>, k_block_norm<4, false>},
       {k_block_norm<1, true>, k_block_norm<2, true>, k_block_norm<3, true>, k_block_norm<4, true>}};
-  const long long need = (static_cast<long long>(a.T) + teams - 1) / teams, most = static_cast<long long>(sms) * (threads == 256 ? 3 : 1);
-  return launch_early(kernels[res32][per_thread - 1], 1, dim3(static_cast<unsigned>(need < most ? need : most)),
+  const Kernel kernel = kernels[res32][per_thread - 1];
+  static std::atomic<int> resident[2][4][2];  // blocks an SM holds
+  int occ = resident[res32][per_thread - 1][threads > 256].load(std::memory_order_relaxed);
+  if (!occ) {
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0);
+    if (e != cudaSuccess) return e;
+    resident[res32][per_thread - 1][threads > 256].store(occ, std::memory_order_relaxed);
+  }
+  const long long need = (static_cast<long long>(a.T) + teams - 1) / teams, most = static_cast<long long>(sms) * occ;
+  return launch_early(kernel, 1, dim3(static_cast<unsigned>(need < most ? need : most)),
                       dim3(threads), 0, stream, a, warps);
 }
 
-cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& a, bool res32, int sms, cudaStream_t stream) {
-  auto kernel = res32 ? k_block_norm_backward<true> : k_block_norm_backward<false>;
-  static std::atomic<unsigned long long> ready[2];  // devices set up, a bit each
-  cudaError_t e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[res32], 0);
-  if (e != cudaSuccess) return e;
+namespace {
+
+using Backward = void (*)(BlockNormBackwardArgs, int, int);
+template <bool kRes32>
+Backward backward_kernel(bool pre, bool y, bool token) {
+  static const Backward kernels[8] = {
+      k_block_norm_backward<kRes32, false, false, false>, k_block_norm_backward<kRes32, false, false, true>,
+      k_block_norm_backward<kRes32, false, true, false>,  k_block_norm_backward<kRes32, false, true, true>,
+      k_block_norm_backward<kRes32, true, false, false>,  k_block_norm_backward<kRes32, true, false, true>,
+      k_block_norm_backward<kRes32, true, true, false>,   k_block_norm_backward<kRes32, true, true, true>};
+  return kernels[pre * 4 + y * 2 + token];
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool res32, int sms, cudaStream_t stream) {
+  BlockNormBackwardArgs a = args;
+  const bool token = a.n.gate && a.n.gate_per_token, block = a.grad_y || a.grad_gate || a.grad_post;
+  a.need_y = a.grad_gate || a.grad_post || (a.grad_y && a.n.post);
+  a.sum_y = a.grad_post || (a.grad_gate && !token);
   int blocks = sms < kBlockNormMaxBlocks ? sms : kBlockNormMaxBlocks;
-  if (blocks > a.n.T) blocks = a.n.T;
-  e = launch_early(kernel, 1, dim3(blocks), dim3(kBackThreads), sizeof(float) * 3 * a.n.H, stream, a);
-  const bool vector = a.grad_gate && !a.n.gate_per_token;
-  if (e != cudaSuccess || !(a.grad_pre || a.grad_post || vector)) return e;
-  return launch_early(k_block_norm_sums, 1, dim3((a.n.H + 127) / 128, 3), dim3(256), 0, stream,
-                      static_cast<const float*>(a.partial), blocks, a.n.H, a.grad_pre, a.grad_post,
-                      vector ? static_cast<float*>(a.grad_gate) : nullptr);
+  cudaError_t e;
+  if (a.n.H <= kBackHidden) {
+    // a row's words over as few warps as hold them, and as many teams of them as fill
+    // a block, unless that leaves SMs without rows
+    const bool gate = token && block;
+    const int warps = (a.n.H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach), per_sm = (a.n.T + sms - 1) / sms;
+    int teams = kBackWarps / warps;
+    if (teams > per_sm) teams = per_sm;
+    auto kernel = (res32 ? backward_kernel<true> : backward_kernel<false>)(a.grad_x != nullptr, a.need_y, gate);
+    static std::atomic<unsigned long long> ready[16];  // devices set up, a bit each
+    const int which = res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
+    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess) return e;
+    int device = 0, smem = 0;
+    if ((e = cudaGetDevice(&device)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
+      return e;
+    const int r = res32 ? 4 : 2;
+    const int bytes = a.n.H * ((a.grad_new ? r : 0) + (a.grad_x ? r + 2 : 0) + (a.need_y ? 2 : 0) + (gate ? 2 : 0)) * teams;
+    const int sums = teams > 1 ? 8 * a.n.H * teams : 0, room = smem - static_cast<int>(sizeof(BackShared));
+    int stages = bytes ? room / bytes : 1;
+    if (stages > kMaxStages) stages = kMaxStages;
+    const int need = bytes * stages > sums ? bytes * stages : sums;
+    if (stages < 1 || need > room) return cudaErrorInvalidValue;
+    const int most = (a.n.T + teams - 1) / teams;
+    if (blocks > most) blocks = most;
+    e = launch_early(kernel, 1, dim3(blocks), dim3(teams * warps * 32), need, stream, a, warps, stages);
+  } else {
+    auto kernel = res32 ? k_block_norm_backward_long<true> : k_block_norm_backward_long<false>;
+    static std::atomic<unsigned long long> ready[2];
+    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[res32], 0)) != cudaSuccess) return e;
+    if (blocks > a.n.T) blocks = a.n.T;
+    e = launch_early(kernel, 1, dim3(blocks), dim3(kBackThreads), sizeof(float) * 2 * a.n.H, stream, a);
+  }
+  if (e != cudaSuccess || !(a.grad_pre || a.sum_y)) return e;
+  return launch_early(k_block_norm_sums, 1, dim3((a.n.H + 127) / 128, 2), dim3(256), 0, stream, a, blocks);
 }
 
 }  // namespace ep

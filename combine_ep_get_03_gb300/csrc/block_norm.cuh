@@ -33,7 +33,8 @@ struct BlockNormBackwardArgs {
   void* grad_gate;       // fp32 [H], or bf16 [T][H] per token, or null
   float* grad_post;      // [H] or null
   float* grad_pre;       // [H] or null
-  float* partial;        // [blocks][3][H]
+  float* partial;        // [blocks][2][H]
+  int need_y, sum_y;     // set by the launch: y is read; its sum over tokens is wanted
 };
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaStream_t stream);
