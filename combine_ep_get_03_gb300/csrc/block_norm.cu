@@ -52,6 +52,51 @@ __device__ __forceinline__ void store8(void* p, bool fp32, long long c, const fl
   }
 }
 
+// Pairs of fp32: one instruction for two operations, each rounded as ever.
+__device__ __forceinline__ uint64_t bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ void load8(const void* p, bool fp32, long long c, float2* v) {
+  if (fp32) {
+    const float4* f = static_cast<const float4*>(p) + 2 * c;
+    const float4 a = f[0], b = f[1];
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+  } else {
+    const uint4 q = static_cast<const uint4*>(p)[c];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
+  }
+}
+__device__ __forceinline__ void store8(void* p, bool fp32, long long c, const float2* v) {
+  if (fp32) {
+    float4* f = static_cast<float4*>(p) + 2 * c;
+    f[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    f[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  } else {
+    static_cast<uint4*>(p)[c] = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                           pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
@@ -189,84 +234,101 @@ __global__ void __launch_bounds__(512) k_block_norm(const BlockNormArgs a, int w
 namespace {
 
 constexpr int kBackThreads = 512, kBackWarps = kBackThreads / 32;
-constexpr int kWordsEach = 2;                                       // 8-channel words of a row that a thread owns
-constexpr int kBackHidden = kBackThreads * kWordsEach * 8;          // beyond: k_block_norm_backward_long
+constexpr int kWordsEach = 2;                               // 8-channel words of a row that a thread owns
+constexpr int kBackHidden = kBackThreads * kWordsEach * 8;  // beyond: k_block_norm_backward_long
 constexpr int kMaxStages = 4;
+constexpr int kNarrowWarps = 14;
 
 struct BackShared {
-  uint64_t full[kBackWarps][kMaxStages], empty[kBackWarps][kMaxStages];
-  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team]
+  uint64_t full[kBackWarps][kMaxStages];
+  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team], zeros past the team
   int quit;
 };
 
 }  // namespace
 
 // A team of warps takes a row at a time; its tensors' rows arrive by bulk copies in
-// a ring of stages in shared memory, read twice: for the sums, and for the results.
+// a ring of two stages or more in shared memory, read twice: for the sums, and for
+// the results.  The barrier of a row's sums says that the stage of the row before
+// has been read, so its refill needs no other; each tensor's copy is asked for by a
+// warp of its own.
 // kPre: x's gradient takes part; kY: y is needed (a norm behind the block or its
 // gate's gradient); kToken: the gate comes per token.
-template <bool kRes32, bool kPre, bool kY, bool kToken>
-__global__ void __launch_bounds__(kBackThreads, 1)
+// kThreads: the most that the block has; 448 leave a thread 144 registers.
+template <int kThreads, bool kRes32, bool kPre, bool kY, bool kToken>
+__global__ void __launch_bounds__(kThreads, 1)
     k_block_norm_backward(const BlockNormBackwardArgs a, int warps, int num_stages) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ BackShared s;
   const BlockNormArgs& n = a.n;
   const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
-  const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads;
+  const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads, warp = tid >> 5;
   const int words = n.H >> 3;
   constexpr int kR = kRes32 ? 4 : 2;
-  const int o_h = a.grad_new ? kR * n.H : 0, o_x = o_h + (kPre ? kR * n.H : 0), o_y = o_x + (kPre ? 2 * n.H : 0);
+  const bool grad_new = a.grad_new != nullptr;
+  const int o_h = grad_new ? kR * n.H : 0, o_x = o_h + (kPre ? kR * n.H : 0), o_y = o_x + (kPre ? 2 * n.H : 0);
   const int o_g = o_y + (kY ? 2 * n.H : 0), stage_bytes = o_g + (kToken ? 2 * n.H : 0);
   unsigned char* stages = ring + static_cast<size_t>(team) * num_stages * stage_bytes;
-  uint64_t *full = s.full[team], *empty = s.empty[team];
+  uint64_t* full = s.full[team];
+  const int copies = grad_new + 2 * kPre + kY + kToken;
+  // the i-th tensor's rows are copied by lane 0 of warp i % warps
+  unsigned mine = 0;
+  for (int i = 0; lane == 0 && i < copies; ++i)
+    if (i % warps == warp) mine |= 1u << i;
   if (tid == 0) {
-    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], warps);
+    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], copies);
     s.quit = 0;
     mbar_init_fence();
   }
+  if (tid < 32) s.part[team][tid >> 4][tid & 15] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   after_previous();
   __syncthreads();
   const long long step = static_cast<long long>(gridDim.x) * teams;
   const long long first = static_cast<long long>(blockIdx.x) * teams + team;
+  // row t's copies into stage st
   auto fetch = [&](long long t, int st) {
+    if (t >= n.T || !mine) return;
     unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
     const long long at = t * n.H;
-    mbar_arrive_expect_tx(&full[st], stage_bytes);
-    if (a.grad_new) bulk_load(d, static_cast<const char*>(a.grad_new) + at * kR, kR * n.H, &full[st]);
-    if (kPre) bulk_load(d + o_h, static_cast<const char*>(n.new_residual) + at * kR, kR * n.H, &full[st]);
-    if (kPre) bulk_load(d + o_x, static_cast<const char*>(a.grad_x) + at * 2, 2 * n.H, &full[st]);
-    if (kY) bulk_load(d + o_y, static_cast<const char*>(n.y) + at * 2, 2 * n.H, &full[st]);
-    if (kToken) bulk_load(d + o_g, static_cast<const char*>(n.gate) + at * 2, 2 * n.H, &full[st]);
+    int i = 0;
+    auto copy = [&](int to, const void* from, int size) {
+      if (!(mine >> i++ & 1)) return;
+      mbar_arrive_expect_tx(&full[st], size * n.H);
+      bulk_load(d + to, static_cast<const char*>(from) + at * size, size * n.H, &full[st]);
+    };
+    if (grad_new) copy(0, a.grad_new, kR);
+    if (kPre) copy(o_h, n.new_residual, kR), copy(o_x, a.grad_x, 2);
+    if (kY) copy(o_y, n.y, 2);
+    if (kToken) copy(o_g, n.gate, 2);
   };
-  if (tid == 0 && stage_bytes)
-    for (int i = 0; i < num_stages && first + i * step < n.T; ++i) fetch(first + i * step, i);
+  for (int i = 0; i < num_stages; ++i) fetch(first + i * step, i);
 
   // the channels' constants: pre, and q = scale post (times gate where it is a vector)
-  const bool post = kY && n.post, reduce = kPre || post;
+  const bool post = kY && n.post;
   const float inv_h = 1.0f / static_cast<float>(n.H);
-  float wp[kPre ? kWordsEach : 1][8], q[kWordsEach][8];
-  float sum_pre[kPre ? kWordsEach : 1][8], sum_y[kY ? kWordsEach : 1][8];
+  float2 wp[kPre ? kWordsEach : 1][4], q[kWordsEach][4];
+  float2 sum_pre[kPre ? kWordsEach : 1][4], sum_y[kY ? kWordsEach : 1][4];
 #pragma unroll
   for (int k = 0; k < kWordsEach; ++k) {
     const int c = tid + k * threads;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q[k][j] = n.scale;
-      if (kPre) wp[k][j] = sum_pre[k][j] = 0.0f;
-      if (kY) sum_y[k][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      q[k][j] = both(n.scale);
+      if (kPre) wp[k][j] = sum_pre[k][j] = both(0.0f);
+      if (kY) sum_y[k][j] = both(0.0f);
     }
     if (c < words) {
-      float v[8];
+      float2 v[4];
       if (kPre) load8(n.pre, n.weight32, c, wp[k]);
       if (n.post && kY) {
         load8(n.post, n.weight32, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[k][j] *= v[j];
+        for (int j = 0; j < 4; ++j) q[k][j] = mul2(q[k][j], v[j]);
       }
       if (n.gate && !n.gate_per_token) {
         load8(n.gate, n.weight32, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[k][j] *= v[j];
+        for (int j = 0; j < 4; ++j) q[k][j] = mul2(q[k][j], v[j]);
       }
     }
   }
@@ -288,39 +350,33 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       if (kPre) next2 = n.rstd[n.T + t + step];
     }
     const unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
-    const bool landed = !stage_bytes || wait_or_quit(&full[st], phase, &s.quit, nullptr);
-    float g[kWordsEach][8];
-    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    const bool landed = !copies || wait_or_quit(&full[st], phase, &s.quit, nullptr);
+    float2 g[kWordsEach][4];
+    float2 t1 = both(0.0f), t2 = t1, t3 = t1;
 #pragma unroll
     for (int k = 0; k < kWordsEach; ++k) {
       const int c = tid + k * threads;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[k][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) g[k][j] = both(0.0f);
       if (c < words && live) {
-        float hn[8];
-        if (a.grad_new) load8(d, kRes32, c, g[k]);
-        if (kPre) {
-          float x[8];
-          load8(d + o_h, kRes32, c, hn);
-          load8(d + o_x, false, c, x);
+        float2 hn[4], x[4], y[4], u[4];
+        if (grad_new) load8(d, kRes32, c, g[k]);
+        if (kPre) load8(d + o_h, kRes32, c, hn), load8(d + o_x, false, c, x);
+        if (kY) load8(d + o_y, false, c, y);
+        if (kY && kToken) load8(d + o_g, false, c, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            hn[j] *= r2;
-            x[j] *= wp[k][j];
-            s1 = fmaf(x[j], hn[j], s1);
-            g[k][j] = fmaf(r2, x[j], g[k][j]);
+        for (int j = 0; j < 4; ++j) {
+          // sums of a h, u g and u h: rstd2 and rstd1 come in behind them
+          if (kPre) {
+            x[j] = mul2(x[j], wp[k][j]);
+            t1 = fma2(x[j], hn[j], t1);
+            g[k][j] = fma2(both(r2), x[j], g[k][j]);
           }
-        }
-        if (kY) {
-          float y[8], u[8];
-          load8(d + o_y, false, c, y);
-          if (kToken) load8(d + o_g, false, c, u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[j] *= r1 * q[k][j];
-            if (kToken) y[j] *= u[j];
-            s2 = fmaf(y[j], g[k][j], s2);
-            if (kPre) s3 = fmaf(y[j], hn[j], s3);
+          if (kY) {
+            y[j] = mul2(y[j], q[k][j]);
+            if (kToken) y[j] = mul2(y[j], u[j]);
+            t2 = fma2(y[j], g[k][j], t2);
+            if (kPre) t3 = fma2(y[j], hn[j], t3);
           }
         }
       }
@@ -329,27 +385,33 @@ __global__ void __launch_bounds__(kBackThreads, 1)
 #pragma unroll
       for (int k = 0; k < kWordsEach; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[k][j] = __int_as_float(0x7fc00000);
+        for (int j = 0; j < 4; ++j) g[k][j] = both(__int_as_float(0x7fc00000));
     }
-    float m1 = 0.0f, m2 = 0.0f;
-    if (reduce) {
-      if (kPre) s1 = warp_sum(s1);
-      if (kY) s2 = warp_sum(s2);
-      if (kPre && kY) s3 = warp_sum(s3);
-      if (warps > 1) {
-        float4* part = s.part[team][turn];
-        if (lane == 0) part[tid >> 5] = make_float4(s1, s2, s3, 0.0f);
-        team_barrier(team, threads);
-        s1 = s2 = s3 = 0.0f;
-        for (int w = 0; w < warps; ++w) {
-          const float4 p = part[w];
-          s1 += p.x, s2 += p.y, s3 += p.z;
-        }
-        turn ^= 1;
+    float s1 = t1.x + t1.y, s2 = t2.x + t2.y, s3 = t3.x + t3.y;
+    if (kPre) s1 = warp_sum(s1);
+    if (kY) s2 = warp_sum(s2);
+    if (kPre && kY) s3 = warp_sum(s3);
+    if (warps > 1) {
+      float4* part = s.part[team][turn];
+      if (lane == 0) part[warp] = make_float4(s1, s2, s3, 0.0f);
+      team_barrier(team, threads);
+      // sixteen parts, each half of the warp the same
+      const float4 p = part[lane & 15];
+      s1 = p.x, s2 = p.y, s3 = p.z;
+#pragma unroll
+      for (int b = 8; b; b >>= 1) {
+        if (kPre) s1 += __shfl_xor_sync(kFullMask, s1, b);
+        if (kY) s2 += __shfl_xor_sync(kFullMask, s2, b);
+        if (kPre && kY) s3 += __shfl_xor_sync(kFullMask, s3, b);
       }
-      m1 = s1 * inv_h * r2;
-      if (post) m2 = inv_h * fmaf(-m1, s3, s2);
+      turn ^= 1;
+    } else {
+      __syncwarp();
     }
+    // the row before has been read by everyone
+    if (t != first) fetch(t + (num_stages - 1) * step, st ? st - 1 : num_stages - 1);
+    const float m1 = s1 * r2 * inv_h * r2;
+    const float m2 = post ? inv_h * r1 * fmaf(-m1 * r2, s3, s2) : 0.0f;
     const long long row = t * words;
 #pragma unroll
     for (int k = 0; k < kWordsEach; ++k) {
@@ -362,50 +424,46 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         if (kToken && a.grad_gate) store8(a.grad_gate, false, row + c, zero);
         continue;
       }
+      float2 u[4], y[4];
       if (kPre) {
-        float hn[8], x[8];
+        float2 hn[4], x[4];
         load8(d + o_h, kRes32, c, hn);
         load8(d + o_x, false, c, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          hn[j] *= r2;
-          sum_pre[k][j] = fmaf(x[j], hn[j], sum_pre[k][j]);
-          g[k][j] = fmaf(-hn[j], m1, g[k][j]);
+        for (int j = 0; j < 4; ++j) {
+          hn[j] = mul2(hn[j], both(r2));
+          sum_pre[k][j] = fma2(x[j], hn[j], sum_pre[k][j]);
+          g[k][j] = fma2(hn[j], both(-m1), g[k][j]);
         }
       }
-      if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g[k]);
-      float u[8];
+      if (kY) load8(d + o_y, false, c, y);
       if (kToken) load8(d + o_g, false, c, u);
+      if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g[k]);
       if (kY) {
-        float y[8], dg[8];
-        load8(d + o_y, false, c, y);
+        float2 dg[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y[j] *= r1;
-          const float v = g[k][j] * y[j];
+        for (int j = 0; j < 4; ++j) {
+          y[j] = mul2(y[j], both(r1));
           if (kToken) {
-            dg[j] = q[k][j] * v;
-            sum_y[k][j] = fmaf(u[j], v, sum_y[k][j]);
+            const float2 v = mul2(g[k][j], y[j]);
+            dg[j] = mul2(q[k][j], v);
+            sum_y[k][j] = fma2(u[j], v, sum_y[k][j]);
+            g[k][j] = mul2(mul2(q[k][j], u[j]), g[k][j]);
           } else {
-            sum_y[k][j] += v;
+            sum_y[k][j] = fma2(g[k][j], y[j], sum_y[k][j]);
+            g[k][j] = mul2(q[k][j], g[k][j]);
           }
-          const float b = (kToken ? q[k][j] * u[j] : q[k][j]) * g[k][j];
-          g[k][j] = r1 * fmaf(-y[j], m2, b);
+          g[k][j] = mul2(both(r1), fma2(y[j], both(-m2), g[k][j]));
         }
         if (kToken && a.grad_gate) store8(a.grad_gate, false, row + c, dg);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[k][j] *= kToken ? q[k][j] * u[j] : q[k][j];
+        for (int j = 0; j < 4; ++j) {
+          g[k][j] = mul2(q[k][j], g[k][j]);
+          if (kToken) g[k][j] = mul2(u[j], g[k][j]);
+        }
       }
       if (a.grad_y) store8(a.grad_y, false, row + c, g[k]);
-    }
-    __syncwarp();
-    if (stage_bytes) {
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (tid == 0 && t + num_stages * step < n.T) {
-        wait_or_quit(&empty[st], phase, &s.quit, nullptr);
-        fetch(t + num_stages * step, st);
-      }
     }
     __syncwarp();
     if (++st == num_stages) st = 0, phase ^= 1;
@@ -607,13 +665,13 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
 namespace {
 
 using Backward = void (*)(BlockNormBackwardArgs, int, int);
-template <bool kRes32>
+template <int kThreads, bool kRes32>
 Backward backward_kernel(bool pre, bool y, bool token) {
   static const Backward kernels[8] = {
-      k_block_norm_backward<kRes32, false, false, false>, k_block_norm_backward<kRes32, false, false, true>,
-      k_block_norm_backward<kRes32, false, true, false>,  k_block_norm_backward<kRes32, false, true, true>,
-      k_block_norm_backward<kRes32, true, false, false>,  k_block_norm_backward<kRes32, true, false, true>,
-      k_block_norm_backward<kRes32, true, true, false>,   k_block_norm_backward<kRes32, true, true, true>};
+      k_block_norm_backward<kThreads, kRes32, false, false, false>, k_block_norm_backward<kThreads, kRes32, false, false, true>,
+      k_block_norm_backward<kThreads, kRes32, false, true, false>,  k_block_norm_backward<kThreads, kRes32, false, true, true>,
+      k_block_norm_backward<kThreads, kRes32, true, false, false>,  k_block_norm_backward<kThreads, kRes32, true, false, true>,
+      k_block_norm_backward<kThreads, kRes32, true, true, false>,   k_block_norm_backward<kThreads, kRes32, true, true, true>};
   return kernels[pre * 4 + y * 2 + token];
 }
 
@@ -626,28 +684,33 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
   a.sum_y = a.grad_post || (a.grad_gate && !token);
   int blocks = sms < kBlockNormMaxBlocks ? sms : kBlockNormMaxBlocks;
   cudaError_t e;
-  if (a.n.H <= kBackHidden) {
-    // a row's words over as few warps as hold them, and as many teams of them as fill
-    // a block, unless that leaves SMs without rows
-    const bool gate = token && block;
+  // A row's words over as few warps as hold them, and as many teams of them as fill
+  // a block and leave each two stages of all that a row can have (so that no sum's
+  // order depends on which gradients are asked for), unless SMs would have no rows.
+  const bool gate = token && block;
+  const int r = res32 ? 4 : 2;
+  const int all = a.n.H * (2 * r + 4 + (token ? 2 : 0)), bytes = a.n.H * ((a.grad_new ? r : 0) + (a.grad_x ? r + 2 : 0) + (a.need_y ? 2 : 0) + (gate ? 2 : 0));
+  int device = 0, smem = 0;
+  if ((e = cudaGetDevice(&device)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
+    return e;
+  const int room = smem - static_cast<int>(sizeof(BackShared));
+  if (a.n.H <= kBackHidden && 2 * all <= room) {
     const int warps = (a.n.H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach), per_sm = (a.n.T + sms - 1) / sms;
-    int teams = kBackWarps / warps;
+    const bool wide = warps > kNarrowWarps;
+    int teams = (wide ? kBackWarps : kNarrowWarps) / warps;
     if (teams > per_sm) teams = per_sm;
-    auto kernel = (res32 ? backward_kernel<true> : backward_kernel<false>)(a.grad_x != nullptr, a.need_y, gate);
-    static std::atomic<unsigned long long> ready[16];  // devices set up, a bit each
-    const int which = res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
-    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess) return e;
-    int device = 0, smem = 0;
-    if ((e = cudaGetDevice(&device)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
-      return e;
-    const int r = res32 ? 4 : 2;
-    const int bytes = a.n.H * ((a.grad_new ? r : 0) + (a.grad_x ? r + 2 : 0) + (a.need_y ? 2 : 0) + (gate ? 2 : 0)) * teams;
-    const int sums = teams > 1 ? 8 * a.n.H * teams : 0, room = smem - static_cast<int>(sizeof(BackShared));
-    int stages = bytes ? room / bytes : 1;
+    if (teams > room / (2 * all)) teams = room / (2 * all);
+    int stages = bytes ? room / (bytes * teams) : 2;
     if (stages > kMaxStages) stages = kMaxStages;
-    const int need = bytes * stages > sums ? bytes * stages : sums;
-    if (stages < 1 || need > room) return cudaErrorInvalidValue;
+    const int sums = teams > 1 ? 8 * a.n.H * teams : 0;
+    const int need = bytes * teams * stages > sums ? bytes * teams * stages : sums;
+    auto pick = wide ? (res32 ? backward_kernel<32 * kBackWarps, true> : backward_kernel<32 * kBackWarps, false>)
+                     : (res32 ? backward_kernel<32 * kNarrowWarps, true> : backward_kernel<32 * kNarrowWarps, false>);
+    auto kernel = pick(a.grad_x != nullptr, a.need_y, gate);
+    static std::atomic<unsigned long long> ready[32];  // devices set up, a bit each
+    const int which = wide * 16 + res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
+    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess) return e;
     const int most = (a.n.T + teams - 1) / teams;
     if (blocks > most) blocks = most;
     e = launch_early(kernel, 1, dim3(blocks), dim3(teams * warps * 32), need, stream, a, warps, stages);
