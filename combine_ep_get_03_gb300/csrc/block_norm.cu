@@ -19,6 +19,7 @@
 // partial sums are added by a second kernel in a fixed order.
 #include "block_norm.cuh"
 #include "experts.cuh"
+#include "pairs.cuh"
 
 namespace ep {
 
@@ -52,28 +53,6 @@ __device__ __forceinline__ void store8(void* p, bool fp32, long long c, const fl
   }
 }
 
-// Pairs of fp32: one instruction for two operations, each rounded as ever.
-__device__ __forceinline__ uint64_t bits(float2 v) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-  return r;
-}
-__device__ __forceinline__ float2 pair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return pair(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return pair(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ void load8(const void* p, bool fp32, long long c, float2* v) {
   if (fp32) {
     const float4* f = static_cast<const float4*>(p) + 2 * c;

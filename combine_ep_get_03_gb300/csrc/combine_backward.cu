@@ -10,6 +10,7 @@
 #include "device_common.cuh"
 #include "ep_internal.h"
 #include "experts.cuh"
+#include "pairs.cuh"
 
 namespace ep {
 
@@ -22,6 +23,13 @@ __device__ __forceinline__ uint4 ld_cached(const void* p) {
   uint4 v;
   asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+
+// The larger of two pairs of bf16; a NaN loses.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 }  // namespace
@@ -45,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const CombineB
     const float w = a.topk_weights ? a.topk_weights[i] : 0.0f;
     const uint16_t* g = a.grad_out + i / a.k * a.H;
     const uint16_t* y = a.grad_weights ? a.y + row * a.H : nullptr;
-    float dot = 0.0f;
+    float2 dot = both(0.0f);
     for (int c0 = lane; c0 - lane < words; c0 += 32 * kBatch) {
       uint4 gv[kBatch], yv[kBatch];
 #pragma unroll
@@ -54,48 +62,58 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const CombineB
         gv[b] = c < words ? ld_cached(g + 8 * c) : make_uint4(0, 0, 0, 0);
         if (y) yv[b] = c < words ? ld_stream(y + 8 * c) : make_uint4(0, 0, 0, 0);
       }
+      float inv = 0.0f;
+      if (kFP8 && a.grad_y) {
+        // Sixteen lanes hold a group of 128 channels, and a batch four groups of
+        // theirs: the maxima of |grad_out| are halved in number as they are exchanged, so that
+        // lanes 4 n + b end with group b's.  The largest |w grad_out| is |w| times that.
+        uint32_t m[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          m[b] = max2(max2(gv[b].x & 0x7fff7fffu, gv[b].y & 0x7fff7fffu), max2(gv[b].z & 0x7fff7fffu, gv[b].w & 0x7fff7fffu));
+        const bool odd = lane & 1, upper = lane & 2;
+        const uint32_t m01 = max2(odd ? m[1] : m[0], __shfl_xor_sync(kFullMask, odd ? m[0] : m[1], 1));
+        const uint32_t m23 = max2(odd ? m[3] : m[2], __shfl_xor_sync(kFullMask, odd ? m[2] : m[3], 1));
+        uint32_t most = max2(upper ? m23 : m01, __shfl_xor_sync(kFullMask, upper ? m01 : m23, 2));
+        most = max2(most, __shfl_xor_sync(kFullMask, most, 4));
+        most = max2(most, __shfl_xor_sync(kFullMask, most, 8));
+        const float sc = group_scale(fabsf(w) * fmaxf(bf16_lo(most), bf16_hi(most)), &inv);
+        const int c = c0 + 32 * (lane & 3);
+        if ((lane & 12) == 0 && c < words) st_keep(a.grad_y_scales + (c >> 4) * a.scales_ld + row, sc);
+      }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int c = c0 + 32 * b;
         const uint32_t gw[4] = {gv[b].x, gv[b].y, gv[b].z, gv[b].w};
-        if (y) {
-          const uint32_t yw[4] = {yv[b].x, yv[b].y, yv[b].z, yv[b].w};
+        const uint32_t yw[4] = {yv[b].x, yv[b].y, yv[b].z, yv[b].w};
+        float2 v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dot = fmaf(bf16_lo(gw[j]), bf16_lo(yw[j]), dot);
-            dot = fmaf(bf16_hi(gw[j]), bf16_hi(yw[j]), dot);
-          }
+        for (int j = 0; j < 4; ++j) {
+          v[j] = make_float2(bf16_lo(gw[j]), bf16_hi(gw[j]));
+          if (y) dot = fma2(v[j], make_float2(bf16_lo(yw[j]), bf16_hi(yw[j])), dot);
+          v[j] = mul2(v[j], both(w));
         }
-        if (a.grad_y) {
-          float v[8];
+        if (!a.grad_y) continue;
+        if constexpr (kFP8) {
+          const float2 by = both(__shfl_sync(kFullMask, inv, (lane & 16) + b));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[2 * j] = w * bf16_lo(gw[j]), v[2 * j + 1] = w * bf16_hi(gw[j]);
-          if constexpr (kFP8) {
-            // sixteen lanes hold a group of 128 channels
-            float most = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
-#pragma unroll
-            for (int d = 8; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, d));
-            float inv;
-            const float sc = group_scale(most, &inv);
-            if (c < words) {
-              uint2 q = make_uint2(quant4(v, inv), quant4(v + 4, inv));
-              *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.grad_y) + row * a.H + 8 * c) = q;
-              if ((lane & 15) == 0) st_keep(a.grad_y_scales + (c >> 4) * a.scales_ld + row, sc);
-            }
-          } else if (c < words) {
-            st_na(static_cast<uint16_t*>(a.grad_y) + row * a.H + 8 * c,
-                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                             pack_bf16x2(v[6], v[7])));
-          }
+          for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], by);
+          if (c < words)
+            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.grad_y) + row * a.H + 8 * c) =
+                make_uint2(pack_e4m3x2(v[0].x, v[0].y) | (pack_e4m3x2(v[1].x, v[1].y) << 16),
+                           pack_e4m3x2(v[2].x, v[2].y) | (pack_e4m3x2(v[3].x, v[3].y) << 16));
+        } else if (c < words) {
+          st_na(static_cast<uint16_t*>(a.grad_y) + row * a.H + 8 * c,
+                make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                           pack_bf16x2(v[3].x, v[3].y)));
         }
       }
     }
     if (a.grad_weights) {
+      float sum = dot.x + dot.y;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFullMask, dot, d);
-      if (lane == 0) a.grad_weights[i] = dot;
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+      if (lane == 0) a.grad_weights[i] = sum;
     }
   }
 }
