@@ -105,41 +105,69 @@ struct Handover {
   uint64_t* empty;
 };
 
-// Item m of a hand-over is chunk m % kOf, 16 columns, of its (m / kOf)th block of
-// k.  Its sixteen registers: [sixteen lanes][8 columns][8 lanes][2 columns] in the
-// plain product, [gate, up][sixteen lanes][8 lanes][2 columns] in SwiGLU.  A thread
-// then has the same two columns of eight at each step, so four weight rows share a
-// pair of scales: with a weight row a thread, every thread takes every scale from
-// shared memory, 900 of 1 750 cycles a stage of 112 tokens.
+// How a warp reads a block of k of up to kOf chunks of 16 tokens.  Its columns are
+// octets of 8 tokens in planes of 16 weight rows: in the plain product two planes
+// (the warp's 32 rows) of 2 kOf octets, in SwiGLU four (the gate's, then the up
+// projection's) of kOf, as a warp takes half of the tokens there.  Of an octet and
+// a plane a thread has four numbers: two weight rows by two tokens, the same two of
+// eight at every octet, so that all its rows share a pair of scales an octet.
+// (With a weight row a thread, every thread took every scale from shared memory:
+// swiglu decode 103 us instead of 96, prefill 949 instead of 834.)
+// An item is 16 registers: as many octets of a plane as one load brings, since
+// each load takes some 18 cycles to issue whatever it brings.
 template <bool kSwiglu, int kOf>
-__device__ __forceinline__ void load_item(uint32_t (&v)[4][16], const Handover& h, int m, int items) {
-  if (m >= items) return;
-  constexpr uint32_t kSixteen = 16u << 16;  // lanes
-  const uint32_t from = h.from + (m / kOf) * 2 * h.widest;
-  uint32_t* to = v[m & 3];
-  if constexpr (kSwiglu) {
-    const uint32_t gate = from + 8 * (m % kOf), up = gate + h.widest;
-    tmem_load_16x8(gate, to), tmem_load_16x8(gate + kSixteen, to + 4);
-    tmem_load_16x8(up, to + 8), tmem_load_16x8(up + kSixteen, to + 12);
-  } else {
-    const uint32_t at = from + 16 * (m % kOf);
-    tmem_load_16x16(at, to), tmem_load_16x16(at + kSixteen, to + 8);
+struct Plan {
+  static constexpr int kPlanes = kSwiglu ? 4 : 2, kOctets = kSwiglu ? kOf : 2 * kOf;
+  static constexpr int kItems = kOf == kChunks ? 8 : kOf;  // of a block of k
+  static constexpr int kBlocks = kOf == 1 ? 4 : kOf == kChunks ? 1 : 2;  // blocks of k in a hand-over, at most
+  static constexpr int kMost = kItems * kBlocks;
+  // octets that one load of item i brings, and the plane and octet of its g-th four registers
+  __host__ __device__ static constexpr int load(int i) {
+    return kOf == kChunks ? 4 : kOf == 3 ? (i < 2 ? kPlanes == 2 ? 4 : 2 : kPlanes == 2 ? 2 : 1) : kOctets;
+  }
+  __host__ __device__ static constexpr int plane(int i, int g) {
+    return kOf == kChunks ? i % kPlanes : (kOf == 3 && i == 2 ? 0 : i * (4 / load(i))) + g / load(i);
+  }
+  __host__ __device__ static constexpr int octet(int i, int g) {
+    return kOf == kChunks ? i / kPlanes * 4 + g : (kOf == 3 && i == 2 ? load(0) : 0) + g % load(i);
+  }
+};
+
+template <bool kSwiglu, int kOf, int kItem, int kLoad = 0>
+__device__ __forceinline__ void load_planes(uint32_t (&v)[16], uint32_t from, uint32_t widest) {
+  using P = Plan<kSwiglu, kOf>;
+  constexpr int kOctets = P::load(kItem), g = kLoad * kOctets;
+  if constexpr (g < 4) {
+    constexpr int plane = P::plane(kItem, g);
+    constexpr uint32_t at = 8 * P::octet(kItem, g) + ((plane & 1) << 20);  // sixteen lanes on: 16 << 16
+    tmem_load_octets<kOctets>(from + at + (plane >> 1) * widest, v + 4 * g);
+    load_planes<kSwiglu, kOf, kItem, kLoad + 1>(v, from, widest);
   }
 }
 
-template <bool kSwiglu, int kOf>
-__device__ __forceinline__ void add_item(float (&acc)[16 * kOf], const uint32_t (&v)[4][16], const Handover& h, int m,
+// Item m of a hand-over: item m % kItems of its (m / kItems)th block of k.
+template <bool kSwiglu, int kOf, int m>
+__device__ __forceinline__ void load_item(uint32_t (&v)[4][16], const Handover& h, int items) {
+  constexpr int kItems = Plan<kSwiglu, kOf>::kItems;
+  if (m < items) load_planes<kSwiglu, kOf, m % kItems>(v[m & 3], h.from + (m / kItems) * 2 * h.widest, h.widest);
+}
+
+template <bool kSwiglu, int kOf, int m>
+__device__ __forceinline__ void add_item(float (&acc)[16 * kOf], const uint32_t (&v)[4][16],
+                                         const float2 (&scales)[Plan<kSwiglu, kOf>::kBlocks][Plan<kSwiglu, kOf>::kOctets],
                                          int items) {
+  using P = Plan<kSwiglu, kOf>;
   if (m >= items) return;
-  // scales of rows past the group's end are anything
-  const float2* f = reinterpret_cast<const float2*>(h.scales + ((h.it + m / kOf) % h.kept) * h.widest) +
-                    (m % kOf) * (kSwiglu ? 4 : 8);
-  const float2 s0 = f[0], s1 = kSwiglu ? s0 : f[4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float2 s = j & 4 ? s1 : s0;
-    float& a = acc[16 * (m % kOf) + j];
-    a = fmaf(__uint_as_float(v[m & 3][j]), j & 1 ? s.y : s.x, a);
+  for (int g = 0; g < 4; ++g) {
+    const int plane = P::plane(m % P::kItems, g), octet = P::octet(m % P::kItems, g);
+    if (octet >= P::kOctets) continue;
+    const float2 s = scales[m / P::kItems][octet];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float& a = acc[(octet * P::kPlanes + plane) * 4 + r];
+      a = fmaf(__uint_as_float(v[m & 3][4 * g + r]), r & 1 ? s.y : s.x, a);
+    }
   }
 }
 
@@ -149,30 +177,42 @@ __device__ __forceinline__ void release(const Handover& h) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(h.empty);
 }
 
-// Adds a hand-over's items, `kMost` at most: 64 columns are on their way at a
-// time, and the accumulator goes back as soon as the last are here.
-template <bool kSwiglu, int kOf, int kMost>
-__device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, int items) {
+// Adds a hand-over's `blocks` blocks of k, `items` items: 64 registers' loads are on
+// their way at a time, and the accumulator goes back as soon as the last are here.
+template <bool kSwiglu, int kOf>
+__device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, int blocks, int items) {
+  using P = Plan<kSwiglu, kOf>;
   uint32_t v[4][16];
+  load_item<kSwiglu, kOf, 0>(v, h, items), load_item<kSwiglu, kOf, 1>(v, h, items);
+  load_item<kSwiglu, kOf, 2>(v, h, items), load_item<kSwiglu, kOf, 3>(v, h, items);
+  // scales of rows past the group's end are anything
+  float2 scales[P::kBlocks][P::kOctets];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) load_item<kSwiglu, kOf>(v, h, m, items);
+  for (int k = 0; k < P::kBlocks; ++k) {
+    if (k && k >= blocks) continue;
+    const float2* f = reinterpret_cast<const float2*>(h.scales + ((h.it + k) & (h.kept - 1)) * h.widest);
+#pragma unroll
+    for (int o = 0; o < P::kOctets; ++o) scales[k][o] = f[4 * o];
+  }
 #pragma unroll
   for (int m = 0; m < 4; ++m) tmem_load_wait16(v[m]);
-  if (kMost <= 4 || items <= 4) {
+  if (P::kMost <= 4 || items <= 4) {
     release(h);
+    add_item<kSwiglu, kOf, 0>(acc, v, scales, items), add_item<kSwiglu, kOf, 1>(acc, v, scales, items);
+    add_item<kSwiglu, kOf, 2>(acc, v, scales, items), add_item<kSwiglu, kOf, 3>(acc, v, scales, items);
+  } else if constexpr (P::kMost > 4) {
+    add_item<kSwiglu, kOf, 0>(acc, v, scales, items), load_item<kSwiglu, kOf, 4>(v, h, items);
+    add_item<kSwiglu, kOf, 1>(acc, v, scales, items), load_item<kSwiglu, kOf, 5>(v, h, items);
+    add_item<kSwiglu, kOf, 2>(acc, v, scales, items);
+    if constexpr (P::kMost > 6) load_item<kSwiglu, kOf, 6>(v, h, items);
+    add_item<kSwiglu, kOf, 3>(acc, v, scales, items);
+    if constexpr (P::kMost > 6) load_item<kSwiglu, kOf, 7>(v, h, items);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) add_item<kSwiglu, kOf>(acc, v, h, m, items);
-  } else {
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      add_item<kSwiglu, kOf>(acc, v, h, m, items);
-      if (m + 4 < kMost) load_item<kSwiglu, kOf>(v, h, m + 4, items);
-    }
-#pragma unroll
-    for (int m = 4; m < kMost; ++m) tmem_load_wait16(v[m & 3]);
+    for (int m = 4; m < P::kMost; ++m) tmem_load_wait16(v[m & 3]);
     release(h);
-#pragma unroll
-    for (int m = 4; m < kMost; ++m) add_item<kSwiglu, kOf>(acc, v, h, m, items);
+    add_item<kSwiglu, kOf, 4>(acc, v, scales, items), add_item<kSwiglu, kOf, 5>(acc, v, scales, items);
+    if constexpr (P::kMost > 6)
+      add_item<kSwiglu, kOf, 6>(acc, v, scales, items), add_item<kSwiglu, kOf, 7>(acc, v, scales, items);
   }
 }
 
@@ -213,7 +253,8 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
       if (!ok) return;
       tmem_fence_after();
       const Handover h{from + ac * l.acc_columns, l.widest, s.x_scale + first + pair, it, l.kept, &s.acc_empty[ac]};
-      take<kSwiglu, kOf, kOf == 3 ? 6 : kOf < 3 ? 4 : kOf>(acc, h, kOf == kChunks ? c.columns >> 4 : n * kOf);
+      using P = Plan<kSwiglu, kOf>;
+      take<kSwiglu, kOf>(acc, h, n, kOf == kChunks ? (c.columns + 16 * P::kPlanes - 1) / (16 * P::kPlanes) * P::kPlanes : n * kOf);
       kb += n;
       it += n;
     }
@@ -225,8 +266,8 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
       const int rows = c.rows - pair - odd, n_left = p.N - (c.n * 256 + half * 128 + in_half - odd);
 #pragma unroll
       for (int i = 0; i < kColumns / 2; ++i) {
-        // [chunk][sixteen lanes][8 columns][8 lanes]
-        const int token = 16 * (i >> 3) + 8 * ((i >> 1) & 1), n = 16 * ((i >> 2) & 1) + 8 * (i & 1);
+        // [octet][plane][8 weight rows]
+        const int token = 8 * (i >> 2), n = 8 * (i & 3);
         const float mine = odd ? acc[2 * i + 1] : acc[2 * i];
         const float other = __shfl_xor_sync(kFullMask, odd ? acc[2 * i] : acc[2 * i + 1], 4);
         if (token < rows && n < n_left)

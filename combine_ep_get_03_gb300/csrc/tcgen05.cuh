@@ -148,19 +148,30 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
       : "r"(addr)
       : "memory");
 }
-// Sixteen lanes by 16 or 8 columns, as an MMA's result lies in a warp: register
-// 4 c + 2 h + e of thread t is (lane base + 8 h + t / 4, column + 8 c + 2 (t % 4) + e).
-__device__ __forceinline__ void tmem_load_16x16(uint32_t addr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_load_16x8(uint32_t addr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(addr)
-               : "memory");
+// Sixteen lanes by kOctets times 8 columns, as an MMA's result lies in a warp:
+// register 4 c + 2 h + e of thread t is (lane base + 8 h + t / 4, column + 8 c +
+// 2 (t % 4) + e).
+template <int kOctets>
+__device__ __forceinline__ void tmem_load_octets(uint32_t addr, uint32_t* v) {
+  static_assert(kOctets == 1 || kOctets == 2 || kOctets == 4, "");
+  if constexpr (kOctets == 4)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
+  else if constexpr (kOctets == 2)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
 }
 // One word to four consecutive columns of the warp's 32 lanes, and the wait for it.
 __device__ __forceinline__ void tmem_fill4(uint32_t addr, uint32_t v) {
