@@ -65,6 +65,10 @@ struct Shared {
   float amax[2][2][4][kTileT / 2];  // [tile parity][half][warp][token]
 };
 
+// The same value in every lane, said so that the compiler keeps it, and what is
+// made of it, in uniform registers: MMAs and tensor loads take their operands there.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(kFullMask, v, 0); }
+
 struct Tile {
   int group, n;   // group and column tile
   long long row;  // first row
@@ -230,7 +234,6 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2, quarter = warp & 3;
   const int pair = 2 * (lane & 3);                        // the thread's columns of eight
-  const int in_half = quarter * 32 + (lane >> 2);         // its weight rows in its half: this one, and 8, 16 and 24 on
   volatile int* quit = &s.quit;
   int* err = p.groups.err;
   const int F = p.N >> 1;
@@ -259,20 +262,23 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
       it += n;
     }
     if constexpr (!kSwiglu) {
-      // lanes t and t ^ 4 hold neighbouring weight rows of the same two tokens: each
-      // takes both rows of one of them
-      const bool odd = lane & 4;
-      uint16_t* o = p.out + (c.row + pair + odd) * p.N + c.n * 256 + half * 128 + in_half - odd;
-      const int rows = c.rows - pair - odd, n_left = p.N - (c.n * 256 + half * 128 + in_half - odd);
+      // Lanes 4 a + t hold weight rows a, a + 8, a + 16 and a + 24 of the same tokens.
+      // Four of them swap theirs, so that each has four rows in a row, 8 bytes.
+      const int a = lane >> 2;
+      const int n = c.n * 256 + half * 128 + quarter * 32 + 8 * (a & 3) + (a & 4);
+      uint16_t* o = p.out + (c.row + pair) * p.N + n;
+      const int rows = n < p.N ? c.rows - pair : 0;
 #pragma unroll
-      for (int i = 0; i < kColumns / 2; ++i) {
-        // [octet][plane][8 weight rows]
-        const int token = 8 * (i >> 2), n = 8 * (i & 3);
-        const float mine = odd ? acc[2 * i + 1] : acc[2 * i];
-        const float other = __shfl_xor_sync(kFullMask, odd ? acc[2 * i] : acc[2 * i + 1], 4);
-        if (token < rows && n < n_left)
-          *reinterpret_cast<uint32_t*>(o + static_cast<long long>(token) * p.N + n) =
-              odd ? pack_bf16x2(other, mine) : pack_bf16x2(mine, other);
+      for (int i = 0; i < kColumns / 4; ++i) {
+        const float* v = acc + 8 * (i >> 1) + (i & 1);  // token 8 (i / 2) + pair + i % 2
+        const uint32_t w0 = pack_bf16x2(v[0], v[2]), w1 = pack_bf16x2(v[4], v[6]);
+        const uint32_t x = __shfl_xor_sync(kFullMask, __byte_perm(w0, w1, a & 1 ? 0x5410 : 0x7632), 4);
+        const uint32_t u0 = a & 1 ? __byte_perm(w0, x, 0x3254) : __byte_perm(w0, x, 0x5410);
+        const uint32_t u1 = a & 1 ? __byte_perm(w1, x, 0x3276) : __byte_perm(w1, x, 0x7610);
+        const uint32_t y = __shfl_xor_sync(kFullMask, a & 2 ? u0 : u1, 8);
+        const int token = 8 * (i >> 1) + (i & 1);
+        if (token < rows)
+          *reinterpret_cast<uint2*>(o + static_cast<long long>(token) * p.N) = a & 2 ? make_uint2(y, u1) : make_uint2(u0, y);
       }
     } else {
       const int live = c.rows - first;  // of this warp's tokens (and more, where the other half has some)
@@ -359,10 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = uniform(s.tmem);
   // As many stages as fit beside the largest tile's tokens; an accumulator holds
   // several blocks of k where the tiles have few.
-  const uint32_t widest = s.columns;
+  const uint32_t widest = uniform(s.columns);
   const uint32_t stage_bytes = kTokens + widest * kBlockK;
   const uint32_t num_stages = min(static_cast<uint32_t>(kMaxStages),
                                   (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
@@ -392,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
+        const int row = uniform(static_cast<uint32_t>(c.row)), columns = uniform(c.columns), n = uniform(c.n), g = uniform(c.group);
         for (int kb = 0; kb < blocks_k; ++kb, ++it) {
           if (it >= num_stages) {
             ok = __all_sync(kFullMask, wait_or_quit(&s.empty[st], phase ^ 1, quit, err));
@@ -402,18 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* f = a + 2 * kHalfBytes;
             unsigned char* b = a + kTokens;
             uint64_t* bar = &s.full[st];
-            mbar_arrive_expect_tx(bar, 2 * (kHalfLoad + kScaleBytes) + c.columns * kBlockK);
+            mbar_arrive_expect_tx(bar, 2 * (kHalfLoad + kScaleBytes) + columns * kBlockK);
             if constexpr (kSwiglu) {
-              tma_load_4d(a, &maps.w, kb * kBlockK, c.n * 128, 0, c.group, bar);
-              tma_load_3d(f, &maps.scales, kb * (kScaleBytes / 4), c.n, c.group * 2, bar);
+              tma_load_4d(a, &maps.w, kb * kBlockK, n * 128, 0, g, bar);
+              tma_load_3d(f, &maps.scales, kb * (kScaleBytes / 4), n, g * 2, bar);
             } else {
-              tma_load_3d(a, &maps.w, kb * kBlockK, c.n * 256, c.group, bar);
-              tma_load_2d(f, &maps.scales, kb * (kScaleBytes / 4), c.group * blocks_n + 2 * c.n, bar);
+              tma_load_3d(a, &maps.w, kb * kBlockK, n * 256, g, bar);
+              tma_load_2d(f, &maps.scales, kb * (kScaleBytes / 4), g * blocks_n + 2 * n, bar);
             }
-            int y = static_cast<int>(c.row);
+            int y = row;
 #pragma unroll
             for (int i = 2; i >= 0; --i) {
-              if (c.columns & (16 << i)) {
+              if (columns & (16 << i)) {
                 tma_load_2d(b, &maps.x[i], kb * kBlockK, y, bar);
                 b += (16 << i) * kBlockK;
                 y += 16 << i;
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
-        const uint32_t desc = mma_mx_desc(128, c.columns, 0);
+        const uint32_t desc = mma_mx_desc(128, uniform(c.columns), 0);
         for (int kb = 0, in = 0; kb < blocks_k; ++kb, ++it) {
           const uint32_t at = st, round = phase, ac = group & 1, turn = (group >> 1) & 1, slot = in;
           const bool first_turn = group < 2, last = kb + 1 == blocks_k;
