@@ -23,6 +23,7 @@
 
 #include "ep_internal.h"
 #include "experts.cuh"
+#include "pairs.cuh"
 #include "tcgen05.cuh"
 
 namespace ep {
@@ -168,9 +169,11 @@ __device__ __forceinline__ void add_item(float (&acc)[16 * kOf], const uint32_t 
     if (octet >= P::kOctets) continue;
     const float2 s = scales[m / P::kItems][octet];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float& a = acc[(octet * P::kPlanes + plane) * 4 + r];
-      a = fmaf(__uint_as_float(v[m & 3][4 * g + r]), r & 1 ? s.y : s.x, a);
+    for (int r = 0; r < 4; r += 2) {
+      float* a = acc + (octet * P::kPlanes + plane) * 4 + r;
+      const uint32_t* f = v[m & 3] + 4 * g + r;
+      const float2 sum = fma2(make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])), s, make_float2(a[0], a[1]));
+      a[0] = sum.x, a[1] = sum.y;
     }
   }
 }
