@@ -688,38 +688,41 @@ def ep_grouped_weight_grad(grad_out, grad_out_scales, x, x_scales, grad_w, group
 # ------------------------------------------------ the norms around a block
 
 _REALS = (torch.float32, torch.bfloat16)
+_BF = torch.bfloat16
 
 
-def _tokens(t, T, H, dtypes, name, dev):
-    """Device pointer of a contiguous [T, H] tensor."""
-    p = _dev_ptr(t, dtypes, name, dev)
-    if t.shape != (T, H):
-        raise ValueError(f"{name} must be [{T}, {H}], got {list(t.shape)}")
-    return p
+def _shaped(t, shape, dtype, name, dev):
+    """Device pointer of a contiguous tensor of a shape and dtype, NULL for None."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor: refused below
+        pass
+    _dev_ptr(t, (dtype,), name, dev)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _block_norm(residual, name, post_weight, pre_weight, gate, token_mask, eps, residual_scale, dev):
-    """ep_block_norm_t of a call on [T, H] tensors, T, H, whether the gate comes per token."""
-    if not isinstance(residual, torch.Tensor) or residual.dim() != 2 or residual.dtype not in _REALS:
+def _block_norm(like, name, post_weight, pre_weight, gate, token_mask, eps, residual_scale, dev):
+    """ep_block_norm_t of a call on tensors like [T, H] `like`, its shape and
+    dtype, whether the gate comes per token."""
+    if not isinstance(like, torch.Tensor) or like.dim() != 2 or like.dtype not in _REALS:
         raise ValueError(f"{name} must be a [T, H] fp32 or bf16 tensor")
-    T, H = residual.shape
+    shape, dtype = like.shape, like.dtype
+    T, H = shape
     per_token = gate is not None and gate.dim() == 2
-    kind, weights = None, []
-    for t, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (None if per_token else gate, "gate")):
-        if t is None:
-            weights.append(None)
-            continue
-        weights.append(_dev_ptr(t, _REALS, what, dev))
-        if t.shape != (H,):
-            raise ValueError(f"{what} must be [{H}]{' or [T, H]' if what == 'gate' else ''}, got {list(t.shape)}")
-        if kind is not None and t.dtype is not kind:
-            raise ValueError("post_weight, pre_weight and a gate [H] must have one dtype")
-        kind = t.dtype
-    if per_token:
-        weights[2] = _tokens(gate, T, H, _BF16, "gate", dev)
-    real = lambda d: EP_REAL_BF16 if d is torch.bfloat16 else EP_REAL_FP32  # noqa: E731
-    return _BLOCK_NORM.pack(*(w or 0 for w in weights), _optional(token_mask, T, _MASK, "token_mask", dev) or 0, T, H,
-                            per_token, real(residual.dtype), real(kind), eps, residual_scale), T, H, per_token
+    first = post_weight if post_weight is not None else pre_weight if pre_weight is not None else gate
+    kind = torch.float32 if first is None or per_token and first is gate else first.dtype
+    if kind not in _REALS:
+        raise ValueError(f"weights must be fp32 or bf16, got {kind}")
+    row = (H,)
+    post = _shaped(post_weight, row, kind, "post_weight", dev)
+    pre = _shaped(pre_weight, row, kind, "pre_weight", dev)
+    g = _shaped(gate, shape, _BF, "gate", dev) if per_token else _shaped(gate, row, kind, "gate", dev)
+    mask = 0 if token_mask is None else _vector(token_mask, T, _MASK, "token_mask", dev)
+    return _BLOCK_NORM.pack(post or 0, pre or 0, g or 0, mask, T, H, per_token, dtype is _BF, kind is _BF, eps,
+                            residual_scale), shape, dtype, per_token
 
 
 def ep_block_norm_forward(residual, y, new_residual, x, rstd=None, post_weight=None, pre_weight=None, gate=None,
@@ -729,25 +732,27 @@ def ep_block_norm_forward(residual, y, new_residual, x, rstd=None, post_weight=N
     and x = norm(new_residual) * pre_weight, norm(v) = v / sqrt(mean(v^2) + eps).
 
     residual and new_residual [T, H] fp32 or bf16 (they may be one tensor); y
-    and x [T, H] bf16; weights [H] fp32 or bf16; gate [H], or [T, H] bf16.
-    post_weight, gate and pre_weight (with x) may be None; y None: no block
-    behind, x is the norm of residual.  rstd [2, T] fp32 keeps what the
+    and x [T, H] bf16; weights [H] fp32 or bf16, all of one dtype; gate [H], or
+    [T, H] bf16.  post_weight, gate and pre_weight (with x) may be None; y None:
+    no block behind, x is the norm of residual.  rstd [2, T] fp32 keeps what the
     backward pass needs."""
     dev = torch.cuda.current_device()
-    n, T, H, _ = _block_norm(residual, "residual", post_weight, pre_weight, gate, token_mask, eps, residual_scale, dev)
+    n, shape, dtype, _ = _block_norm(residual, "residual", post_weight, pre_weight, gate, token_mask, eps, residual_scale,
+                                     dev)
     if (x is None) != (pre_weight is None):
         raise ValueError("x and pre_weight come together")
-    if y is None and (post_weight is not None or gate is not None or new_residual is not None):
-        raise ValueError("post_weight, gate and new_residual need y")
-    if y is None and x is None:
-        raise ValueError("y or x is required")
-    tokens = lambda t, dt, name: None if t is None else _tokens(t, T, H, dt, name, dev)  # noqa: E731
-    if y is not None and new_residual is None:
+    if y is None:
+        if post_weight is not None or gate is not None or new_residual is not None:
+            raise ValueError("post_weight, gate and new_residual need y")
+        if x is None:
+            raise ValueError("y or x is required")
+    elif new_residual is None:
         raise ValueError("new_residual is required")
     _check(lib().ep_block_norm_forward(
-        n, _tokens(residual, T, H, _REALS, "residual", dev), tokens(y, _BF16, "y"),
-        tokens(new_residual, (residual.dtype,), "new_residual"), tokens(x, _BF16, "x"),
-        _optional(rstd, 2 * T, _F32, "rstd", dev), num_sms, _stream_on(stream, dev)), "ep_block_norm_forward")
+        n, _shaped(residual, shape, dtype, "residual", dev), _shaped(y, shape, _BF, "y", dev),
+        _shaped(new_residual, shape, dtype, "new_residual", dev), _shaped(x, shape, _BF, "x", dev),
+        None if rstd is None else _vector(rstd, 2 * shape[0], _F32, "rstd", dev), num_sms, _stream_on(stream, dev)),
+        "ep_block_norm_forward")
 
 
 def ep_block_norm_workspace_bytes(hidden: int) -> int:
@@ -769,20 +774,21 @@ def ep_block_norm_backward(new_residual, y, rstd, grad_new_residual, grad_x, gra
     may be None.  workspace: ep_block_norm_workspace_bytes(H) bytes."""
     dev = torch.cuda.current_device()
     like = new_residual if new_residual is not None else grad_residual if grad_residual is not None else grad_new_residual
-    n, T, H, per_token = _block_norm(like, "new_residual", post_weight, pre_weight, gate, token_mask, 0.0, residual_scale,
-                                     dev)
-    tokens = lambda t, dt, name: None if t is None else _tokens(t, T, H, dt, name, dev)  # noqa: E731
-    real = (like.dtype,)
+    n, shape, dtype, per_token = _block_norm(like, "new_residual", post_weight, pre_weight, gate, token_mask, 0.0,
+                                             residual_scale, dev)
+    T, H = shape
+    row, f32 = (H,), torch.float32
     if workspace is not None and (not isinstance(workspace, torch.Tensor) or
                                   workspace.numel() * workspace.element_size() < 3072 * H):
         raise ValueError(f"workspace must be a tensor of at least {3072 * H} bytes")
     _check(lib().ep_block_norm_backward(
-        n, tokens(new_residual, real, "new_residual"), tokens(y, _BF16, "y"), _optional(rstd, 2 * T, _F32, "rstd", dev),
-        tokens(grad_new_residual, real, "grad_new_residual"), tokens(grad_x, _BF16, "grad_x"),
-        tokens(grad_residual, real, "grad_residual"), tokens(grad_y, _BF16, "grad_y"),
-        tokens(grad_gate, _BF16, "grad_gate") if per_token else _optional(grad_gate, H, _F32, "grad_gate", dev),
-        _optional(grad_post_weight, H, _F32, "grad_post_weight", dev),
-        _optional(grad_pre_weight, H, _F32, "grad_pre_weight", dev),
+        n, _shaped(new_residual, shape, dtype, "new_residual", dev), _shaped(y, shape, _BF, "y", dev),
+        None if rstd is None else _vector(rstd, 2 * T, _F32, "rstd", dev),
+        _shaped(grad_new_residual, shape, dtype, "grad_new_residual", dev), _shaped(grad_x, shape, _BF, "grad_x", dev),
+        _shaped(grad_residual, shape, dtype, "grad_residual", dev), _shaped(grad_y, shape, _BF, "grad_y", dev),
+        _shaped(grad_gate, shape, _BF, "grad_gate", dev) if per_token else _shaped(grad_gate, row, f32, "grad_gate", dev),
+        _shaped(grad_post_weight, row, f32, "grad_post_weight", dev),
+        _shaped(grad_pre_weight, row, f32, "grad_pre_weight", dev),
         None if workspace is None else _dev_ptr(workspace, (workspace.dtype,), "workspace", dev), num_sms,
         _stream_on(stream, dev)), "ep_block_norm_backward")
 
