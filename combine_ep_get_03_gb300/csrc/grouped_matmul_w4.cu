@@ -63,7 +63,8 @@ struct Shared {
   int quit, columns;
   unsigned sums[32];
   alignas(16) float x_scale[kScaleWords];
-  float amax[2][2][4][kTileT / 2];  // [tile parity][half][warp][token]
+  alignas(16) float amax[2][2][kTileT / 2][4];  // [tile parity][half][token][warp]
+  float inv[2][4][kTileT / 2];                  // [half][warp][token]
 };
 
 // The same value in every lane, said so that the compiler keeps it, and what is
@@ -286,23 +287,29 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
     } else {
       const int live = c.rows - first;  // of this warp's tokens (and more, where the other half has some)
       const long long row = c.row + first;
-      float (*amax)[kTileT / 2] = s.amax[turn][half];
+      float (*amax)[4] = s.amax[turn][half];
+      // the weights of all its tokens are on their way together
+      float w[2 * kOf];
+#pragma unroll
+      for (int i = 0; i < 2 * kOf; ++i) {
+        const int token = 8 * (i >> 1) + pair + (i & 1);
+        w[i] = p.row_weights && token < min(live, c.columns >> 1) ? p.row_weights[row + token] : 1.0f;
+      }
 #pragma unroll
       for (int i = 0; i < 2 * kOf; ++i) {
         // token 8 (i / 2) + pair + i % 2: its four weight rows of this thread
         const int token = 8 * (i >> 1) + pair + (i & 1);
-        const float w = p.row_weights && token < min(live, c.columns >> 1) ? p.row_weights[row + token] : 1.0f;
         float most = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float& g = acc[16 * (i >> 1) + 2 * r + (i & 1)];
           const float u = acc[16 * (i >> 1) + 8 + 2 * r + (i & 1)];
-          g = __fdividef(g, 1.0f + __expf(-g)) * u * w;
+          g = __fdividef(g, 1.0f + __expf(-g)) * u * w[i];
           most = fmaxf(most, fabsf(g));  // a NaN does not enter the maximum
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, d));
-        if (lane < 4) amax[quarter][token] = most;
+        if (lane < 4) amax[token][quarter] = most;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.amax_full[half]);
@@ -313,23 +320,27 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
       const int a = lane >> 2;
       unsigned char* o = p.act.data + row * F + c.n * 128 + quarter * 32 + 8 * (a & 3) + (a & 4);
       const int mine = min(live, c.columns >> 1);
+      // a lane's tokens' scales and their inverses: two divisions for each, not in every lane
+      float* inv = s.inv[half][quarter];
+#pragma unroll 1
+      for (int token = lane; token < 8 * kOf; token += 32) {
+        const float4 m = *reinterpret_cast<const float4*>(amax[token]);
+        const float sc = group_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)), &inv[token]);
+        if (quarter == 0 && token < mine) *p.act.scale(row + token, c.n) = sc;
+      }
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 2 * kOf; ++i) {
         const int token = 8 * (i >> 1) + pair + (i & 1);
-        float inv;
-        const float sc = group_scale(fmaxf(fmaxf(amax[0][token], amax[1][token]), fmaxf(amax[2][token], amax[3][token])), &inv);
         float q[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) q[r] = acc[16 * (i >> 1) + 2 * r + (i & 1)];
-        uint32_t w = quant4(q, inv);
-        uint32_t x = __shfl_xor_sync(kFullMask, w, 4);
-        w = a & 1 ? __byte_perm(w, x, 0x3715) : __byte_perm(w, x, 0x6240);
-        x = __shfl_xor_sync(kFullMask, w, 8);
-        w = a & 2 ? __byte_perm(w, x, 0x3276) : __byte_perm(w, x, 0x5410);
-        if (token < mine) {
-          if (quarter == 0 && a == 0) *p.act.scale(row + token, c.n) = sc;
-          *reinterpret_cast<uint32_t*>(o + static_cast<long long>(token) * F) = w;
-        }
+        uint32_t v = quant4(q, inv[token]);
+        uint32_t x = __shfl_xor_sync(kFullMask, v, 4);
+        v = a & 1 ? __byte_perm(v, x, 0x3715) : __byte_perm(v, x, 0x6240);
+        x = __shfl_xor_sync(kFullMask, v, 8);
+        v = a & 2 ? __byte_perm(v, x, 0x3276) : __byte_perm(v, x, 0x5410);
+        if (token < mine) *reinterpret_cast<uint32_t*>(o + static_cast<long long>(token) * F) = v;
       }
     }
   }
