@@ -330,6 +330,8 @@ def ep_em_combine_weighted_backward(h, grad_out, y, topk_weights, dtype: int, gr
     like = grad_y if grad_y is not None else y
     if like is None:
         raise ValueError("grad_y or y is required")
+    if y is not None and y.shape != like.shape:
+        raise ValueError(f"y is {list(y.shape)}, grad_y {list(like.shape)}")
     if fp8 and grad_y is not None and (grad_y_scales is None or grad_y_scales.dim() != 2):
         raise ValueError("grad_y_scales must be a contiguous [H/128, scales_ld] tensor")
     _check(lib().ep_em_combine_weighted_backward(

@@ -618,8 +618,8 @@ typedef struct {
   const void* pre_weight;  /* dev [H] weight_type, or NULL: no norm in front             */
   const void* gate;        /* dev [H] weight_type, or (gate_per_token) dev bf16 [T][H],
                               or NULL: 1                                                 */
-  const uint8_t* token_mask; /* dev [T] or NULL: 0 marks a padding token, whose rows are
-                                not read and whose results are 0                        */
+  const uint8_t* token_mask; /* dev [T] or NULL: 0 marks a padding token, whose rows may
+                                hold anything and whose results are 0                    */
   int num_tokens;          /* T >= 0                                                     */
   int hidden;              /* H, a multiple of 8, 8..16384                               */
   int gate_per_token;

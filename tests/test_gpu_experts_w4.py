@@ -106,6 +106,24 @@ def test_every_code_and_exponents_apart(rows):
     within(r.read16(out), y, y.abs() * 2.0 ** -8 + sum_err(K) * mag, "product")
 
 
+@pytest.mark.parametrize("low,sig", [(2, 100), (230, -110)])
+def test_exponents_at_both_ends(low, sig):
+    """Exponents near 2^-125 and 2^103, the rows' scales at the other end."""
+    N, K = 128, 256
+    r = Rows([40], "em")
+    xq, xs, x = r.fp8(K, 45)
+    xs[:, :40] *= 2.0 ** sig
+    x = x * 2.0 ** sig
+    q = torch.randint(0, 256, (1, N, K // 2), generator=gen(46), device=DEV, dtype=torch.int32).to(torch.uint8)
+    s = torch.randint(low, low + 8, (1, 1, 2, 512), generator=gen(47), device=DEV, dtype=torch.int32).to(torch.uint8)
+    out = r.out16(N)
+    ep.ep_grouped_matmul_w4(xq, xs, q, s, out, **r.args())
+    y, mag = product64(r, x, unpack(q, s, N, K))
+    # products below fp32's smallest normal number may count as 0: 256 of them, times the row's scale
+    tiny = 256 * 2.0 ** -126 * xs[:, :40].max().item()
+    within(r.read16(out), y, y.abs() * 2.0 ** -8 + sum_err(K) * mag + tiny, "product")
+
+
 def test_special_scales_and_values_stay_in_their_rows():
     """A NaN exponent ruins its weight row only, a NaN code or an infinite scale
     of x its token only."""
