@@ -108,7 +108,8 @@ struct Handover {
   uint32_t from, widest;
   const float* scales;
   uint32_t it, kept;
-  uint64_t* empty;
+  uint64_t *empty, *next;  // ... and the one that hands over the next
+  uint32_t next_parity;
 };
 
 // How a warp reads a block of k of up to kOf chunks of 16 tokens.  Its columns are
@@ -185,10 +186,23 @@ __device__ __forceinline__ void release(const Handover& h) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(h.empty);
 }
 
+// Whether a barrier's phase is complete, without waiting.
+__device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return done != 0;
+}
+
 // Adds a hand-over's `blocks` blocks of k, `items` items: 64 registers' loads are on
 // their way at a time, and the accumulator goes back as soon as the last are here.
+// Returns whether the next hand-over is there already, asked for before the last
+// sums, since the answer takes as long as they do (decode 51.0 -> 49.9 us; where a
+// hand-over fills the registers, one more costs spills: prefill 596 -> 748 us).
 template <bool kSwiglu, int kOf>
-__device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, int blocks, int items) {
+__device__ __forceinline__ bool take(float (&acc)[16 * kOf], const Handover& h, int blocks, int items) {
   using P = Plan<kSwiglu, kOf>;
   uint32_t v[4][16];
   load_item<kSwiglu, kOf, 0>(v, h, items), load_item<kSwiglu, kOf, 1>(v, h, items);
@@ -204,8 +218,10 @@ __device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, 
   }
 #pragma unroll
   for (int m = 0; m < 4; ++m) tmem_load_wait16(v[m]);
+  bool next = false;
   if (P::kMost <= 4 || items <= 4) {
     release(h);
+    if constexpr (kOf != kChunks) next = phase_over(smem_u32(h.next), h.next_parity);
     add_item<kSwiglu, kOf, 0>(acc, v, scales, items), add_item<kSwiglu, kOf, 1>(acc, v, scales, items);
     add_item<kSwiglu, kOf, 2>(acc, v, scales, items), add_item<kSwiglu, kOf, 3>(acc, v, scales, items);
   } else if constexpr (P::kMost > 4) {
@@ -218,10 +234,12 @@ __device__ __forceinline__ void take(float (&acc)[16 * kOf], const Handover& h, 
 #pragma unroll
     for (int m = 4; m < P::kMost; ++m) tmem_load_wait16(v[m & 3]);
     release(h);
+    if constexpr (kOf != kChunks) next = phase_over(smem_u32(h.next), h.next_parity);
     add_item<kSwiglu, kOf, 4>(acc, v, scales, items), add_item<kSwiglu, kOf, 5>(acc, v, scales, items);
     if constexpr (P::kMost > 6)
       add_item<kSwiglu, kOf, 6>(acc, v, scales, items), add_item<kSwiglu, kOf, 7>(acc, v, scales, items);
   }
+  return next;
 }
 
 // What all warps know of the launch.
@@ -243,7 +261,7 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
   const int F = p.N >> 1;
   uint32_t it = 0, group = 0;  // blocks of k and hand-overs of all tiles
   int turn = 0;
-  bool ok;
+  bool ok, ready = false;  // whether the next hand-over is there
   for (unsigned t = blockIdx.x; t < l.tiles; t += gridDim.x, turn ^= 1) {
     const Tile c = tile_at(p.groups, prefix, l.tiles_n, t);
     // a warp's columns: all of its half's, or half of both halves' (SwiGLU: 8
@@ -256,12 +274,15 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
     for (int kb = 0; kb < l.blocks_k; ++group) {
       const uint32_t ac = group & 1;
       const int n = min(l.per, l.blocks_k - kb);
-      ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (group >> 1) & 1, quit, err));
-      if (!ok) return;
+      if (!__all_sync(kFullMask, ready)) {
+        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (group >> 1) & 1, quit, err));
+        if (!ok) return;
+      }
       tmem_fence_after();
-      const Handover h{from + ac * l.acc_columns, l.widest, s.x_scale + first + pair, it, l.kept, &s.acc_empty[ac]};
+      const Handover h{from + ac * l.acc_columns, l.widest, s.x_scale + first + pair, it, l.kept, &s.acc_empty[ac],
+                       &s.acc_full[ac ^ 1], ((group + 1) >> 1) & 1};
       using P = Plan<kSwiglu, kOf>;
-      take<kSwiglu, kOf>(acc, h, n, kOf == kChunks ? (c.columns + 16 * P::kPlanes - 1) / (16 * P::kPlanes) * P::kPlanes : n * kOf);
+      ready = take<kSwiglu, kOf>(acc, h, n, kOf == kChunks ? (c.columns + 16 * P::kPlanes - 1) / (16 * P::kPlanes) * P::kPlanes : n * kOf);
       kb += n;
       it += n;
     }
