@@ -100,9 +100,196 @@ __device__ __forceinline__ float team_sum(float v, float* part, int team, int wa
 
 }  // namespace
 
-// kWords: 16-byte words of bf16 that a thread holds of each row.
+namespace {
+
+constexpr int kBackThreads = 512, kBackWarps = kBackThreads / 32;
+constexpr int kWordsEach = 2;                               // 8-channel words of a row that a thread owns
+constexpr int kBackHidden = kBackThreads * kWordsEach * 8;  // beyond: k_block_norm_backward_long
+constexpr int kMaxStages = 4;
+constexpr int kNarrowWarps = 14;
+
+// Barriers and partial sums of a block's teams.
+struct RingShared {
+  uint64_t full[kBackWarps][kMaxStages];
+  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team], zeros past the team
+  int quit;
+};
+
+}  // namespace
+
+// Forward: a team of warps takes a row at a time; its tensors' rows arrive by bulk
+// copies in a ring of stages in shared memory, and a thread keeps its channels'
+// weights in registers over all rows.  The first barrier of a row's sums says that
+// the stage of the row before has been read, so its refill needs no other.
+// kY: there is a block behind; kToken: its gate comes per token.
+template <bool kRes32, bool kY, bool kToken>
+__global__ void __launch_bounds__(kBackThreads, 1) k_block_norm(const BlockNormArgs a, int warps, int num_stages) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ RingShared s;
+  const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
+  const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads, warp = tid >> 5;
+  const int words = a.H >> 3;
+  constexpr int kR = kRes32 ? 4 : 2, kCopies = 1 + kY + kToken;
+  const int o_y = kR * a.H, o_g = o_y + (kY ? 2 * a.H : 0), stage_bytes = o_g + (kToken ? 2 * a.H : 0);
+  unsigned char* stages = ring + static_cast<size_t>(team) * num_stages * stage_bytes;
+  uint64_t* full = s.full[team];
+  // the i-th tensor's rows are copied by lane 0 of warp i % warps
+  unsigned mine = 0;
+  for (int i = 0; lane == 0 && i < kCopies; ++i)
+    if (i % warps == warp) mine |= 1u << i;
+  if (tid == 0) {
+    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], kCopies);
+    s.quit = 0;
+    mbar_init_fence();
+  }
+  if (tid < 32) s.part[team][tid >> 4][tid & 15] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  after_previous();
+  __syncthreads();
+  const long long step = static_cast<long long>(gridDim.x) * teams;
+  const long long first = static_cast<long long>(blockIdx.x) * teams + team;
+  auto fetch = [&](long long t, int st) {
+    if (t >= a.T || !mine) return;
+    unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
+    const long long at = t * a.H;
+    int i = 0;
+    auto copy = [&](int to, const void* from, int size) {
+      if (!(mine >> i++ & 1)) return;
+      mbar_arrive_expect_tx(&full[st], size * a.H);
+      bulk_load(d + to, static_cast<const char*>(from) + at * size, size * a.H, &full[st]);
+    };
+    copy(0, a.residual, kR);
+    if (kY) copy(o_y, a.y, 2);
+    if (kToken) copy(o_g, a.gate, 2);
+  };
+  for (int i = 0; i < num_stages; ++i) fetch(first + i * step, i);
+
+  // the channels' constants: pre, and q = scale post (times gate where it is a vector)
+  const bool post = kY && a.post, pre = a.x != nullptr;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  float2 wp[kWordsEach][4], q[kWordsEach][4];
+#pragma unroll
+  for (int k = 0; k < kWordsEach; ++k) {
+    const int c = tid + k * threads;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wp[k][j] = both(0.0f), q[k][j] = both(a.scale);
+    if (c >= words) continue;
+    float2 v[4];
+    if (pre) load8(a.pre, a.weight32, c, wp[k]);
+    if (post) {
+      load8(a.post, a.weight32, c, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[k][j] = mul2(q[k][j], v[j]);
+    }
+    if (kY && !kToken && a.gate) {
+      load8(a.gate, a.weight32, c, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[k][j] = mul2(q[k][j], v[j]);
+    }
+  }
+
+  int st = 0, phase = 0, turn = 0;
+  // sum over the team; the other of the two sets of parts at each call
+  auto sum = [&](float2 v) {
+    float f = warp_sum(v.x + v.y);
+    if (warps == 1) return f;
+    float4* part = s.part[team][turn];
+    turn ^= 1;
+    if (lane == 0) part[warp].x = f;
+    team_barrier(team, threads);
+    f = part[lane & 15].x;
+#pragma unroll
+    for (int b = 8; b; b >>= 1) f += __shfl_xor_sync(kFullMask, f, b);
+    return f;
+  };
+  bool next_live = !a.mask || first >= a.T || a.mask[first];
+  for (long long t = first; t < a.T; t += step) {
+    const bool live = next_live;
+    if (a.mask && t + step < a.T) next_live = a.mask[t + step];
+    const unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
+    const bool landed = wait_or_quit(&full[st], phase, &s.quit, nullptr);
+    float2 h[kWordsEach][4], y[kY ? kWordsEach : 1][4];
+    float2 t1 = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < kWordsEach; ++k) {
+      const int c = tid + k * threads;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[k][j] = both(0.0f);
+        if (kY) y[k][j] = both(0.0f);
+      }
+      if (c >= words || !live) continue;
+      load8(d, kRes32, c, h[k]);
+      if (kY) {
+        load8(d + o_y, false, c, y[k]);
+        if (post) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t1 = fma2(y[k][j], y[k][j], t1);
+        }
+      }
+    }
+    if (!landed) {  // a copy that never came: NaN, not old values
+#pragma unroll
+      for (int k = 0; k < kWordsEach; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] = both(__int_as_float(0x7fc00000));
+    }
+    float r1 = 1.0f;
+    if (post) r1 = rsqrtf(fmaf(sum(t1), inv_h, a.eps));
+    if (!live) r1 = 0.0f;
+    auto refill = [&]() {
+      if (t != first) fetch(t + (num_stages - 1) * step, st ? st - 1 : num_stages - 1);
+    };
+    if (post) refill();
+    const long long row = t * words;
+    if (kY) {
+      if (post && tid == 0 && a.rstd) a.rstd[t] = r1;
+#pragma unroll
+      for (int k = 0; k < kWordsEach; ++k) {
+        const int c = tid + k * threads;
+        if (c >= words) continue;
+        float2 u[4];
+        if (kToken) load8(d + o_g, false, c, u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 v = mul2(y[k][j], both(r1));
+          if (kToken) v = live ? mul2(v, u[j]) : both(0.0f);
+          h[k][j] = fma2(q[k][j], v, h[k][j]);
+        }
+        store8(a.new_residual, kRes32, row + c, h[k]);
+      }
+    }
+    if (pre) {
+      float2 t2 = both(0.0f);
+#pragma unroll
+      for (int k = 0; k < kWordsEach; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t2 = fma2(h[k][j], h[k][j], t2);
+      float r2 = rsqrtf(fmaf(sum(t2), inv_h, a.eps));
+      if (!live) r2 = 0.0f;
+      if (!post) refill();
+      if (tid == 0 && a.rstd) a.rstd[a.T + t] = r2;
+#pragma unroll
+      for (int k = 0; k < kWordsEach; ++k) {
+        const int c = tid + k * threads;
+        if (c >= words) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] = mul2(mul2(h[k][j], both(r2)), wp[k][j]);
+        store8(a.x, false, row + c, h[k]);
+      }
+    } else if (!post) {
+      if (warps > 1) team_barrier(team, threads);
+      else __syncwarp();
+      refill();
+    }
+    __syncwarp();
+    if (++st == num_stages) st = 0, phase ^= 1;
+  }
+}
+
+// The forward pass of rows too long for that: a block a row, the row in its threads'
+// registers.  kWords: 16-byte words of bf16 that a thread holds of each row.
 template <int kWords, bool kRes32>
-__global__ void __launch_bounds__(512) k_block_norm(const BlockNormArgs a, int warps) {
+__global__ void __launch_bounds__(512) k_block_norm_long(const BlockNormArgs a, int warps) {
   __shared__ float part[2][32];
   after_previous();
   const int per_team = warps * 32, teams = blockDim.x / per_team;
@@ -210,24 +397,7 @@ __global__ void __launch_bounds__(512) k_block_norm(const BlockNormArgs a, int w
   }
 }
 
-namespace {
-
-constexpr int kBackThreads = 512, kBackWarps = kBackThreads / 32;
-constexpr int kWordsEach = 2;                               // 8-channel words of a row that a thread owns
-constexpr int kBackHidden = kBackThreads * kWordsEach * 8;  // beyond: k_block_norm_backward_long
-constexpr int kMaxStages = 4;
-constexpr int kNarrowWarps = 14;
-
-struct BackShared {
-  uint64_t full[kBackWarps][kMaxStages];
-  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team], zeros past the team
-  int quit;
-};
-
-}  // namespace
-
-// A team of warps takes a row at a time; its tensors' rows arrive by bulk copies in
-// a ring of two stages or more in shared memory, read twice: for the sums, and for
+// Backward: the same teams and rings, of two stages or more, read twice: for the sums, and for
 // the results.  The barrier of a row's sums says that the stage of the row before
 // has been read, so its refill needs no other; with an fp32 residual, where a long
 // row leaves room for two stages only, a second barrier lets the refill start half a
@@ -240,7 +410,7 @@ template <int kThreads, bool kRes32, bool kPre, bool kY, bool kToken>
 __global__ void __launch_bounds__(kThreads, 1)
     k_block_norm_backward(const BlockNormBackwardArgs a, int warps, int num_stages) {
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ BackShared s;
+  __shared__ RingShared s;
   const BlockNormArgs& n = a.n;
   const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
   const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads, warp = tid >> 5;
@@ -628,27 +798,53 @@ __global__ void __launch_bounds__(256) k_block_norm_sums(const BlockNormBackward
   }
 }
 
+namespace {
+
+// Shared memory for rings on the current device.
+cudaError_t ring_room(int* room) {
+  int device = 0, smem = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+  *room = smem - static_cast<int>(sizeof(RingShared));
+  return e;
+}
+
+// Warps that hold a row.
+int row_warps(int H) { return (H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach); }
+
+}  // namespace
+
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaStream_t stream) {
-  const int words = a.H / 8;
-  int warps = 1;
-  while (warps * 32 * 4 < words) warps *= 2;
-  const int per_thread = (words + warps * 32 - 1) / (warps * 32);
-  const int threads = warps < 8 ? 256 : warps * 32, teams = threads / (warps * 32);
-  using Kernel = void (*)(BlockNormArgs, int);
-  static const Kernel kernels[2][4] = {
-      {k_block_norm<1, false>, k_block_norm<2, false>, k_block_norm<3, false>, k_block_norm<4, false>},
-      {k_block_norm<1, true>, k_block_norm<2, true>, k_block_norm<3, true>, k_block_norm<4, true>}};
-  const Kernel kernel = kernels[res32][per_thread - 1];
-  static std::atomic<int> resident[2][4][2];  // blocks an SM holds
-  int occ = resident[res32][per_thread - 1][threads > 256].load(std::memory_order_relaxed);
-  if (!occ) {
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0);
-    if (e != cudaSuccess) return e;
-    resident[res32][per_thread - 1][threads > 256].store(occ, std::memory_order_relaxed);
+  cudaError_t e;
+  if (a.H <= kBackHidden) {
+    const bool y = a.y != nullptr, token = y && a.gate_per_token;
+    using Kernel = void (*)(BlockNormArgs, int, int);
+    static const Kernel kernels[2][3] = {
+        {k_block_norm<false, false, false>, k_block_norm<false, true, false>, k_block_norm<false, true, true>},
+        {k_block_norm<true, false, false>, k_block_norm<true, true, false>, k_block_norm<true, true, true>}};
+    const Kernel kernel = kernels[res32][y + token];
+    static std::atomic<unsigned long long> ready[6];  // devices set up, a bit each
+    int room = 0;
+    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[res32 * 3 + y + token], 0)) != cudaSuccess ||
+        (e = ring_room(&room)) != cudaSuccess)
+      return e;
+    const int bytes = a.H * ((res32 ? 4 : 2) + (y ? 2 : 0) + (token ? 2 : 0));
+    const int warps = row_warps(a.H), per_sm = (a.T + sms - 1) / sms;
+    int teams = kBackWarps / warps;
+    if (teams > per_sm) teams = per_sm;
+    if (teams > room / (2 * bytes)) teams = room / (2 * bytes);
+    int stages = room / (bytes * teams);
+    if (stages > kMaxStages) stages = kMaxStages;
+    const int most = (a.T + teams - 1) / teams;
+    return launch_early(kernel, 1, dim3(sms < most ? sms : most), dim3(teams * warps * 32), bytes * teams * stages, stream,
+                        a, warps, stages);
   }
-  const long long need = (static_cast<long long>(a.T) + teams - 1) / teams, most = static_cast<long long>(sms) * occ;
-  return launch_early(kernel, 1, dim3(static_cast<unsigned>(need < most ? need : most)),
-                      dim3(threads), 0, stream, a, warps);
+  int warps = 16;
+  const int words = a.H / 8, per_thread = (words + warps * 32 - 1) / (warps * 32);
+  using Kernel = void (*)(BlockNormArgs, int);
+  static const Kernel kernels[2][2] = {{k_block_norm_long<3, false>, k_block_norm_long<4, false>},
+                                       {k_block_norm_long<3, true>, k_block_norm_long<4, true>}};
+  return launch_early(kernels[res32][per_thread - 3], 1, dim3(sms < a.T ? sms : a.T), dim3(warps * 32), 0, stream, a, warps);
 }
 
 namespace {
@@ -679,13 +875,10 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
   const bool gate = token && block;
   const int r = res32 ? 4 : 2;
   const int all = a.n.H * (2 * r + 4 + (token ? 2 : 0)), bytes = a.n.H * ((a.grad_new ? r : 0) + (a.grad_x ? r + 2 : 0) + (a.need_y ? 2 : 0) + (gate ? 2 : 0));
-  int device = 0, smem = 0;
-  if ((e = cudaGetDevice(&device)) != cudaSuccess ||
-      (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device)) != cudaSuccess)
-    return e;
-  const int room = smem - static_cast<int>(sizeof(BackShared));
+  int room = 0;
+  if ((e = ring_room(&room)) != cudaSuccess) return e;
   if (a.n.H <= kBackHidden && 2 * all <= room) {
-    const int warps = (a.n.H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach), per_sm = (a.n.T + sms - 1) / sms;
+    const int warps = row_warps(a.n.H), per_sm = (a.n.T + sms - 1) / sms;
     const bool wide = warps > kNarrowWarps;
     int teams = (wide ? kBackWarps : kNarrowWarps) / warps;
     if (teams > per_sm) teams = per_sm;
