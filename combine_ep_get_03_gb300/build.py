@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libep_gb300.so")
-SOURCES = ["api.cu", "layout.cu", "dispatch.cu", "combine.cu", "combine_backward.cu", "ll_dispatch.cu", "layout_noalloc.cu", "scatter_tma.cu", "dispatch_fused.cu",
+SOURCES = ["api.cu", "layout.cu", "dispatch.cu", "combine.cu", "combine_weighted.cu", "combine_backward.cu", "ll_dispatch.cu", "layout_noalloc.cu", "scatter_tma.cu", "dispatch_fused.cu",
            "em_weights.cu", "experts_api.cu", "gate.cu", "block_norm.cu", "grouped_matmul.cu", "grouped_matmul_w4.cu", "swiglu_backward.cu", "weight_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -8,6 +8,7 @@
 #include <new>
 
 #include "ep.h"
+#include "em_combine.cuh"
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "routing.cuh"
@@ -22,7 +23,7 @@ struct ep_handle {
   size_t layout_smem, ll_smem, layout_tokens_smem;
   int layout_cmax, ll_cmax;
   // occupancy (blocks per SM) of the persistent kernels
-  int occ_dispatch[2], occ_combine[5];  // combine: rank-major bf16, rank-major e4m3, low latency, expert-major, weighted
+  int occ_dispatch[2], occ_combine[4];  // combine: rank-major bf16, rank-major e4m3, low latency, expert-major
   // TMA scatter: row stages and consumer warps per block for
   // [fp8][rank-major, low latency, expert-major]; 0 stages = rows too long,
   // the register-resident kernels are used instead (none for expert-major)
@@ -336,8 +337,8 @@ ep_status_t ep_handle_create(int R, int E, int k, int H, int max_tpr, ep_handle_
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, ep::dispatch_kernel(m == 1), ep::dispatch_threads(), 0);
     h->occ_dispatch[m] = occ > 0 ? occ : 1;
   }
-  for (int m = 0; m < 5; ++m) {
-    const int src = m < 2 ? ep::kSrcRanks : m - 1;
+  for (int m = 0; m < 4; ++m) {
+    const int src = m < 2 ? ep::kSrcRanks : m == 2 ? ep::kSrcLowLatency : ep::kSrcExpertMajor;
     int occ = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, ep::combine_kernel(src, m == 1), ep::combine_threads(),
                                                   ep::combine_smem_bytes(src, R, E));
@@ -876,11 +877,9 @@ ep_status_t ep_em_get_layout(ep_handle_t h, int* num_recv_tokens_per_expert, int
   return static_cast<ep_status_t>(hp[0]);
 }
 
-namespace {
-
-// topk_weights null: unweighted.
-ep_status_t em_combine(ep_handle* h, const void* y, int64_t y_rows, const float* topk_weights, void* out, int num_sms,
-                       ep_stream_t stream) {
+ep_status_t ep_em_combine(ep_handle_t h, const void* y, int64_t y_rows, void* out, int num_sms, ep_stream_t stream) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  if (h->T_em < 0) return EP_ERR_STATE;
   const int T = h->T_em;
   if (y_rows < 0 || (T > 0 && (!out || (y_rows > 0 && !y)))) return EP_ERR_INVALID_ARG;
   if ((y && !aligned16(y)) || (out && !aligned16(out))) return EP_ERR_INVALID_ARG;
@@ -899,30 +898,37 @@ ep_status_t em_combine(ep_handle* h, const void* y, int64_t y_rows, const float*
   a.E = h->E;
   a.ent_idx = h->em_idx;
   a.ent_slot = h->em_slot;
-  a.topk_weights = topk_weights;
   a.expert_offset = h->em_offset;
   a.err = h->err;
-  const int src = topk_weights ? ep::kSrcExpertMajorWeighted : ep::kSrcExpertMajor;
-  const int blocks = grid_for(h, h->occ_combine[src + 1], num_sms, T * ((h->H + 1023) / 1024), ep::combine_threads() / 32);
-  ep::launch_combine(a, src, false, blocks, reinterpret_cast<cudaStream_t>(stream));
-  if (h->debug) std::fprintf(stderr, "[ep] em combine T=%d%s: %d blocks\n", T, topk_weights ? " weighted" : "", blocks);
+  const int blocks = grid_for(h, h->occ_combine[3], num_sms, T * ((h->H + 1023) / 1024), ep::combine_threads() / 32);
+  ep::launch_combine(a, ep::kSrcExpertMajor, false, blocks, reinterpret_cast<cudaStream_t>(stream));
+  if (h->debug) std::fprintf(stderr, "[ep] em combine T=%d: %d blocks\n", T, blocks);
   return cuda_status(cudaGetLastError(), "k_combine(em) launch");
 }
 
-}  // namespace
+namespace {
 
-ep_status_t ep_em_combine(ep_handle_t h, const void* y, int64_t y_rows, void* out, int num_sms, ep_stream_t stream) {
-  if (!h) return EP_ERR_INVALID_ARG;
-  if (h->T_em < 0) return EP_ERR_STATE;
-  return em_combine(h, y, y_rows, nullptr, out, num_sms, stream);
-}
+ep::EmEntries em_entries(const ep_handle* h) { return ep::EmEntries{h->em_idx, h->em_slot, h->em_offset, h->T_em, h->k, h->err}; }
+
+}  // namespace
 
 ep_status_t ep_em_combine_weighted(ep_handle_t h, const void* y, int64_t y_rows, const float* topk_weights, void* out,
                                    int num_sms, ep_stream_t stream) {
   if (!h) return EP_ERR_INVALID_ARG;
   if (h->T_em < 0) return EP_ERR_STATE;
-  if (h->T_em > 0 && (!topk_weights || !aligned4(topk_weights))) return EP_ERR_INVALID_ARG;
-  return em_combine(h, y, y_rows, topk_weights, out, num_sms, stream);
+  if (y_rows < 0 || (h->T_em > 0 && (!topk_weights || !out || (y_rows > 0 && !y)))) return EP_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(out) || !aligned4(topk_weights)) return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_device(h);
+  if (st != EP_OK || h->T_em == 0) return st;
+  ep::CombineWeightedArgs a{};
+  a.entries = em_entries(h);
+  a.y = static_cast<const uint16_t*>(y);
+  a.topk_weights = topk_weights;
+  a.out = static_cast<uint16_t*>(out);
+  a.rows = y_rows;
+  a.H = h->H;
+  return cuda_status(ep::launch_combine_weighted(a, sms_for(h, num_sms), reinterpret_cast<cudaStream_t>(stream)),
+                     "k_combine_weighted launch");
 }
 
 ep_status_t ep_em_combine_weighted_backward(ep_handle_t h, const void* grad_out, const void* y, int64_t rows,
@@ -943,23 +949,17 @@ ep_status_t ep_em_combine_weighted_backward(ep_handle_t h, const void* grad_out,
   ep_status_t st = check_device(h);
   if (st != EP_OK || T == 0) return st;
   ep::CombineBackwardArgs a{};
+  a.entries = em_entries(h);
   a.grad_out = static_cast<const uint16_t*>(grad_out);
   a.y = static_cast<const uint16_t*>(y);
   a.topk_weights = topk_weights;
-  a.ent_idx = h->em_idx;
-  a.ent_slot = h->em_slot;
-  a.expert_offset = h->em_offset;
   a.grad_y = grad_y;
   a.grad_y_scales = grad_y_scales;
   a.grad_weights = grad_topk_weights;
   a.scales_ld = scales_ld;
   a.rows = rows;
-  a.entries = static_cast<long long>(T) * h->k;
   a.H = h->H;
-  a.k = h->k;
-  a.err = h->err;
-  const int sms = num_sms <= 0 || num_sms > h->num_sms ? h->num_sms : num_sms;
-  return cuda_status(ep::launch_combine_backward(a, fp8, sms, reinterpret_cast<cudaStream_t>(stream)),
+  return cuda_status(ep::launch_combine_backward(a, fp8, sms_for(h, num_sms), reinterpret_cast<cudaStream_t>(stream)),
                      "k_combine_backward launch");
 }
 

@@ -15,8 +15,7 @@
 //                over t's unmasked entries in ascending expert id (k-index
 //                breaks ties), from +0.0;
 //  expert-major: out[t] = bf16( sum of fp32(y[row_j]) ) over t's unmasked
-//                entries in ascending expert id, from +0.0 with RN adds; weighted:
-//                as low latency.
+//                entries in ascending expert id, from +0.0 with RN adds.
 //
 // HBM-bound gather-reduce.  Two blocks per SM (at most 128 registers a
 // thread), three for the e4m3 input (at most 85): its dequantisation makes it
@@ -120,8 +119,6 @@ __device__ __forceinline__ void add_e4m3_slab(float (&acc)[kChunks][16], const E
 
 template <int kSrc, bool kFP8>
 __global__ void __launch_bounds__(kCombineThreads, kFP8 ? 3 : 2) k_combine(CombineArgs a) {
-  constexpr bool kEM = kSrc == kSrcExpertMajor || kSrc == kSrcExpertMajorWeighted;
-  constexpr bool kWeighted = kSrc == kSrcLowLatency || kSrc == kSrcExpertMajorWeighted;
   extern __shared__ int base_smem[];  // rank_offset [R+1] or expert_offset [E+1]
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
@@ -130,7 +127,7 @@ __global__ void __launch_bounds__(kCombineThreads, kFP8 ? 3 : 2) k_combine(Combi
   if (kSrc == kSrcRanks) {
     for (int r = threadIdx.x; r <= a.R; r += kCombineThreads) base_smem[r] = a.rank_offset[r];
     __syncthreads();
-  } else if (kEM) {
+  } else if (kSrc == kSrcExpertMajor) {
     for (int e = threadIdx.x; e <= a.E; e += kCombineThreads) base_smem[e] = a.expert_offset[e];
     __syncthreads();
   }
@@ -157,7 +154,7 @@ __global__ void __launch_bounds__(kCombineThreads, kFP8 ? 3 : 2) k_combine(Combi
       const int s = a.ent_slot[static_cast<size_t>(t) * a.k + lane];
       if (e >= 0 && s >= 0) {
         row = kSrc == kSrcLowLatency ? static_cast<long long>(e) * a.M + s : static_cast<long long>(base_smem[e]) + s;
-        if (kWeighted) w = a.topk_weights[static_cast<size_t>(t) * a.k + lane];
+        if (kSrc == kSrcLowLatency) w = a.topk_weights[static_cast<size_t>(t) * a.k + lane];
         key = e;
       }
     }
@@ -184,11 +181,11 @@ __global__ void __launch_bounds__(kCombineThreads, kFP8 ? 3 : 2) k_combine(Combi
     // positions are distinct, so each slot below n is written once
     if (valid) {
       s_row[warp][pos] = row;
-      if (kWeighted) s_w[warp][pos] = w;
+      if (kSrc == kSrcLowLatency) s_w[warp][pos] = w;
     }
     __syncwarp();
     const long long srow = lane < n ? s_row[warp][lane] : -1;
-    const float sw = kWeighted && lane < n ? s_w[warp][lane] : 0.0f;
+    const float sw = kSrc == kSrcLowLatency && lane < n ? s_w[warp][lane] : 0.0f;
     __syncwarp();  // read before the next item writes
 
     if (kSrc == kSrcRanks && a.recv_topk_weights && part == 0) {
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(kCombineThreads, kFP8 ? 3 : 2) k_combine(Combi
                 const uint32_t q[4] = {v[s][c].x, v[s][c].y, v[s][c].z, v[s][c].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  if (kWeighted) {
+                  if (kSrc == kSrcLowLatency) {
                     acc[c][2 * i] = __fmaf_rn(ws, bf16_lo(q[i]), acc[c][2 * i]);
                     acc[c][2 * i + 1] = __fmaf_rn(ws, bf16_hi(q[i]), acc[c][2 * i + 1]);
                   } else {
@@ -302,13 +299,12 @@ const void* combine_fn(int src, bool fp8) {
     return fp8 ? reinterpret_cast<const void*>(k_combine<kSrcRanks, true>)
                : reinterpret_cast<const void*>(k_combine<kSrcRanks, false>);
   if (src == kSrcLowLatency) return reinterpret_cast<const void*>(k_combine<kSrcLowLatency, false>);
-  if (src == kSrcExpertMajorWeighted) return reinterpret_cast<const void*>(k_combine<kSrcExpertMajorWeighted, false>);
   return reinterpret_cast<const void*>(k_combine<kSrcExpertMajor, false>);
 }
 }  // namespace
 
 size_t combine_smem_bytes(int src, int R, int E) {
-  return src == kSrcRanks ? 4 * static_cast<size_t>(R + 1) : src == kSrcLowLatency ? 0 : 4 * static_cast<size_t>(E + 1);
+  return src == kSrcRanks ? 4 * static_cast<size_t>(R + 1) : src == kSrcExpertMajor ? 4 * static_cast<size_t>(E + 1) : 0;
 }
 
 void launch_combine(const CombineArgs& a, int src, bool fp8, int blocks, cudaStream_t stream) {
@@ -320,8 +316,6 @@ void launch_combine(const CombineArgs& a, int src, bool fp8, int blocks, cudaStr
       (void)launch_kernel(k_combine<kSrcRanks, false>, dim3(blocks), dim3(kCombineThreads), smem, stream, a);
   } else if (src == kSrcLowLatency) {
     (void)launch_kernel(k_combine<kSrcLowLatency, false>, dim3(blocks), dim3(kCombineThreads), smem, stream, a);
-  } else if (src == kSrcExpertMajorWeighted) {
-    (void)launch_kernel(k_combine<kSrcExpertMajorWeighted, false>, dim3(blocks), dim3(kCombineThreads), smem, stream, a);
   } else {
     (void)launch_kernel(k_combine<kSrcExpertMajor, false>, dim3(blocks), dim3(kCombineThreads), smem, stream, a);
   }

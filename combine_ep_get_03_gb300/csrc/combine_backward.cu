@@ -8,6 +8,7 @@
 // product ends in one exchange inside the warp: its order, and with it the result,
 // is always the same.
 #include "device_common.cuh"
+#include "em_combine.cuh"
 #include "ep_internal.h"
 #include "experts.cuh"
 #include "pairs.cuh"
@@ -38,12 +39,14 @@ template <bool kFP8>
 __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const CombineBackwardArgs a) {
   const int lane = threadIdx.x & 31;
   const int words = a.H >> 3;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < a.entries;
+  const EmEntries& n = a.entries;
+  const long long entries = static_cast<long long>(n.T) * n.k;
+  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < entries;
        i += static_cast<long long>(gridDim.x) * kWarps) {
-    const int e = a.ent_idx[i], slot = a.ent_slot[i];
-    long long row = e >= 0 && slot >= 0 ? static_cast<long long>(a.expert_offset[e]) + slot : -1;
+    const int e = n.idx[i], slot = n.slot[i];
+    long long row = e >= 0 && slot >= 0 ? static_cast<long long>(n.offset[e]) + slot : -1;
     if (row >= a.rows) {
-      if (lane == 0) latch_error(a.err, kErrCapacity);
+      if (lane == 0) latch_error(n.err, kErrCapacity);
       row = -1;
     }
     if (row < 0) {
@@ -51,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const CombineB
       continue;
     }
     const float w = a.topk_weights ? a.topk_weights[i] : 0.0f;
-    const uint16_t* g = a.grad_out + i / a.k * a.H;
+    const uint16_t* g = a.grad_out + i / n.k * a.H;
     const uint16_t* y = a.grad_weights ? a.y + row * a.H : nullptr;
     float2 dot = both(0.0f);
     for (int c0 = lane; c0 - lane < words; c0 += 32 * kBatch) {
@@ -120,7 +123,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const CombineB
 
 cudaError_t launch_combine_backward(const CombineBackwardArgs& a, bool fp8, int sms, cudaStream_t stream) {
   auto kernel = fp8 ? k_combine_backward<true> : k_combine_backward<false>;
-  const long long need = (a.entries + kWarps - 1) / kWarps, most = static_cast<long long>(sms) * 4;
+  const long long entries = static_cast<long long>(a.entries.T) * a.entries.k, need = (entries + kWarps - 1) / kWarps;
+  const long long most = static_cast<long long>(sms) * 4;
   return launch_kernel(kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(kThreads), 0, stream, a);
 }
 

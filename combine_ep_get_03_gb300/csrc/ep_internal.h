@@ -85,8 +85,7 @@ int dispatch_threads();
 const void* dispatch_kernel(bool fp8);
 
 // combine: one warp per (token, 1024-channel part), every receive layout.
-// (kSrcExpertMajorWeighted: combine only)
-enum : int { kSrcRanks = 0, kSrcLowLatency = 1, kSrcExpertMajor = 2, kSrcExpertMajorWeighted = 3 };
+enum : int { kSrcRanks = 0, kSrcLowLatency = 1, kSrcExpertMajor = 2 };
 struct CombineArgs {
   const void* y;               // rows [.][H]: bf16, or e4m3 bytes with y_scales
   const float* y_scales;       // [y_rows][H/128] (e4m3 rows)
@@ -102,7 +101,7 @@ struct CombineArgs {
   // its slot inside the expert
   const int* ent_idx;          // [T][k]
   const int* ent_slot;         // [T][k]
-  const float* topk_weights;   // [T][k] (low latency, expert-major weighted)
+  const float* topk_weights;   // [T][k] (low latency)
   int M;                       // low latency: rows per expert
   const int* expert_offset;    // expert-major: [E+1] first row of each expert
   int* err;
@@ -111,23 +110,6 @@ void launch_combine(const CombineArgs& a, int src, bool fp8, int blocks, cudaStr
 size_t combine_smem_bytes(int src, int R, int E);
 int combine_threads();
 const void* combine_kernel(int src, bool fp8);
-
-// Backward of the weighted expert-major combine: a warp per (token, k) entry.
-struct CombineBackwardArgs {
-  const uint16_t* grad_out;    // [T][H] bf16
-  const uint16_t* y;           // [rows][H] bf16 (with grad_weights)
-  const float* topk_weights;   // [T][k] (with grad_y)
-  const int* ent_idx;          // [T][k]
-  const int* ent_slot;         // [T][k]
-  const int* expert_offset;    // [E+1]
-  void* grad_y;                // [rows][H] bf16 or e4m3, or null
-  float* grad_y_scales;        // [H/128][scales_ld] (e4m3)
-  float* grad_weights;         // [T][k] or null
-  long long scales_ld, rows, entries;
-  int H, k;
-  int* err;
-};
-cudaError_t launch_combine_backward(const CombineBackwardArgs& a, bool fp8, int sms, cudaStream_t stream);
 
 // Control words shared by the row-moving kernels (the handle's
 // fused_barrier array): [0] grid-barrier arrivals, [1] launch generation,
