@@ -4,12 +4,19 @@
 // Everything between loads and stores is fp32; the second norm takes h before it
 // is rounded.
 //
-// Forward.  HBM-bound: each row of y and of the residual is read once, h and x are
-// written once.  A team of 1, 2, 4, .. 16 warps takes a row, so that a thread
-// holds up to 32 channels in registers across the two sums of squares; a sum
-// ends in one exchange through shared memory, in a fixed order.
+// Both are HBM-bound: each tensor's row is read once and each result's written once.
+// A team of warps takes a row, two 8-channel words a thread; short rows leave room
+// for several teams in a block, one block an SM.  A sum over a row ends in an exchange through
+// shared memory, in a fixed order.
 //
-// Backward.  With hn = h rstd2, yn = y rstd1, a = grad_x pre, q = scale gate post:
+// Forward: two sums a row, of y^2 and of h^2.  16 384 tokens of 7168 channels: fp32
+// residual 224 us (6.3 TB/s), bf16 150; 4 096 channels fp32 123; one token 3.6 us in
+// a graph.  (Rows loaded to registers, a block of 8 warps a row: 226 us with the next
+// rows fetched to L2, 158, 132 and 4.9; 240, 191 without.  The second sum exchanged
+// with the next row's first, one barrier a row: 245, 150, 145 and 3.9.)
+//
+// Backward.  8 192 tokens of 7168, gate a vector: bf16 115 us (6.1 TB/s), fp32 165; 4 099
+// of 2048, fp32, gate per token: 41 us, some 8 of them two launches' start and end.  With hn = h rstd2, yn = y rstd1, a = grad_x pre, q = scale gate post:
 //   gh = grad_h + rstd2 (a - hn m1),        m1 = mean(a hn)
 //   grad_residual = gh,  grad_gate = scale gh yn post,  grad_post = scale gate gh yn,
 //   grad_pre = grad_x hn,  grad_y = rstd1 (q gh - yn m2),  m2 = mean(q gh yn)

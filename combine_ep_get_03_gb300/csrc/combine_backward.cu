@@ -6,7 +6,9 @@
 // once; the token's row of grad_out serves its k entries from L1 and L2.  A warp
 // takes an entry, so the entries of a token are neighbours in a block, and the dot
 // product ends in one exchange inside the warp: its order, and with it the result,
-// is always the same.
+// is always the same.  8 192 tokens of 8 rows, 7168 channels: bf16 rows 311 us (6.4
+// TB/s), e4m3 240 (6.3); with each group's maximum and divisions in all of its lanes
+// 301.  Bulk prefetches of the next entry's row to L2 made it 373.
 #include "device_common.cuh"
 #include "em_combine.cuh"
 #include "ep_internal.h"
