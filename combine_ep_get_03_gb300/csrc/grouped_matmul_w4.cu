@@ -11,15 +11,15 @@
 // cores take beside 8-bit operands, and the exponents are applied inside the
 // MMA (their blocks of 512 bytes go from shared memory to TMEM): no instruction
 // unpacks or scales a weight.  Every 128 channels have a fresh accumulator, since
-// x's scales are arbitrary; the adding warps read it, a lane a weight row, and
-// add it to fp32 registers times its column's scale.
+// x's scales are arbitrary; the adding warps read it and add it to fp32 registers
+// times its column's scale.
 //
 // Tile 256 weight rows (two halves of 128, in SwiGLU the gate's and the up
 // projection's of the same channels) x up to 112 tokens; two accumulators of
-// both halves take 448 TMEM columns, the scales the next ones.  With few tokens a
+// both halves take 448 TMEM columns, the scales 20 more.  With few tokens a
 // tile an accumulator holds two or four blocks of k, as many as are handed over
-// together, and the ring has more stages.  A block of k is always added alone and in order, so
-// a row's bits do not depend on the other rows, the tile or the SMs.
+// together, and the ring has more stages.  A block of k is always added alone and in
+// order, so a row's bits do not depend on the other rows, the tile or the SMs.
 //
 // Few rows: the stream of weights.  128 tokens by 8 of 32 experts, 2 048 -> 7 168: 50 us
 // (8-bit 77), 5.4 TB/s; one token's eight experts of 7 168 -> 4 096: 26 us (43), of which 5
@@ -59,8 +59,11 @@ constexpr int kThreads = (kEpilogueWarps + 4) * 32;  // a load, two MMA and a sc
 constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 232, kOtherRegisters = 40;
 static_assert(kEpilogueWarps * 32 * kEpilogueRegisters + 4 * 32 * kOtherRegisters <= kThreads * kLaunchRegisters, "");
 constexpr uint32_t kTmemColumns = 512;
-constexpr uint32_t kWeightScales = 4 * kTileT, kTokenScales = kWeightScales + 16;
-static_assert(kTokenScales + 4 <= kTmemColumns, "");
+// TMEM: two accumulators, behind them eight columns of exponents for each of their
+// blocks of k (an MMA's are its accumulator's, so nothing overwrites those of one
+// that runs), the tokens' scales at the end.
+constexpr uint32_t kTokenScales = kTmemColumns - 4;
+static_assert(2 * (2 * kTileT + 8) <= kTokenScales && 2 * 2 * (2 * 48 + 8) <= kTokenScales && 2 * 4 * (2 * 16 + 8) <= kTokenScales, "");
 // Blocks of k whose token scales are kept, and words for them.  A slot is filled
 // again when the MMAs of `kept - stages` blocks later are done; the warps that
 // add may then be reading those of three hand-overs before.
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t odd = warp - kEpilogueWarps - 1;  // the warp issues the even or the odd blocks of k
       const uint64_t first = smem_desc(smem_u32(stages), 16, 1024);
       const uint64_t first_scales = scale_desc(smem_u32(stages) + 2 * kHalfBytes);
-      const uint32_t a_scales = tmem + kWeightScales + odd * 8, b_scales = tmem + kTokenScales;
+      const uint32_t b_scales = tmem + kTokenScales;
       uint32_t it = 0, st = 0, phase = 0, group = 0;  // of all tiles: blocks of k, their stage, hand-overs
       bool ok = true;
       for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t a = first + at * (stage_bytes >> 4), b = a + (kTokens >> 4);
             const uint64_t f = first_scales + at * (stage_bytes >> 4);
             const uint32_t d = tmem + ac * acc_columns + slot * 2 * widest;
+            const uint32_t a_scales = tmem + 2 * acc_columns + (ac * per + slot) * 8;
 #pragma unroll
             for (int h = 0; h < 2; ++h) tmem_copy_scales(a_scales + 4 * h, f + h * (kScaleBytes >> 4));
 #pragma unroll
