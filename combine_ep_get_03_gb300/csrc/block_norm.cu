@@ -93,32 +93,16 @@ __device__ __forceinline__ void team_barrier(int team, int threads) {
   asm volatile("bar.sync %0, %1;" : : "r"(team + 1), "r"(threads) : "memory");
 }
 
-// Sum over a team of `warps` warps; `part` holds a word for each.
-__device__ __forceinline__ float team_sum(float v, float* part, int team, int warps) {
-  v = warp_sum(v);
-  if (warps == 1) return v;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % warps;
-  if (lane == 0) part[warp] = v;
-  team_barrier(team, warps * 32);
-  float s = 0.0f;
-  for (int w = 0; w < warps; ++w) s += part[w];
-  return s;
-}
-
-}  // namespace
-
-namespace {
-
-constexpr int kBackThreads = 512, kBackWarps = kBackThreads / 32;
+constexpr int kRingThreads = 512, kRingWarps = kRingThreads / 32;
 constexpr int kWordsEach = 2;                               // 8-channel words of a row that a thread owns
-constexpr int kBackHidden = kBackThreads * kWordsEach * 8;  // beyond: k_block_norm_backward_long
+constexpr int kRingHidden = kRingThreads * kWordsEach * 8;  // rows beyond take the kernels for long rows
 constexpr int kMaxStages = 4;
-constexpr int kNarrowWarps = 14;
+constexpr int kNarrowWarps = 14;  // the backward pass has 144 registers a thread for as many
 
 // Barriers and partial sums of a block's teams.
 struct RingShared {
-  uint64_t full[kBackWarps][kMaxStages];
-  float4 part[kBackWarps][2][kBackWarps];  // [team][parity][warp of the team], zeros past the team
+  uint64_t full[kRingWarps][kMaxStages];
+  float4 part[kRingWarps][2][kRingWarps];  // [team][parity][warp of the team], zeros past the team
   int quit;
 };
 
@@ -130,7 +114,7 @@ struct RingShared {
 // the stage of the row before has been read, so its refill needs no other.
 // kY: there is a block behind; kToken: its gate comes per token.
 template <bool kRes32, bool kY, bool kToken>
-__global__ void __launch_bounds__(kBackThreads, 1) k_block_norm(const BlockNormArgs a, int warps, int num_stages) {
+__global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormArgs a, int warps, int num_stages) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ RingShared s;
   const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
@@ -296,20 +280,29 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm(const BlockNormA
 // The forward pass of rows too long for that: a block a row, the row in its threads'
 // registers.  kWords: 16-byte words of bf16 that a thread holds of each row.
 template <int kWords, bool kRes32>
-__global__ void __launch_bounds__(512) k_block_norm_long(const BlockNormArgs a, int warps) {
-  __shared__ float part[2][32];
+__global__ void __launch_bounds__(kRingThreads) k_block_norm_long(const BlockNormArgs a) {
+  __shared__ float part[2][kRingWarps];
   after_previous();
-  const int per_team = warps * 32, teams = blockDim.x / per_team;
-  const int team = threadIdx.x / per_team, tid = threadIdx.x % per_team;
-  float* sums[2] = {part[0] + team * warps, part[1] + team * warps};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = a.H >> 3;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  for (long long t = static_cast<long long>(blockIdx.x) * teams + team; t < a.T;
-       t += static_cast<long long>(gridDim.x) * teams) {
+  int turn = 0;
+  auto sum = [&](float v) {  // in the other of the two sets of parts at each call
+    float* parts = part[turn];
+    turn ^= 1;
+    v = warp_sum(v);
+    if (lane == 0) parts[warp] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRingWarps; ++w) v += parts[w];
+    return v;
+  };
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const long long row = t * words;
     if (a.mask && !a.mask[t]) {
       const float zero[8] = {};
-      for (int c = tid; c < words; c += per_team) {
+      for (int c = tid; c < words; c += kRingThreads) {
         if (a.y) store8(a.new_residual, kRes32, row + c, zero);
         if (a.x) store8(a.x, false, row + c, zero);
       }
@@ -319,9 +312,9 @@ __global__ void __launch_bounds__(512) k_block_norm_long(const BlockNormArgs a, 
       }
       continue;
     }
-    if (tid == 0 && t + gridDim.x * teams < a.T) {
-      // the team's next rows on their way to L2
-      const long long next = (t + gridDim.x * teams) * a.H;
+    if (tid == 0 && t + gridDim.x < a.T) {
+      // the block's next rows on their way to L2
+      const long long next = (t + gridDim.x) * a.H;
       constexpr int kR = kRes32 ? 4 : 2;
       prefetch_l2_bulk(static_cast<const char*>(a.residual) + next * kR, a.H * kR);
       if (a.y) prefetch_l2_bulk(static_cast<const uint16_t*>(a.y) + next, a.H * 2);
@@ -332,13 +325,13 @@ __global__ void __launch_bounds__(512) k_block_norm_long(const BlockNormArgs a, 
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int c = tid + i * per_team;
+      const int c = tid + i * kRingThreads;
       y[i] = make_uint4(0, 0, 0, 0);
       if (c < words && a.y) y[i] = ld_stream(static_cast<const uint16_t*>(a.y) + 8 * (row + c));
     }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int c = tid + i * per_team;
+      const int c = tid + i * kRingThreads;
       if (c < words) {
         load8(a.residual, kRes32, row + c, h[i]);
       } else {
@@ -356,57 +349,54 @@ __global__ void __launch_bounds__(512) k_block_norm_long(const BlockNormArgs a, 
 #pragma unroll
           for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
         }
-        r1 = rsqrtf(fmaf(team_sum(s, sums[0], team, warps), inv_h, a.eps));
+        r1 = rsqrtf(fmaf(sum(s), inv_h, a.eps));
         if (tid == 0 && a.rstd) a.rstd[t] = r1;
       }
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const int c = tid + i * per_team;
-        if (c < words) {
-          float v[8], w[8];
-          unpack8(y[i], v);
-          if (a.post) {
-            load8(a.post, a.weight32, c, w);
+        const int c = tid + i * kRingThreads;
+        if (c >= words) continue;
+        float v[8], w[8];
+        unpack8(y[i], v);
+        if (a.post) {
+          load8(a.post, a.weight32, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= r1 * w[j];
-          }
-          if (a.gate) {
-            load8(a.gate, a.weight32 && !a.gate_per_token, a.gate_per_token ? row + c : c, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= w[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = fmaf(a.scale, v[j], h[i][j]);
-          store8(a.new_residual, kRes32, row + c, h[i]);
+          for (int j = 0; j < 8; ++j) v[j] *= r1 * w[j];
         }
+        if (a.gate) {
+          load8(a.gate, a.weight32 && !a.gate_per_token, a.gate_per_token ? row + c : c, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = fmaf(a.scale, v[j], h[i][j]);
+        store8(a.new_residual, kRes32, row + c, h[i]);
       }
     }
-    if (a.x) {
-      s = 0.0f;
+    if (!a.x) continue;
+    s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i)
+    for (int i = 0; i < kWords; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
-      const float r2 = rsqrtf(fmaf(team_sum(s, sums[1], team, warps), inv_h, a.eps));
-      if (tid == 0 && a.rstd) a.rstd[a.T + t] = r2;
+      for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+    const float r2 = rsqrtf(fmaf(sum(s), inv_h, a.eps));
+    if (tid == 0 && a.rstd) a.rstd[a.T + t] = r2;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int c = tid + i * per_team;
-        if (c < words) {
-          float w[8];
-          load8(a.pre, a.weight32, c, w);
+    for (int i = 0; i < kWords; ++i) {
+      const int c = tid + i * kRingThreads;
+      if (c >= words) continue;
+      float w[8];
+      load8(a.pre, a.weight32, c, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] *= h[i][j] * r2;
-          store8(a.x, false, row + c, w);
-        }
-      }
+      for (int j = 0; j < 8; ++j) w[j] *= h[i][j] * r2;
+      store8(a.x, false, row + c, w);
     }
   }
 }
 
-// Backward: the same teams and rings, of two stages or more, read twice: for the sums, and for
-// the results.  The barrier of a row's sums says that the stage of the row before
-// has been read, so its refill needs no other; with an fp32 residual, where a long
+// Backward: the same teams and rings, of two stages or more, each row read twice: for
+// the sums, and for the results.  The barrier of a row's sums says that the stage of
+// the row before has been read, so its refill needs no other; with an fp32 residual, where a long
 // row leaves room for two stages only, a second barrier lets the refill start half a
 // row earlier (8192 x 7168: 228 -> 166 us; with a bf16 residual, three stages, 116 ->
 // 146).  Each tensor's copy is asked for by a warp of its own.
@@ -657,24 +647,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The same for rows too long for a thread's registers: read from memory twice,
 // sums in shared memory, [2][H], a thread's channels its own.
 template <bool kRes32>
-__global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward_long(const BlockNormBackwardArgs a) {
+__global__ void __launch_bounds__(kRingThreads, 1) k_block_norm_backward_long(const BlockNormBackwardArgs a) {
   extern __shared__ float4 own4[];
   float* own = reinterpret_cast<float*>(own4);
-  __shared__ float part[2][3][kBackWarps];
+  __shared__ float part[2][3][kRingWarps];
   after_previous();
   const BlockNormArgs& n = a.n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = n.H >> 3;
   const float inv_h = 1.0f / static_cast<float>(n.H);
   const bool pre = a.grad_x != nullptr, post = a.need_y && n.post;
-  for (int i = tid; i < 2 * n.H; i += kBackThreads) own[i] = 0.0f;
+  for (int i = tid; i < 2 * n.H; i += kRingThreads) own[i] = 0.0f;
   __syncthreads();
   int turn = 0;
   for (long long t = blockIdx.x; t < n.T; t += gridDim.x) {
     const long long row = t * words;
     if (n.mask && !n.mask[t]) {
       const float zero[8] = {};
-      for (int c = tid; c < words; c += kBackThreads) {
+      for (int c = tid; c < words; c += kRingThreads) {
         if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, zero);
         if (a.grad_y) store8(a.grad_y, false, row + c, zero);
         if (a.grad_gate && n.gate_per_token) store8(a.grad_gate, false, row + c, zero);
@@ -713,7 +703,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward_long(co
     };
     if (pre || post) {
       float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-      for (int c = tid; c < words; c += kBackThreads) {
+      for (int c = tid; c < words; c += kRingThreads) {
         float g[8], hn[8], x[8], w[8], y[8], q[8], u[8];
         fetch(c, g, hn, x, w, y, q, u);
 #pragma unroll
@@ -729,12 +719,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward_long(co
       __syncthreads();
       s1 = s2 = s3 = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kBackWarps; ++w) s1 += part[turn][0][w], s2 += part[turn][1][w], s3 += part[turn][2][w];
+      for (int w = 0; w < kRingWarps; ++w) s1 += part[turn][0][w], s2 += part[turn][1][w], s3 += part[turn][2][w];
       turn ^= 1;
       m1 = s1 * inv_h * r2;
       if (post) m2 = inv_h * fmaf(-m1, s3, s2);
     }
-    for (int c = tid; c < words; c += kBackThreads) {
+    for (int c = tid; c < words; c += kRingThreads) {
       float g[8], hn[8], x[8], w[8], y[8], q[8], u[8], dg[8];
       fetch(c, g, hn, x, w, y, q, u);
       float *op = own + 8 * c, *oy = op + n.H;
@@ -755,7 +745,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_block_norm_backward_long(co
       if (a.grad_y) store8(a.grad_y, false, row + c, g);
     }
   }
-  for (int c = tid; c < words; c += kBackThreads)
+  for (int c = tid; c < words; c += kRingThreads)
     for (int k = 0; k < 2; ++k)
       if (k == 0 ? a.grad_pre != nullptr : a.sum_y)
         for (int j = 0; j < 8; ++j)
@@ -823,7 +813,7 @@ int row_warps(int H) { return (H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach);
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaStream_t stream) {
   cudaError_t e;
-  if (a.H <= kBackHidden) {
+  if (a.H <= kRingHidden) {
     const bool y = a.y != nullptr, token = y && a.gate_per_token;
     using Kernel = void (*)(BlockNormArgs, int, int);
     static const Kernel kernels[2][3] = {
@@ -837,7 +827,7 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
       return e;
     const int bytes = a.H * ((res32 ? 4 : 2) + (y ? 2 : 0) + (token ? 2 : 0));
     const int warps = row_warps(a.H), per_sm = (a.T + sms - 1) / sms;
-    int teams = kBackWarps / warps;
+    int teams = kRingWarps / warps;
     if (teams > per_sm) teams = per_sm;
     if (teams > room / (2 * bytes)) teams = room / (2 * bytes);
     int stages = room / (bytes * teams);
@@ -846,12 +836,12 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
     return launch_early(kernel, 1, dim3(sms < most ? sms : most), dim3(teams * warps * 32), bytes * teams * stages, stream,
                         a, warps, stages);
   }
-  int warps = 16;
-  const int words = a.H / 8, per_thread = (words + warps * 32 - 1) / (warps * 32);
-  using Kernel = void (*)(BlockNormArgs, int);
+  using Kernel = void (*)(BlockNormArgs);
   static const Kernel kernels[2][2] = {{k_block_norm_long<3, false>, k_block_norm_long<4, false>},
                                        {k_block_norm_long<3, true>, k_block_norm_long<4, true>}};
-  return launch_early(kernels[res32][per_thread - 3], 1, dim3(sms < a.T ? sms : a.T), dim3(warps * 32), 0, stream, a, warps);
+  static_assert(kRingHidden >= 2 * 8 * kRingThreads && kBlockNormMaxHidden <= 4 * 8 * kRingThreads, "");
+  return launch_early(kernels[res32][a.H > 3 * 8 * kRingThreads], 1, dim3(sms < a.T ? sms : a.T), dim3(kRingThreads), 0,
+                      stream, a);
 }
 
 namespace {
@@ -884,17 +874,17 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
   const int all = a.n.H * (2 * r + 4 + (token ? 2 : 0)), bytes = a.n.H * ((a.grad_new ? r : 0) + (a.grad_x ? r + 2 : 0) + (a.need_y ? 2 : 0) + (gate ? 2 : 0));
   int room = 0;
   if ((e = ring_room(&room)) != cudaSuccess) return e;
-  if (a.n.H <= kBackHidden && 2 * all <= room) {
+  if (a.n.H <= kRingHidden && 2 * all <= room) {
     const int warps = row_warps(a.n.H), per_sm = (a.n.T + sms - 1) / sms;
     const bool wide = warps > kNarrowWarps;
-    int teams = (wide ? kBackWarps : kNarrowWarps) / warps;
+    int teams = (wide ? kRingWarps : kNarrowWarps) / warps;
     if (teams > per_sm) teams = per_sm;
     if (teams > room / (2 * all)) teams = room / (2 * all);
     int stages = bytes ? room / (bytes * teams) : 2;
     if (stages > kMaxStages) stages = kMaxStages;
     const int sums = teams > 1 ? 8 * a.n.H * teams : 0;
     const int need = bytes * teams * stages > sums ? bytes * teams * stages : sums;
-    auto pick = wide ? (res32 ? backward_kernel<32 * kBackWarps, true> : backward_kernel<32 * kBackWarps, false>)
+    auto pick = wide ? (res32 ? backward_kernel<32 * kRingWarps, true> : backward_kernel<32 * kRingWarps, false>)
                      : (res32 ? backward_kernel<32 * kNarrowWarps, true> : backward_kernel<32 * kNarrowWarps, false>);
     auto kernel = pick(a.grad_x != nullptr, a.need_y, gate);
     static std::atomic<unsigned long long> ready[32];  // devices set up, a bit each
@@ -908,7 +898,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
     static std::atomic<unsigned long long> ready[2];
     if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[res32], 0)) != cudaSuccess) return e;
     if (blocks > a.n.T) blocks = a.n.T;
-    e = launch_early(kernel, 1, dim3(blocks), dim3(kBackThreads), sizeof(float) * 2 * a.n.H, stream, a);
+    e = launch_early(kernel, 1, dim3(blocks), dim3(kRingThreads), sizeof(float) * 2 * a.n.H, stream, a);
   }
   if (e != cudaSuccess || !(a.grad_pre || a.sum_y)) return e;
   return launch_early(k_block_norm_sums, 1, dim3((a.n.H + 4 * kRunWords - 1) / (4 * kRunWords), 2), dim3(256), 0, stream, a, blocks);

@@ -636,7 +636,8 @@ typedef struct {
  *      rstd          dev fp32 [2][T] or NULL: 1 / sqrt(mean + eps) of y (with
  *                    post_weight) and of the new residual (with pre_weight), for the
  *                    backward pass; the other entries are left as they are.
- * 16-byte aligned; one launch. */
+ * 16-byte aligned; one launch.  A row whose copy into shared memory never lands (a
+ * bounded wait that gives up) becomes NaN, here and in the backward pass. */
 ep_status_t ep_block_norm_forward(const ep_block_norm_t* norm, const void* residual, const void* y, void* new_residual,
                                   void* x, float* rstd, int num_sms, ep_stream_t stream);
 

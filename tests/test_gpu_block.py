@@ -258,6 +258,7 @@ CASES = [dict(T=1, H=8, post=True, pre=True, gate="none"), dict(T=3, H=16, post=
          dict(T=40, H=2560, post=True, pre=True, gate="none", masked=True), dict(T=20, H=4104, post=False, pre=True, gate="none"),
          dict(T=305, H=7168, post=True, pre=True, gate="vector"), dict(T=9, H=8192, post=True, pre=True, gate="token"),
          dict(T=10, H=8200, post=True, pre=True, gate="token", masked=True), dict(T=6, H=16384, post=True, pre=True, gate="vector"),
+         dict(T=700, H=8200, post=True, pre=False, gate="none"), dict(T=700, H=12296, post=False, pre=True, gate="vector", masked=True),
          dict(T=7, H=12288, post=False, pre=False, gate="token"), dict(T=2, H=520, post=False, pre=False, gate="vector")]
 TYPES = [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)]
 
