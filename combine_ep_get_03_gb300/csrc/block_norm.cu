@@ -644,12 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The same for rows too long for a thread's registers: read from memory twice,
-// sums in shared memory, [2][H], a thread's channels its own.
+// The same for rows too long for a thread's registers: read from memory twice (the
+// next ones fetched to L2 meanwhile), sums in shared memory, a thread's channels its
+// own, [pre, y][first, second four of a word][words].
 template <bool kRes32>
 __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm_backward_long(const BlockNormBackwardArgs a) {
-  extern __shared__ float4 own4[];
-  float* own = reinterpret_cast<float*>(own4);
+  extern __shared__ float4 own[];
   __shared__ float part[2][3][kRingWarps];
   after_previous();
   const BlockNormArgs& n = a.n;
@@ -657,8 +657,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm_backward_long(co
   const int words = n.H >> 3;
   const float inv_h = 1.0f / static_cast<float>(n.H);
   const bool pre = a.grad_x != nullptr, post = a.need_y && n.post;
-  for (int i = tid; i < 2 * n.H; i += kRingThreads) own[i] = 0.0f;
+  for (int i = tid; i < 4 * words; i += kRingThreads) own[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   __syncthreads();
+  auto take = [&](const float4* o, float* v) {
+    const float4 a = o[0], b = o[words];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  };
+  auto put = [&](float4* o, const float* v) {
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[words] = make_float4(v[4], v[5], v[6], v[7]);
+  };
   int turn = 0;
   for (long long t = blockIdx.x; t < n.T; t += gridDim.x) {
     const long long row = t * words;
@@ -670,6 +678,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm_backward_long(co
         if (a.grad_gate && n.gate_per_token) store8(a.grad_gate, false, row + c, zero);
       }
       continue;
+    }
+    if (tid == 0 && t + gridDim.x < n.T) {
+      // the block's next rows on their way to L2
+      const long long next = (t + gridDim.x) * n.H;
+      constexpr int kR = kRes32 ? 4 : 2;
+      if (a.grad_new) prefetch_l2_bulk(static_cast<const char*>(a.grad_new) + next * kR, n.H * kR);
+      if (pre) prefetch_l2_bulk(static_cast<const char*>(n.new_residual) + next * kR, n.H * kR);
+      if (pre) prefetch_l2_bulk(static_cast<const uint16_t*>(a.grad_x) + next, n.H * 2);
+      if (a.need_y) prefetch_l2_bulk(static_cast<const uint16_t*>(n.y) + next, n.H * 2);
+      if (n.gate_per_token) prefetch_l2_bulk(static_cast<const uint16_t*>(n.gate) + next, n.H * 2);
     }
     const float r1 = post ? n.rstd[t] : 1.0f, r2 = pre ? n.rstd[n.T + t] : 0.0f;
     float m1 = 0.0f, m2 = 0.0f;
@@ -727,29 +745,36 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm_backward_long(co
     for (int c = tid; c < words; c += kRingThreads) {
       float g[8], hn[8], x[8], w[8], y[8], q[8], u[8], dg[8];
       fetch(c, g, hn, x, w, y, q, u);
-      float *op = own + 8 * c, *oy = op + n.H;
+      float sum[8];
+      if (a.grad_pre) {
+        take(own + c, sum);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (a.grad_pre) op[j] = fmaf(x[j], hn[j], op[j]);
-        g[j] = fmaf(-hn[j], m1, g[j]);
+        for (int j = 0; j < 8; ++j) sum[j] = fmaf(x[j], hn[j], sum[j]);
+        put(own + c, sum);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = fmaf(-hn[j], m1, g[j]);
+      if (a.sum_y) take(own + 2 * words + c, sum);
       if (a.grad_residual) store8(a.grad_residual, kRes32, row + c, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = g[j] * y[j];
         dg[j] = q[j] * v;
-        if (a.sum_y) oy[j] = fmaf(u[j], v, oy[j]);
+        if (a.sum_y) sum[j] = fmaf(u[j], v, sum[j]);
         g[j] = r1 * fmaf(-y[j], m2, q[j] * u[j] * g[j]);
       }
+      if (a.sum_y) put(own + 2 * words + c, sum);
       if (a.grad_gate && n.gate_per_token) store8(a.grad_gate, false, row + c, dg);
       if (a.grad_y) store8(a.grad_y, false, row + c, g);
     }
   }
   for (int c = tid; c < words; c += kRingThreads)
     for (int k = 0; k < 2; ++k)
-      if (k == 0 ? a.grad_pre != nullptr : a.sum_y)
-        for (int j = 0; j < 8; ++j)
-          a.partial[(static_cast<long long>(blockIdx.x) * 2 + k) * n.H + 8 * c + j] = own[k * n.H + 8 * c + j];
+      if (k == 0 ? a.grad_pre != nullptr : a.sum_y) {
+        float v[8];
+        take(own + 2 * k * words + c, v);
+        store8(a.partial + (static_cast<long long>(blockIdx.x) * 2 + k) * n.H, true, c, v);
+      }
 }
 
 // Sums of the blocks' partial [block][2][H], 32 runs of blocks side by side:
