@@ -5,7 +5,8 @@
 // is rounded.
 //
 // Both are HBM-bound: each tensor's row is read once and each result's written once.
-// A team of warps takes a row, two 8-channel words a thread; short rows leave room
+// A team of warps takes a row, two 8-channel words a thread (one in most of the
+// backward's rows up to 4096); short rows leave room
 // for several teams in a block, one block an SM.  A sum over a row ends in an exchange through
 // shared memory, in a fixed order.
 //
@@ -16,7 +17,8 @@
 // with the next row's first, one barrier a row: 245, 150, 145 and 3.9.)
 //
 // Backward.  8 192 tokens of 7168, gate a vector: bf16 115 us (6.1 TB/s), fp32 165; 4 099
-// of 2048, fp32, gate per token: 41 us, some 8 of them two launches' start and end.  With hn = h rstd2, yn = y rstd1, a = grad_x pre, q = scale gate post:
+// of 2048, fp32, gate per token: 39 us, some 8 of them two launches' start and end.
+// With hn = h rstd2, yn = y rstd1, a = grad_x pre, q = scale gate post:
 //   gh = grad_h + rstd2 (a - hn m1),        m1 = mean(a hn)
 //   grad_residual = gh,  grad_gate = scale gh yn post,  grad_post = scale gate gh yn,
 //   grad_pre = grad_x hn,  grad_y = rstd1 (q gh - yn m2),  m2 = mean(q gh yn)
@@ -402,8 +404,9 @@ __global__ void __launch_bounds__(kRingThreads) k_block_norm_long(const BlockNor
 // 146).  Each tensor's copy is asked for by a warp of its own.
 // kPre: x's gradient takes part; kY: y is needed (a norm behind the block or its
 // gate's gradient); kToken: the gate comes per token.
-// kThreads: the most that the block has; 448 leave a thread 144 registers.
-template <int kThreads, bool kRes32, bool kPre, bool kY, bool kToken>
+// kThreads: the most that the block has; 448 leave a thread 144 registers, 512 128.
+// kWords: the 8-channel words of a row that a thread owns.
+template <int kThreads, int kWords, bool kRes32, bool kPre, bool kY, bool kToken>
 __global__ void __launch_bounds__(kThreads, 1)
     k_block_norm_backward(const BlockNormBackwardArgs a, int warps, int num_stages) {
   extern __shared__ __align__(128) unsigned char ring[];
@@ -455,10 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the channels' constants: pre, and q = scale post (times gate where it is a vector)
   const bool post = kY && n.post;
   const float inv_h = 1.0f / static_cast<float>(n.H);
-  float2 wp[kPre ? kWordsEach : 1][4], q[kWordsEach][4];
-  float2 sum_pre[kPre ? kWordsEach : 1][4], sum_y[kY ? kWordsEach : 1][4];
+  float2 wp[kPre ? kWords : 1][4], q[kWords][4];
+  float2 sum_pre[kPre ? kWords : 1][4], sum_y[kY ? kWords : 1][4];
 #pragma unroll
-  for (int k = 0; k < kWordsEach; ++k) {
+  for (int k = 0; k < kWords; ++k) {
     const int c = tid + k * threads;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -500,10 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
     const bool landed = !copies || wait_or_quit(&full[st], phase, &s.quit, nullptr);
-    float2 g[kWordsEach][4];
+    float2 g[kWords][4];
     float2 t1 = both(0.0f), t2 = t1, t3 = t1;
 #pragma unroll
-    for (int k = 0; k < kWordsEach; ++k) {
+    for (int k = 0; k < kWords; ++k) {
       const int c = tid + k * threads;
 #pragma unroll
       for (int j = 0; j < 4; ++j) g[k][j] = both(0.0f);
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!landed) {  // a copy that never came: NaN, not old values
 #pragma unroll
-      for (int k = 0; k < kWordsEach; ++k)
+      for (int k = 0; k < kWords; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[k][j] = both(__int_as_float(0x7fc00000));
     }
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float m2 = post ? inv_h * r1 * fmaf(-m1 * r2, s3, s2) : 0.0f;
     const long long row = t * words;
 #pragma unroll
-    for (int k = 0; k < kWordsEach; ++k) {
+    for (int k = 0; k < kWords; ++k) {
       const int c = tid + k * threads;
       if (c >= words) continue;
       if (!live) {
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int k = 0; k < kWordsEach; ++k) {
+  for (int k = 0; k < kWords; ++k) {
     const int c = tid + k * threads;
     if (c >= words) continue;
     float* to = teams == 1 ? a.partial + static_cast<long long>(blockIdx.x) * 2 * n.H : sums + team * 2 * n.H;
@@ -832,7 +835,7 @@ cudaError_t ring_room(int* room) {
 }
 
 // Warps that hold a row.
-int row_warps(int H) { return (H / 8 + 32 * kWordsEach - 1) / (32 * kWordsEach); }
+int row_warps(int H, int words_each) { return (H / 8 + 32 * words_each - 1) / (32 * words_each); }
 
 }  // namespace
 
@@ -851,7 +854,7 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
         (e = ring_room(&room)) != cudaSuccess)
       return e;
     const int bytes = a.H * ((res32 ? 4 : 2) + (y ? 2 : 0) + (token ? 2 : 0));
-    const int warps = row_warps(a.H), per_sm = (a.T + sms - 1) / sms;
+    const int warps = row_warps(a.H, kWordsEach), per_sm = (a.T + sms - 1) / sms;
     int teams = kRingWarps / warps;
     if (teams > per_sm) teams = per_sm;
     if (teams > room / (2 * bytes)) teams = room / (2 * bytes);
@@ -872,13 +875,13 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
 namespace {
 
 using Backward = void (*)(BlockNormBackwardArgs, int, int);
-template <int kThreads, bool kRes32>
+template <int kWarps, int kWords, bool kRes32>
 Backward backward_kernel(bool pre, bool y, bool token) {
   static const Backward kernels[8] = {
-      k_block_norm_backward<kThreads, kRes32, false, false, false>, k_block_norm_backward<kThreads, kRes32, false, false, true>,
-      k_block_norm_backward<kThreads, kRes32, false, true, false>,  k_block_norm_backward<kThreads, kRes32, false, true, true>,
-      k_block_norm_backward<kThreads, kRes32, true, false, false>,  k_block_norm_backward<kThreads, kRes32, true, false, true>,
-      k_block_norm_backward<kThreads, kRes32, true, true, false>,   k_block_norm_backward<kThreads, kRes32, true, true, true>};
+      k_block_norm_backward<32 * kWarps, kWords, kRes32, false, false, false>, k_block_norm_backward<32 * kWarps, kWords, kRes32, false, false, true>,
+      k_block_norm_backward<32 * kWarps, kWords, kRes32, false, true, false>,  k_block_norm_backward<32 * kWarps, kWords, kRes32, false, true, true>,
+      k_block_norm_backward<32 * kWarps, kWords, kRes32, true, false, false>,  k_block_norm_backward<32 * kWarps, kWords, kRes32, true, false, true>,
+      k_block_norm_backward<32 * kWarps, kWords, kRes32, true, true, false>,   k_block_norm_backward<32 * kWarps, kWords, kRes32, true, true, true>};
   return kernels[pre * 4 + y * 2 + token];
 }
 
@@ -900,8 +903,13 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
   int room = 0;
   if ((e = ring_room(&room)) != cudaSuccess) return e;
   if (a.n.H <= kRingHidden && 2 * all <= room) {
-    const int warps = row_warps(a.n.H), per_sm = (a.n.T + sms - 1) / sms;
-    const bool wide = warps > kNarrowWarps;
+    // One word a thread (16 warps of 128 registers) where that fills 15 warps or more, and
+    // for fp32 residuals wherever it holds the row: 8192 x 4096 bf16 77 us instead of 84, fp32
+    // 99 instead of 122; 2048 fp32 55 instead of 62; 2560 (10 warps) bf16 62 instead of 57.
+    const int single = row_warps(a.n.H, 1);
+    const bool one = single <= kRingWarps && (res32 || kRingWarps / single * single >= kRingWarps - 1);
+    const int warps = one ? single : row_warps(a.n.H, kWordsEach), per_sm = (a.n.T + sms - 1) / sms;
+    const bool wide = one || warps > kNarrowWarps;
     int teams = (wide ? kRingWarps : kNarrowWarps) / warps;
     if (teams > per_sm) teams = per_sm;
     if (teams > room / (2 * all)) teams = room / (2 * all);
@@ -909,11 +917,12 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
     if (stages > kMaxStages) stages = kMaxStages;
     const int sums = teams > 1 ? 8 * a.n.H * teams : 0;
     const int need = bytes * teams * stages > sums ? bytes * teams * stages : sums;
-    auto pick = wide ? (res32 ? backward_kernel<32 * kRingWarps, true> : backward_kernel<32 * kRingWarps, false>)
-                     : (res32 ? backward_kernel<32 * kNarrowWarps, true> : backward_kernel<32 * kNarrowWarps, false>);
+    auto pick = one    ? (res32 ? backward_kernel<kRingWarps, 1, true> : backward_kernel<kRingWarps, 1, false>)
+                : wide ? (res32 ? backward_kernel<kRingWarps, kWordsEach, true> : backward_kernel<kRingWarps, kWordsEach, false>)
+                       : (res32 ? backward_kernel<kNarrowWarps, kWordsEach, true> : backward_kernel<kNarrowWarps, kWordsEach, false>);
     auto kernel = pick(a.grad_x != nullptr, a.need_y, gate);
-    static std::atomic<unsigned long long> ready[32];  // devices set up, a bit each
-    const int which = wide * 16 + res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
+    static std::atomic<unsigned long long> ready[48];  // devices set up, a bit each
+    const int which = (one + wide) * 16 + res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
     if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess) return e;
     const int most = (a.n.T + teams - 1) / teams;
     if (blocks > most) blocks = most;

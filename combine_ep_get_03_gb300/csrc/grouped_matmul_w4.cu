@@ -24,9 +24,10 @@
 // Few rows: the stream of weights.  128 tokens by 8 of 32 experts, 2 048 -> 7 168: 50 us
 // (8-bit 77), 5.4 TB/s; one token's eight experts of 7 168 -> 4 096: 26 us (43), of which 5
 // are start and end; with experts enough to fill the SMs four times 90 % of the copy
-// rate.  TMA's spreading costs some 10 % of the rate that plain bytes come at (loads
-// alone 48 us instead of 43).  Many rows: the warps that add, about 1 100 cycles a
-// stage where the MMAs take 470; 16 384 rows, 7 168 -> 2 x 2 048: 590-610 us, 1.6 PFLOP/s.
+// rate.  The loads alone take 45 of the 50 us (39 at the copy rate): TMA's spreading costs
+// some.  Many rows: the warps that add, about 1 100 cycles a stage where the MMAs take
+// 470; 16 384 rows, 7 168 -> 2 x 2 048: 590-610 us, 1.6 PFLOP/s (loads alone 289, without the
+// MMAs 506, without the sums 375).
 #include <cuda.h>
 
 #include <atomic>

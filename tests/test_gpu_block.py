@@ -259,7 +259,9 @@ CASES = [dict(T=1, H=8, post=True, pre=True, gate="none"), dict(T=3, H=16, post=
          dict(T=305, H=7168, post=True, pre=True, gate="vector"), dict(T=9, H=8192, post=True, pre=True, gate="token"),
          dict(T=10, H=8200, post=True, pre=True, gate="token", masked=True), dict(T=6, H=16384, post=True, pre=True, gate="vector"),
          dict(T=700, H=8200, post=True, pre=False, gate="none"), dict(T=700, H=12296, post=False, pre=True, gate="vector", masked=True),
-         dict(T=7, H=12288, post=False, pre=False, gate="token"), dict(T=2, H=520, post=False, pre=False, gate="vector")]
+         dict(T=7, H=12288, post=False, pre=False, gate="token"), dict(T=2, H=520, post=False, pre=False, gate="vector"),
+         dict(T=700, H=2048, post=True, pre=True, gate="token", masked=True), dict(T=310, H=4096, post=True, pre=True, gate="vector"),
+         dict(T=170, H=3848, post=True, pre=True, gate="token"), dict(T=911, H=1280, post=False, pre=True, gate="vector", masked=True)]
 TYPES = [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)]
 
 
