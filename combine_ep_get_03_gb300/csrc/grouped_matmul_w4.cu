@@ -25,9 +25,10 @@
 // (8-bit 77), 5.4 TB/s; one token's eight experts of 7 168 -> 4 096: 26 us (43), of which 5
 // are start and end; with experts enough to fill the SMs four times 90 % of the copy
 // rate.  The loads alone take 45 of the 50 us (39 at the copy rate): TMA's spreading costs
-// some.  Many rows: the warps that add, about 1 100 cycles a stage where the MMAs take
-// 470; 16 384 rows, 7 168 -> 2 x 2 048: 590-610 us, 1.6 PFLOP/s (loads alone 289, without the
-// MMAs 506, without the sums 375).
+// some.  Many rows: the accumulators' round from the MMAs to the warps that add and back,
+// some 1 150 cycles a stage; 16 384 rows, 7 168 -> 2 x 2 048: 560 us, 1.7 PFLOP/s, at 1.3 of
+// 1.4 kW.  Of a stage's cycles shared memory is busy for 850 (weights and tokens are
+// written once and read once, the tokens twice): without the sums 375 us.
 #include <cuda.h>
 
 #include <atomic>
@@ -200,6 +201,15 @@ __device__ __forceinline__ void release(const Handover& h) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(h.empty);
 }
 
+// Registers of loads that the wait for others has settled.
+__device__ __forceinline__ void settled(uint32_t* v) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
 // Whether a barrier's phase is complete, without waiting.
 __device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -231,7 +241,7 @@ __device__ __forceinline__ bool take(float (&acc)[16 * kOf], const Handover& h, 
     for (int o = 0; o < P::kOctets; ++o) scales[k][o] = f[4 * o];
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m) tmem_load_wait16(v[m]);
+  for (int m = 0; m < 4; ++m) m ? settled(v[m]) : tmem_load_wait16(v[m]);
   bool next = false;
   if (P::kMost <= 4 || items <= 4) {
     release(h);
@@ -246,7 +256,7 @@ __device__ __forceinline__ bool take(float (&acc)[16 * kOf], const Handover& h, 
     add_item<kSwiglu, kOf, 3>(acc, v, scales, items);
     if constexpr (P::kMost > 6) load_item<kSwiglu, kOf, 7>(v, h, items);
 #pragma unroll
-    for (int m = 4; m < P::kMost; ++m) tmem_load_wait16(v[m & 3]);
+    for (int m = 4; m < P::kMost; ++m) m > 4 ? settled(v[m & 3]) : tmem_load_wait16(v[m & 3]);
     release(h);
     if constexpr (kOf != kChunks) next = phase_over(smem_u32(h.next), h.next_parity);
     add_item<kSwiglu, kOf, 4>(acc, v, scales, items), add_item<kSwiglu, kOf, 5>(acc, v, scales, items);
@@ -275,7 +285,7 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
   const int F = p.N >> 1;
   uint32_t it = 0, group = 0;  // blocks of k and hand-overs of all tiles
   int turn = 0;
-  bool ok, ready = false;  // whether the next hand-over is there
+  bool ok = true, ready = false;  // whether the next hand-over is there
   for (unsigned t = blockIdx.x; t < l.tiles; t += gridDim.x, turn ^= 1) {
     const Tile c = tile_at(p.groups, prefix, l.tiles_n, t);
     // a warp's columns: all of its half's, or half of both halves' (SwiGLU: 8
@@ -288,10 +298,9 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
     for (int kb = 0; kb < l.blocks_k; ++group) {
       const uint32_t ac = group & 1;
       const int n = min(l.per, l.blocks_k - kb);
-      if (!__all_sync(kFullMask, ready)) {
-        ok = __all_sync(kFullMask, wait_or_quit(&s.acc_full[ac], (group >> 1) & 1, quit, err));
-        if (!ok) return;
-      }
+      // no vote a hand-over (prefill 579 -> 560 us): the tile's end has one
+      ok = ok && (ready || wait_or_quit(&s.acc_full[ac], (group >> 1) & 1, quit, err));
+      __syncwarp();
       tmem_fence_after();
       const Handover h{from + ac * l.acc_columns, l.widest, s.x_scale + first + pair, it, l.kept, &s.acc_empty[ac],
                        &s.acc_full[ac ^ 1], ((group + 1) >> 1) & 1};
@@ -300,6 +309,7 @@ __device__ __forceinline__ void add_tiles(const Matmul4Args& p, Shared& s, const
       kb += n;
       it += n;
     }
+    if (!__all_sync(kFullMask, ok)) return;
     if constexpr (!kSwiglu) {
       // Lanes 4 a + t hold weight rows a, a + 8, a + 16 and a + 24 of the same tokens.
       // Four of them swap theirs, so that each has four rows in a row, 8 bytes.
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t b_scales = tmem + kTokenScales;
       uint32_t it = 0, st = 0, phase = 0, group = 0;  // of all tiles: blocks of k, their stage, hand-overs
       bool ok = true;
-      for (unsigned t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (unsigned t = blockIdx.x; __all_sync(kFullMask, ok) && t < tiles; t += gridDim.x) {
         const Tile c = tile_at(p.groups, prefix, tiles_n, t);
         const uint32_t desc = mma_mx_desc(128, uniform(c.columns), 0);
         for (int kb = 0, in = 0; kb < blocks_k; ++kb, ++it) {
@@ -501,11 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++st == num_stages) st = 0, phase ^= 1;
           if (++in == per || last) in = 0, ++group;
           if ((it & 1) != odd) continue;
-          ok = __all_sync(kFullMask, (first_turn || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err)) &&
-                                         wait_or_quit(&s.full[at], round, quit, err));
-          if (!ok) break;
+          // The operands first, which are here long before the accumulator is back, and
+          // no vote in between: all of it is on the accumulators' round (prefill 605 -> 575 us).
+          ok = ok && wait_or_quit(&s.full[at], round, quit, err) &&
+               (first_turn || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err));
+          __syncwarp();
           tmem_fence_after();
-          if (elect_one()) {
+          if (elect_one() && ok) {
             // descriptors count 16-byte units; 32 channels are two
             const uint64_t a = first + at * (stage_bytes >> 4), b = a + (kTokens >> 4);
             const uint64_t f = first_scales + at * (stage_bytes >> 4);
