@@ -429,9 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // several blocks of k where the tiles have few.
   const uint32_t widest = uniform(s.columns);
   const uint32_t stage_bytes = kTokens + widest * kBlockK;
-  const uint32_t num_stages = min(static_cast<uint32_t>(kMaxStages),
-                                  (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
   const int per = widest <= 16 ? 4 : widest <= 48 ? 2 : 1;
+  // A wait for a stage tells its rounds apart by parity, so the round before has to be
+  // over by then.  With an even number of stages the same issuing warp has waited for
+  // it.  With an odd one the other has, and the accumulators' waits have to say it: that all
+  // before the last hand-over is done (or, per == 1, where the stage is waited for
+  // first, before the last three).
+  const uint32_t fit = min(static_cast<uint32_t>(kMaxStages), (smem_bytes - static_cast<uint32_t>(stages - raw)) / stage_bytes);
+  const uint32_t num_stages = (fit & 1) && (per == 4 || fit < 5) ? fit - 1 : fit;
   const uint32_t acc_columns = per * 2 * widest;
   const uint32_t kept = per == 1 ? 16 : 32;
   if (threadIdx.x == 0) {
@@ -507,14 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t desc = mma_mx_desc(128, uniform(c.columns), 0);
         for (int kb = 0, in = 0; kb < blocks_k; ++kb, ++it) {
           const uint32_t at = st, round = phase, ac = group & 1, turn = (group >> 1) & 1, slot = in;
-          const bool first_turn = group < 2, last = kb + 1 == blocks_k;
+          const bool last = kb + 1 == blocks_k;
           if (++st == num_stages) st = 0, phase ^= 1;
           if (++in == per || last) in = 0, ++group;
           if ((it & 1) != odd) continue;
-          // The operands first, which are here long before the accumulator is back, and
-          // no vote in between: all of it is on the accumulators' round (prefill 605 -> 575 us).
-          ok = ok && wait_or_quit(&s.full[at], round, quit, err) &&
-               (first_turn || wait_or_quit(&s.acc_empty[ac], turn ^ 1, quit, err));
+          // With many tokens the operands first, which are here long before the accumulator
+          // is back, and no vote: all of it is on the accumulators' round (prefill 605 ->
+          // 575 us).  (A fresh barrier counts as having ended the round before its first.)
+          uint64_t *wait1 = &s.acc_empty[ac], *wait2 = &s.full[at];
+          uint32_t parity1 = turn ^ 1, parity2 = round;
+          if (per == 1) {
+            wait1 = &s.full[at], wait2 = &s.acc_empty[ac];
+            parity1 = round, parity2 = turn ^ 1;
+          }
+          ok = ok && wait_or_quit(wait1, parity1, quit, err) && wait_or_quit(wait2, parity2, quit, err);
           __syncwarp();
           tmem_fence_after();
           if (elect_one() && ok) {

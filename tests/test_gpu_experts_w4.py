@@ -182,6 +182,32 @@ def test_4096_groups():
     within(r.read16(out), y, y.abs() * 2.0 ** -8 + sum_err(K) * mag, "product")
 
 
+# As many stages as fit are five where tiles have 17 to 64 tokens, and with 16 where
+# there are thousands of groups: every block of k has to wait for its own fill.
+@pytest.mark.parametrize("counts,layout,K", [([33, 0, 7, 20, 1, 16], "ll", 6272), ([30, 2, 11, 5], "em", 1152), ([64, 9, 50], "em", 1408),
+                                             ([3] * 2500, "em", 640)])
+def test_stages_in_odd_numbers_and_many_launches(counts, layout, K):
+    E, F = len(counts), 256
+    r = Rows(counts, layout, 1, 3)
+    xq, xs, x = r.fp8(K, 41)
+    some = min(E, 6)
+    q, s, w = weights4(some, 2 * F, K, 42)
+    if some < E:
+        pick = torch.arange(E, device=DEV) % some
+        q, s, w = q[pick], s[pick], w[pick]
+    out, (act, acts) = r.out16(2 * F), r.out8(F)
+    ep.ep_grouped_matmul_w4(xq, xs, q, s, out, **r.args())
+    y, mag = product64(r, x, w)
+    within(r.read16(out), y, y.abs() * 2.0 ** -8 + sum_err(K) * mag, "product")
+    ep.ep_grouped_matmul_w4_swiglu(xq, xs, q, s, act, acts, **r.args())
+    first = out.clone(), act.clone(), acts.clone()
+    for _ in range(200):
+        ep.ep_grouped_matmul_w4(xq, xs, q, s, out, **r.args())
+        ep.ep_grouped_matmul_w4_swiglu(xq, xs, q, s, act, acts, **r.args())
+    for a, b in zip(first, (out, act, acts)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_reads_64_bit_offsets():
     """Live rows past 2^31 elements of x and out, weights past 2^31 codes."""
     M, E, K, N = 45000, 8, 7168, 7168
