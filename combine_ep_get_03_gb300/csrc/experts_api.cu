@@ -347,7 +347,7 @@ ep_status_t ep_block_norm_forward(const ep_block_norm_t* norm, const void* resid
 
 ep_status_t ep_block_norm_workspace_bytes(int hidden, int64_t* bytes) {
   if (hidden < 8 || hidden % 8 != 0 || hidden > ep::kBlockNormMaxHidden || !bytes) return EP_ERR_INVALID_ARG;
-  *bytes = static_cast<int64_t>(ep::kBlockNormMaxBlocks) * 3 * sizeof(float) * hidden;
+  *bytes = static_cast<int64_t>(ep::kBlockNormMaxBlocks) * 2 * sizeof(float) * hidden;
   return EP_OK;
 }
 

@@ -781,8 +781,8 @@ def ep_block_norm_backward(new_residual, y, rstd, grad_new_residual, grad_x, gra
     T, H = shape
     row, f32 = (H,), torch.float32
     if workspace is not None and (not isinstance(workspace, torch.Tensor) or
-                                  workspace.numel() * workspace.element_size() < 3072 * H):
-        raise ValueError(f"workspace must be a tensor of at least {3072 * H} bytes")
+                                  workspace.numel() * workspace.element_size() < 2048 * H):
+        raise ValueError(f"workspace must be a tensor of at least {2048 * H} bytes")
     _check(lib().ep_block_norm_backward(
         n, _shaped(new_residual, shape, dtype, "new_residual", dev), _shaped(y, shape, _BF, "y", dev),
         None if rstd is None else _vector(rstd, 2 * T, _F32, "rstd", dev),

@@ -56,7 +56,7 @@ def test_norm_forward_refusals(lib):
 
 def test_norm_workspace_bytes(lib):
     n = ctypes.c_int64()
-    assert lib.ep_block_norm_workspace_bytes(7168, ctypes.byref(n)) == ep.EP_OK and n.value == 256 * 3 * 4 * 7168
+    assert lib.ep_block_norm_workspace_bytes(7168, ctypes.byref(n)) == ep.EP_OK and n.value == 256 * 2 * 4 * 7168
     for H in (0, -8, 4, 20, 16392):
         assert lib.ep_block_norm_workspace_bytes(H, ctypes.byref(n)) == BAD
     assert lib.ep_block_norm_workspace_bytes(64, None) == BAD
