@@ -99,6 +99,7 @@ constexpr int kRingThreads = 512, kRingWarps = kRingThreads / 32;
 constexpr int kWordsEach = 2;                               // 8-channel words of a row that a thread owns
 constexpr int kRingHidden = kRingThreads * kWordsEach * 8;  // rows beyond take the kernels for long rows
 constexpr int kMaxStages = 4;
+constexpr int kRingAlign = 128;  // of the dynamic shared memory, and so of what lies before it
 constexpr int kNarrowWarps = 14;  // the backward pass has 144 registers a thread for as many
 
 // Barriers and partial sums of a block's teams.
@@ -117,7 +118,7 @@ struct RingShared {
 // kY: there is a block behind; kToken: its gate comes per token.
 template <bool kRes32, bool kY, bool kToken>
 __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormArgs a, int warps, int num_stages) {
-  extern __shared__ __align__(128) unsigned char ring[];
+  extern __shared__ __align__(kRingAlign) unsigned char ring[];
   __shared__ RingShared s;
   const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
   const int team = threadIdx.x / (warps * 32), threads = warps * 32, tid = threadIdx.x % threads, warp = tid >> 5;
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kRingThreads) k_block_norm_long(const BlockNor
 template <int kThreads, int kWords, bool kRes32, bool kPre, bool kY, bool kToken>
 __global__ void __launch_bounds__(kThreads, 1)
     k_block_norm_backward(const BlockNormBackwardArgs a, int warps, int num_stages) {
-  extern __shared__ __align__(128) unsigned char ring[];
+  extern __shared__ __align__(kRingAlign) unsigned char ring[];
   __shared__ RingShared s;
   const BlockNormArgs& n = a.n;
   const int lane = threadIdx.x & 31, teams = blockDim.x / (warps * 32);
@@ -830,7 +831,7 @@ cudaError_t ring_room(int* room) {
   int device = 0, smem = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
-  *room = smem - static_cast<int>(sizeof(RingShared));
+  *room = smem - static_cast<int>((sizeof(RingShared) + kRingAlign - 1) / kRingAlign * kRingAlign);
   return e;
 }
 

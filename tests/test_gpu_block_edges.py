@@ -1,0 +1,40 @@
+"""The norms around a block at the ends of what their calls accept: widths whose
+stages fill shared memory, calls that need no input, as many tokens as an int
+counts, weights that are not finite beside padding tokens."""
+import math
+
+import pytest
+import torch
+
+import test_gpu_block as block
+from combine_ep_get_03_gb300 import ep
+from test_gpu_block import Norms, TYPES
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+# Four stages of 5592 channels and three of 7456 take 223 680 bytes where all (bf16) or
+# two (fp32) of the residual-typed rows are there: more than a block has beside its barriers.
+@pytest.mark.parametrize("H", [5592, 7456, 5584, 7464])
+@pytest.mark.parametrize("gate", ["none", "token"])
+@pytest.mark.parametrize("res,wt", TYPES)
+def test_norm_backward_where_stages_fill_shared_memory(H, gate, res, wt):
+    for T in (3, 320):
+        block.test_norm_backward(dict(T=T, H=H, post=True, pre=True, gate=gate), res, wt)
+    c = Norms(320, H, res, wt, True, True, gate)
+    new, _, rstd = c.forward()
+    ws = torch.empty(ep.ep_block_norm_workspace_bytes(H), dtype=torch.uint8, device=DEV)
+
+    def grads(y, dnew, dx):
+        dres, dy = torch.empty_like(new), None if y is None else torch.empty_like(c.y)
+        dpre = None if dx is None else torch.empty(H, device=DEV)
+        ep.ep_block_norm_backward(new, y, rstd, dnew, dx, dres, dy, ws, grad_pre_weight=dpre, **c.how)
+        return [t for t in (dres, dy, dpre) if t is not None]
+
+    # an input left out counts as zeros: the same bits
+    for y in (None, c.y):
+        for dnew, dx in ((None, c.dx), (c.dnew, None)):
+            zeros = [torch.zeros_like(t) if g is None else g for t, g in ((c.dnew, dnew), (c.dx, dx))]
+            for a, b in zip(grads(y, dnew, dx), grads(y, *zeros)):
+                assert torch.equal(a, b)
