@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = 0; lane == 0 && i < copies; ++i)
     if (i % warps == warp) mine |= 1u << i;
   if (tid == 0) {
-    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], copies);
+    // an mbarrier counts from 1; where nothing is read nobody waits
+    for (int i = 0; i < num_stages; ++i) mbar_init(&full[i], copies ? copies : 1);
     s.quit = 0;
     mbar_init_fence();
   }

@@ -38,3 +38,18 @@ def test_norm_backward_where_stages_fill_shared_memory(H, gate, res, wt):
             zeros = [torch.zeros_like(t) if g is None else g for t, g in ((c.dnew, dnew), (c.dx, dx))]
             for a, b in zip(grads(y, dnew, dx), grads(y, *zeros)):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H", [264, 2048, 7168, 8200])
+@pytest.mark.parametrize("gate", ["none", "vector", "token"])
+def test_norm_backward_that_needs_no_input(H, gate):
+    """No gradient given, nothing of y needed: zeros, whatever the gate."""
+    for res, wt in TYPES:
+        c = Norms(33, H, res, wt, False, True, gate, masked=True)
+        dres, dy = torch.full_like(c.residual, 7.0), torch.full_like(c.y, 7.0)
+        how = dict(pre_weight=c.pre, gate=c.gate, token_mask=c.mask)
+        ep.ep_block_norm_backward(None, None, None, None, None, dres, None, None, **how)
+        assert (dres == 0).all()
+        dres.fill_(7.0)
+        ep.ep_block_norm_backward(None, None, None, None, None, dres, dy, None, **how)
+        assert (dres == 0).all() and (dy == 0).all()
