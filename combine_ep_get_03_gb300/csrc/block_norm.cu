@@ -836,6 +836,9 @@ cudaError_t ring_room(int* room) {
   return e;
 }
 
+// a / b rounded up, for every a that an int holds.
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
 // Warps that hold a row.
 int row_warps(int H, int words_each) { return (H / 8 + 32 * words_each - 1) / (32 * words_each); }
 
@@ -856,13 +859,13 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
         (e = ring_room(&room)) != cudaSuccess)
       return e;
     const int bytes = a.H * ((res32 ? 4 : 2) + (y ? 2 : 0) + (token ? 2 : 0));
-    const int warps = row_warps(a.H, kWordsEach), per_sm = (a.T + sms - 1) / sms;
+    const int warps = row_warps(a.H, kWordsEach), per_sm = ceil_div(a.T, sms);
     int teams = kRingWarps / warps;
     if (teams > per_sm) teams = per_sm;
     if (teams > room / (2 * bytes)) teams = room / (2 * bytes);
     int stages = room / (bytes * teams);
     if (stages > kMaxStages) stages = kMaxStages;
-    const int most = (a.T + teams - 1) / teams;
+    const int most = ceil_div(a.T, teams);
     return launch_early(kernel, 1, dim3(sms < most ? sms : most), dim3(teams * warps * 32), bytes * teams * stages, stream,
                         a, warps, stages);
   }
@@ -910,7 +913,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
     // 99 instead of 122; 2048 fp32 55 instead of 62; 2560 (10 warps) bf16 62 instead of 57.
     const int single = row_warps(a.n.H, 1);
     const bool one = single <= kRingWarps && (res32 || kRingWarps / single * single >= kRingWarps - 1);
-    const int warps = one ? single : row_warps(a.n.H, kWordsEach), per_sm = (a.n.T + sms - 1) / sms;
+    const int warps = one ? single : row_warps(a.n.H, kWordsEach), per_sm = ceil_div(a.n.T, sms);
     const bool wide = one || warps > kNarrowWarps;
     int teams = (wide ? kRingWarps : kNarrowWarps) / warps;
     if (teams > per_sm) teams = per_sm;
@@ -926,7 +929,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& args, bool r
     static std::atomic<unsigned long long> ready[48];  // devices set up, a bit each
     const int which = (one + wide) * 16 + res32 * 8 + (a.grad_x != nullptr) * 4 + a.need_y * 2 + gate;
     if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess) return e;
-    const int most = (a.n.T + teams - 1) / teams;
+    const int most = ceil_div(a.n.T, teams);
     if (blocks > most) blocks = most;
     e = launch_early(kernel, 1, dim3(blocks), dim3(teams * warps * 32), need, stream, a, warps, stages);
   } else {

@@ -53,3 +53,35 @@ def test_norm_backward_that_needs_no_input(H, gate):
         dres.fill_(7.0)
         ep.ep_block_norm_backward(None, None, None, None, None, dres, dy, None, **how)
         assert (dres == 0).all() and (dy == 0).all()
+
+
+def test_norm_of_as_many_tokens_as_an_int_counts():
+    """2^31 - 1 rows of eight channels, of which the first and the last are not
+    zeros: the bits of those rows in a small call."""
+    T, H, few = 2 ** 31 - 1, 8, 1000
+    torch.cuda.empty_cache()
+    n = lambda s: torch.randn((2 * few, H), generator=block.gen(s), device=DEV).bfloat16()  # noqa: E731
+    pre = 1 + 0.1 * torch.randn(H, generator=block.gen(3), device=DEV)
+
+    def spread(rows):
+        big = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+        big[:few], big[-few:] = rows[:few], rows[few:]
+        return big
+
+    ends = lambda t: torch.cat((t[:few], t[-few:]))  # noqa: E731
+
+    def run(h, dx):
+        x, rstd = torch.empty_like(h), torch.empty((2, h.shape[0]), device=DEV)
+        ep.ep_block_norm_forward(h, None, None, x, rstd=rstd, pre_weight=pre)
+        # x's memory takes the gradient
+        first = ends(x)
+        ep.ep_block_norm_backward(h, None, rstd, None, dx, x, None, None, pre_weight=pre)
+        assert not x[few:few + 10000].any() and not x[-few - 10000:-few].any() or h.shape[0] == 2 * few
+        return first, ends(rstd[1]), ends(x)
+
+    h, dx = n(1), n(2)
+    want = run(h, dx)
+    got = run(spread(h), spread(dx))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    torch.cuda.empty_cache()
