@@ -102,6 +102,10 @@ constexpr int kMaxStages = 4;
 constexpr int kRingAlign = 128;  // of the dynamic shared memory, and so of what lies before it
 constexpr int kNarrowWarps = 14;  // the backward pass has 144 registers a thread for as many
 
+// What a thread takes for a row whose copies it waited for in vain.  It asks for no
+// more copies then, so that no barrier's rounds mix, and waits in vain for later rows too.
+__device__ __forceinline__ float2 lost() { return both(__int_as_float(0x7fc00000)); }
+
 // Barriers and partial sums of a block's teams.
 struct RingShared {
   uint64_t full[kRingWarps][kMaxStages];
@@ -221,11 +225,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
         }
       }
     }
-    if (!landed) {  // a copy that never came: NaN, not old values
+    if (!landed) {  // a copy that never came: NaN, not old values, in the sums too
+      mine = 0;
+      t1 = lost();
 #pragma unroll
       for (int k = 0; k < kWordsEach; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[k][j] = both(__int_as_float(0x7fc00000));
+        for (int j = 0; j < 4; ++j) h[k][j] = lost();
     }
     float r1 = 1.0f;
     if (post) r1 = rsqrtf(fmaf(sum(t1), inv_h, a.eps));
@@ -535,11 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!landed) {  // a copy that never came: NaN, not old values
+    if (!landed) {  // a copy that never came: NaN, not old values, in the sums too
+      mine = 0;
+      t1 = t2 = lost();
 #pragma unroll
       for (int k = 0; k < kWords; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[k][j] = both(__int_as_float(0x7fc00000));
+        for (int j = 0; j < 4; ++j) {
+          g[k][j] = lost();
+          if (kPre) sum_pre[k][j] = lost();
+        }
     }
     float s1 = t1.x + t1.y, s2 = t2.x + t2.y, s3 = t3.x + t3.y;
     if (kPre) s1 = warp_sum(s1);
@@ -882,11 +893,13 @@ namespace {
 using Backward = void (*)(BlockNormBackwardArgs, int, int);
 template <int kWarps, int kWords, bool kRes32>
 Backward backward_kernel(bool pre, bool y, bool token) {
+  // fp32 with a gate per token: 8192 x 7168 201 us in the instance of 512 threads, 247 in that of 448
+  constexpr int kThreads = 32 * kWarps, kGated = kRes32 ? kRingThreads : kThreads;
   static const Backward kernels[8] = {
-      k_block_norm_backward<32 * kWarps, kWords, kRes32, false, false, false>, k_block_norm_backward<32 * kWarps, kWords, kRes32, false, false, true>,
-      k_block_norm_backward<32 * kWarps, kWords, kRes32, false, true, false>,  k_block_norm_backward<32 * kWarps, kWords, kRes32, false, true, true>,
-      k_block_norm_backward<32 * kWarps, kWords, kRes32, true, false, false>,  k_block_norm_backward<32 * kWarps, kWords, kRes32, true, false, true>,
-      k_block_norm_backward<32 * kWarps, kWords, kRes32, true, true, false>,   k_block_norm_backward<32 * kWarps, kWords, kRes32, true, true, true>};
+      k_block_norm_backward<kThreads, kWords, kRes32, false, false, false>, k_block_norm_backward<kGated, kWords, kRes32, false, false, true>,
+      k_block_norm_backward<kThreads, kWords, kRes32, false, true, false>,  k_block_norm_backward<kGated, kWords, kRes32, false, true, true>,
+      k_block_norm_backward<kThreads, kWords, kRes32, true, false, false>,  k_block_norm_backward<kGated, kWords, kRes32, true, false, true>,
+      k_block_norm_backward<kThreads, kWords, kRes32, true, true, false>,   k_block_norm_backward<kGated, kWords, kRes32, true, true, true>};
   return kernels[pre * 4 + y * 2 + token];
 }
 

@@ -637,7 +637,8 @@ typedef struct {
  *                    post_weight) and of the new residual (with pre_weight), for the
  *                    backward pass; the other entries are left as they are.
  * 16-byte aligned; one launch.  A row whose copy into shared memory never lands (a
- * bounded wait that gives up) becomes NaN, here and in the backward pass. */
+ * bounded wait that gives up) becomes NaN, and so do the rows that its block would have
+ * fetched from then on, their rstd and, in the backward pass, the weights' gradients. */
 ep_status_t ep_block_norm_forward(const ep_block_norm_t* norm, const void* residual, const void* y, void* new_residual,
                                   void* x, float* rstd, int num_sms, ep_stream_t stream);
 
