@@ -100,7 +100,12 @@ constexpr int kWordsEach = 2;                               // 8-channel words o
 constexpr int kRingHidden = kRingThreads * kWordsEach * 8;  // rows beyond take the kernels for long rows
 constexpr int kMaxStages = 4;
 constexpr int kRingAlign = 128;  // of the dynamic shared memory, and so of what lies before it
-constexpr int kNarrowWarps = 14;  // the backward pass has 144 registers a thread for as many
+// Warps of the backward pass's other instance of two words a thread.  A thread has 128
+// registers in both, but what the compiler makes of them differs (8192 rows, us, 14
+// against 16 warps at most: bf16 7168 115 and 143, 5120 97 and 122; fp32 7168 165 and 178, 5120 132
+// and 122; bf16 with a gate per token 7168 188 and 197, 5120 159 and 161; fp32 with one, which
+// therefore takes 16, 247 and 201, 192 and 166).
+constexpr int kNarrowWarps = 14;
 
 // What a thread takes for a row whose copies it waited for in vain.  It asks for no
 // more copies then, so that no barrier's rounds mix, and waits in vain for later rows too.
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kRingThreads) k_block_norm_long(const BlockNor
 // 146).  Each tensor's copy is asked for by a warp of its own.
 // kPre: x's gradient takes part; kY: y is needed (a norm behind the block or its
 // gate's gradient); kToken: the gate comes per token.
-// kThreads: the most that the block has; 448 leave a thread 144 registers, 512 128.
+// kThreads: the most that the block has.
 // kWords: the 8-channel words of a row that a thread owns.
 template <int kThreads, int kWords, bool kRes32, bool kPre, bool kY, bool kToken>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -893,7 +898,6 @@ namespace {
 using Backward = void (*)(BlockNormBackwardArgs, int, int);
 template <int kWarps, int kWords, bool kRes32>
 Backward backward_kernel(bool pre, bool y, bool token) {
-  // fp32 with a gate per token: 8192 x 7168 201 us in the instance of 512 threads, 247 in that of 448
   constexpr int kThreads = 32 * kWarps, kGated = kRes32 ? kRingThreads : kThreads;
   static const Backward kernels[8] = {
       k_block_norm_backward<kThreads, kWords, kRes32, false, false, false>, k_block_norm_backward<kGated, kWords, kRes32, false, false, true>,
