@@ -124,8 +124,10 @@ struct RingShared {
 // copies in a ring of stages in shared memory, and a thread keeps its channels'
 // weights in registers over all rows.  The first barrier of a row's sums says that
 // the stage of the row before has been read, so its refill needs no other.
-// kY: there is a block behind; kToken: its gate comes per token.
-template <bool kRes32, bool kY, bool kToken>
+// kY: there is a block behind; kToken: its gate comes per token; kMask: there may be
+// padding tokens.  (One kernel with and without: 16 384 x 7168 fp32 without 221 -> 227 us,
+// but with a gate per token 272 -> 263, so that is always the one with.)
+template <bool kRes32, bool kY, bool kToken, bool kMask>
 __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormArgs a, int warps, int num_stages) {
   extern __shared__ __align__(kRingAlign) unsigned char ring[];
   __shared__ RingShared s;
@@ -204,12 +206,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
     for (int b = 8; b; b >>= 1) f += __shfl_xor_sync(kFullMask, f, b);
     return f;
   };
-  bool next_live = !a.mask || first >= a.T || a.mask[first];
+  bool next_live = !kMask || !a.mask || first >= a.T || a.mask[first];
   for (long long t = first; t < a.T; t += step) {
     const bool live = next_live;
-    if (a.mask && t + step < a.T) next_live = a.mask[t + step];
+    if (kMask && a.mask && t + step < a.T) next_live = a.mask[t + step];
     const unsigned char* d = stages + static_cast<size_t>(st) * stage_bytes;
     const bool landed = wait_or_quit(&full[st], phase, &s.quit, nullptr);
+    auto refill = [&]() {
+      if (t != first) fetch(t + (num_stages - 1) * step, st ? st - 1 : num_stages - 1);
+    };
+    const long long row = t * words;
+    if (kMask && !live) {  // zeros, whatever the weights are
+      if (warps > 1) team_barrier(team, threads);
+      else __syncwarp();
+      if (!landed) mine = 0;
+      refill();
+      const float zero[8] = {};
+      for (int c = tid; c < words; c += threads) {
+        if (kY) store8(a.new_residual, kRes32, row + c, zero);
+        if (pre) store8(a.x, false, row + c, zero);
+      }
+      if (tid == 0 && a.rstd) {
+        if (post) a.rstd[t] = 0.0f;
+        if (pre) a.rstd[a.T + t] = 0.0f;
+      }
+      __syncwarp();
+      if (++st == num_stages) st = 0, phase ^= 1;
+      continue;
+    }
     float2 h[kWordsEach][4], y[kY ? kWordsEach : 1][4];
     float2 t1 = both(0.0f);
 #pragma unroll
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
         h[k][j] = both(0.0f);
         if (kY) y[k][j] = both(0.0f);
       }
-      if (c >= words || !live) continue;
+      if (c >= words) continue;
       load8(d, kRes32, c, h[k]);
       if (kY) {
         load8(d + o_y, false, c, y[k]);
@@ -240,12 +264,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
     }
     float r1 = 1.0f;
     if (post) r1 = rsqrtf(fmaf(sum(t1), inv_h, a.eps));
-    if (!live) r1 = 0.0f;
-    auto refill = [&]() {
-      if (t != first) fetch(t + (num_stages - 1) * step, st ? st - 1 : num_stages - 1);
-    };
     if (post) refill();
-    const long long row = t * words;
     if (kY) {
       if (post && tid == 0 && a.rstd) a.rstd[t] = r1;
 #pragma unroll
@@ -257,7 +276,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float2 v = mul2(y[k][j], both(r1));
-          if (kToken) v = live ? mul2(v, u[j]) : both(0.0f);
+          if (kToken) v = mul2(v, u[j]);
           h[k][j] = fma2(q[k][j], v, h[k][j]);
         }
         store8(a.new_residual, kRes32, row + c, h[k]);
@@ -269,8 +288,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_block_norm(const BlockNormA
       for (int k = 0; k < kWordsEach; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) t2 = fma2(h[k][j], h[k][j], t2);
-      float r2 = rsqrtf(fmaf(sum(t2), inv_h, a.eps));
-      if (!live) r2 = 0.0f;
+      const float r2 = rsqrtf(fmaf(sum(t2), inv_h, a.eps));
       if (!post) refill();
       if (tid == 0 && a.rstd) a.rstd[a.T + t] = r2;
 #pragma unroll
@@ -865,13 +883,16 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, bool res32, int sms, cudaS
   if (a.H <= kRingHidden) {
     const bool y = a.y != nullptr, token = y && a.gate_per_token;
     using Kernel = void (*)(BlockNormArgs, int, int);
-    static const Kernel kernels[2][3] = {
-        {k_block_norm<false, false, false>, k_block_norm<false, true, false>, k_block_norm<false, true, true>},
-        {k_block_norm<true, false, false>, k_block_norm<true, true, false>, k_block_norm<true, true, true>}};
-    const Kernel kernel = kernels[res32][y + token];
-    static std::atomic<unsigned long long> ready[6];  // devices set up, a bit each
+    static const Kernel kernels[12] = {
+        k_block_norm<false, false, false, false>, k_block_norm<false, true, false, false>, k_block_norm<false, true, true, true>,
+        k_block_norm<true, false, false, false>,  k_block_norm<true, true, false, false>,  k_block_norm<true, true, true, true>,
+        k_block_norm<false, false, false, true>,  k_block_norm<false, true, false, true>,  k_block_norm<false, true, true, true>,
+        k_block_norm<true, false, false, true>,   k_block_norm<true, true, false, true>,   k_block_norm<true, true, true, true>};
+    const int which = (a.mask ? 6 : 0) + res32 * 3 + y + token;
+    const Kernel kernel = kernels[which];
+    static std::atomic<unsigned long long> ready[12];  // devices set up, a bit each
     int room = 0;
-    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[res32 * 3 + y + token], 0)) != cudaSuccess ||
+    if ((e = set_up_kernel(reinterpret_cast<const void*>(kernel), ready[which], 0)) != cudaSuccess ||
         (e = ring_room(&room)) != cudaSuccess)
       return e;
     const int bytes = a.H * ((res32 ? 4 : 2) + (y ? 2 : 0) + (token ? 2 : 0));

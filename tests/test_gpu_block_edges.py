@@ -85,3 +85,24 @@ def test_norm_of_as_many_tokens_as_an_int_counts():
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("H", [64, 2048, 8200])
+@pytest.mark.parametrize("gate", ["none", "vector", "token"])
+def test_padding_beside_weights_that_are_not_finite(H, gate):
+    """A padding token's results are 0 whatever the weights are."""
+    for res, wt in TYPES:
+        c = Norms(60, H, res, wt, True, True, gate, masked=True)
+        c.post[3], c.post[4], c.pre[5], c.pre[6] = math.inf, math.nan, -math.inf, math.nan
+        if gate == "vector":
+            c.gate[7] = math.inf
+        off = ~c.on
+        new, x, rstd = c.forward()
+        assert (new[off] == 0).all() and (x[off] == 0).all() and (rstd[:, off] == 0).all()
+        assert not new[c.on][:, 3:5].isfinite().any() and not x[c.on][:, 3:7].isfinite().any()
+        dres, dy = torch.empty_like(new), torch.empty_like(c.y)
+        ep.ep_block_norm_backward(new, c.y, rstd, c.dnew, c.dx, dres, dy, None, **c.how)
+        assert (dres[off] == 0).all() and (dy[off] == 0).all()
+        x2 = torch.empty_like(x)
+        ep.ep_block_norm_forward(c.residual, None, None, x2, pre_weight=c.pre, token_mask=c.mask)
+        assert (x2[off] == 0).all()
