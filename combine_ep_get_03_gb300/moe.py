@@ -56,7 +56,10 @@ class ExpertWeights:
             self.st = self.s.transpose(1, 2).contiguous()
 
 
-_E2M1_BORDERS = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)  # half way between 0, 0.5, 1, 1.5, 2, 3, 4, 6
+# Half way between 0, 0.5, 1, 1.5, 2, 3, 4, 6, the borders to even codes an fp32 step
+# lower: a weight on a border goes to the even code.
+_STEP = 2.0 ** -24
+_E2M1_BORDERS = (0.25, 0.75 - _STEP, 1.25, 1.75 - 2 * _STEP, 2.5, 3.5 - 4 * _STEP, 5.0)
 
 
 def quantize_e2m1(w: torch.Tensor):
@@ -64,7 +67,7 @@ def quantize_e2m1(w: torch.Tensor):
     channels [E, ceil(N/128), K/128, 512], as ``ep_grouped_matmul_w4`` takes them.
 
     The largest magnitude of 32 channels lies in [4, 8) steps of 2^exponent; what
-    is above 6 becomes 6."""
+    is above 6 becomes 6, the rest rounds to the nearest value, ties to even codes."""
     E, N, K = w.shape
     nb, kb = (N + 127) // 128, K // 128
     codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
