@@ -67,7 +67,8 @@ def quantize_e2m1(w: torch.Tensor):
     channels [E, ceil(N/128), K/128, 512], as ``ep_grouped_matmul_w4`` takes them.
 
     The largest magnitude of 32 channels lies in [4, 8) steps of 2^exponent; what
-    is above 6 becomes 6, the rest rounds to the nearest value, ties to even codes."""
+    is above 6 becomes 6, the rest rounds to the nearest value, ties to even codes.
+    32 channels with a weight that is not finite get the exponent of NaN."""
     E, N, K = w.shape
     nb, kb = (N + 127) // 128, K // 128
     codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
@@ -83,7 +84,7 @@ def quantize_e2m1(w: torch.Tensor):
         c = c.view(N, K // 2, 2)
         codes[e] = c[..., 0] | (c[..., 1] << 4)
         s = torch.full((nb * 128, K // 32), 127, dtype=torch.uint8, device=w.device)
-        s[:N] = (x + 127).to(torch.uint8)
+        s[:N] = torch.where(b.isfinite().all(2), x + 127, 255).to(torch.uint8)
         scales[e] = s.view(nb, 4, 32, kb, 4).permute(0, 3, 2, 1, 4).reshape(nb, kb, 512)
     return codes, scales
 

@@ -36,3 +36,21 @@ def test_ties_go_to_the_even_code(dtype, power):
     assert v[:7].tolist() == even and v[7:14].tolist() == [-x for x in even]
     assert v[14:21].tolist() == [0.5, 1, 1.5, 2, 3, 4, 6] and v[21:28].tolist() == [0, 0.5, 1, 1.5, 2, 3, 4]
     assert v[28] == 6 and (v[29:] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_weights_that_are_not_finite_stay_visible(bad):
+    """32 channels with such a weight get the exponent that stands for NaN (the 8-bit
+    weights' block becomes NaN too); the others keep their codes."""
+    torch.manual_seed(1)
+    w = torch.randn(1, 130, 256)
+    q, s = moe.quantize_e2m1(w)
+    w2 = w.clone()
+    w2[0, 129, 70] = bad
+    q2, s2 = moe.quantize_e2m1(w2)
+    assert exponent(s2, 129, 2) == 255 and exponent(s, 129, 2) < 255
+    codes, codes2 = codes_of(q[0], 130, 256), codes_of(q2[0], 130, 256)
+    rest = torch.ones(130, 256, dtype=torch.bool)
+    rest[129, 64:96] = False
+    assert torch.equal(codes[rest], codes2[rest])
+    assert (s != s2).sum() == 1 and (s2 == 255).sum() == 1
