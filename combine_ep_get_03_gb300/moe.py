@@ -255,7 +255,9 @@ class MoEBlock:
         h' = h + residual_scale * gate * (norm(y) * post)
 
     pre and post [H] (post may be None: no norm behind), gate [H], [T, H] bf16 or
-    None, router [E, H] bf16.  What forward saves is complete, as the layer's."""
+    None, router [E, H] bf16 or fp32.  The logits are fp32 for both: of two experts
+    close together a bf16 logit, of 8 bits, would make a tie.  What forward saves is
+    complete, as the layer's."""
 
     def __init__(self, layer: MoELayer, pre, router, post=None, gate=None, residual_scale=1.0, eps=1e-6):
         self.layer, self.pre, self.post, self.gate, self.router = layer, pre, post, gate, router
@@ -265,7 +267,9 @@ class MoEBlock:
     def _front(self, h, token_mask, rstd=None):
         x = self.layer._bf16(*h.shape)
         ep.ep_block_norm_forward(h, None, None, x, rstd=rstd, pre_weight=self.pre, eps=self.eps, token_mask=token_mask)
-        return x, x @ self.router.t()
+        if self.router.dtype is torch.float32:
+            return x, x.float() @ self.router.t()
+        return x, torch.mm(x, self.router.t(), out_dtype=torch.float32)
 
     def _behind(self, h, y, out, token_mask, rstd=None):
         ep.ep_block_norm_forward(h, y, out, None, rstd=rstd, post_weight=self.post, gate=self.gate, eps=self.eps,
@@ -293,8 +297,13 @@ class MoEBlock:
                                   gate=self.gate, grad_post_weight=grad_post, grad_gate=grad_gate,
                                   residual_scale=self.scale, token_mask=mask)
         grad_x, grad_logits, grad_w1, grad_w2 = self.layer.backward(grad_y, grad_loss, inner, w1, w2)
-        grad_router = grad_logits.t() @ x
-        grad_x = torch.addmm(grad_x, grad_logits, self.router)
+        if self.router.dtype is torch.float32:
+            grad_router = grad_logits.t() @ x.float()
+            grad_x = torch.addmm(grad_x.float(), grad_logits, self.router).bfloat16()
+        else:  # the products take the logits' gradient in bf16; their sums are fp32
+            grad_logits = grad_logits.bfloat16()
+            grad_router = grad_logits.t() @ x
+            grad_x = torch.addmm(grad_x, grad_logits, self.router)
         grad, grad_pre = torch.empty_like(h), f32(True)
         ep.ep_block_norm_backward(h, None, rstd, grad_h, grad_x, grad, None, self.workspace, pre_weight=self.pre,
                                   grad_pre_weight=grad_pre, token_mask=mask)

@@ -1,10 +1,14 @@
 """The layer of experts and the block around it: what a call's result has to be bit
-for bit."""
+for bit, and how the block routes."""
+import math
+
 import pytest
 import torch
 
 from combine_ep_get_03_gb300 import ep
+from combine_ep_get_03_gb300 import moe
 from test_gpu_block import Layout
+from test_gpu_experts import gen
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -33,3 +37,65 @@ def test_combine_gradient_in_e4m3_bit_for_bit(H, scale):
         assert (dy[~l.live] == 0x5A).all() and (ds.t()[:l.rows][~l.live] == 7.25).all() and (ds[:, l.rows:] == 7.25).all()
     assert l.h.get_device_status() == ep.EP_OK
     l.h.close()
+
+
+def block_and_weights(router, weigh=False, T=256, R=2, k=1, E=8, H=256, F=128):
+    torch.manual_seed(3)
+    layer = moe.MoELayer(R, E, k, H, F, T // R, weigh_in_combine=weigh, expert_alignment=16)
+    w1 = moe.ExpertWeights(torch.randn((E, 2 * F, H), device=DEV) / H ** 0.5)
+    w2 = moe.ExpertWeights(torch.randn((E, H, F), device=DEV) / F ** 0.5)
+    pre = 1 + 0.1 * torch.randn(H, device=DEV)
+    return moe.MoEBlock(layer, pre, router), w1, w2
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_routing_of_experts_close_together(dtype):
+    """Experts in pairs whose logits differ by about a thousandth of themselves: a bf16
+    logit has 8 bits and would tie them, fp32's error (256 products) is far below."""
+    T, E, H = 256, 8, 256
+    g = gen(21)
+    base = torch.randn((E // 2, 1, H), generator=g, device=DEV)
+    router = (base + 2.0 ** -10 * torch.randn((E // 2, 2, H), generator=g, device=DEV) * (dtype is torch.float32)).reshape(E, H)
+    if dtype is torch.bfloat16:  # one channel of the second of a pair a step of bf16 away
+        router = router.bfloat16()
+        router[1::2, 0] = (router[1::2, 0].view(torch.int16) + 1).view(torch.bfloat16)
+    block, w1, w2 = block_and_weights(router)
+    h = torch.randn((T, H), generator=g, device=DEV)
+    out, _, saved = block.forward(h, w1, w2)
+    x, idx = saved[1], saved[5][2][:, 0]
+    logits = x.double() @ router.double().t()
+    top = logits.topk(2, 1)
+    err = (H + 4) * 2.0 ** -24 * (x.double().abs() @ router.double().abs().t()).amax(1)
+    clear = top.values[:, 0] - top.values[:, 1] > 2 * err
+    assert clear.sum() > T // 8 and torch.equal(idx[clear], top.indices[clear, 0])
+    # gradients of the router's type, and of the stream
+    grads = block.backward(torch.randn((T, H), generator=g, device=DEV), torch.ones(1, device=DEV), saved, w1, w2)
+    assert grads["router"].dtype is dtype and grads["router"].isfinite().all() and grads["h"].isfinite().all()
+    dec = block.decode(h.clone(), w1, w2)
+    assert ((dec - out).norm() / (out - h).norm()).item() < 3 * math.sqrt(4) * 0.026
+    block.layer.check()
+    block.layer.close()
+
+
+def test_gradients_of_an_fp32_router():
+    """Against 64 bits, from the layer's own gradient of the logits: the balance
+    loss alone, so that nothing but the router's products rounds."""
+    T, E, H = 256, 8, 256
+    router = torch.randn((E, H), generator=gen(22), device=DEV) / 16
+    block, w1, w2 = block_and_weights(router, k=2)
+    h = torch.randn((T, H), generator=gen(23), device=DEV)
+    _, _, saved = block.forward(h, w1, w2)
+    zero = torch.zeros((T, H), device=DEV)
+    grads = block.backward(zero, torch.full((1,), 100.0, device=DEV), saved, w1, w2)
+    x, idx = saved[1].double(), saved[5][2]
+    hd = h.double().requires_grad_(True)
+    rd = router.double().requires_grad_(True)
+    xd = hd * (hd.square().mean(1, keepdim=True) + 1e-6).rsqrt() * block.pre.double()
+    p = torch.softmax(xd @ rd.t(), 1).mean(0)
+    count = torch.bincount(idx.reshape(-1), minlength=E)
+    (100.0 * 1e-2 * E / (2 * T) * (count * p).sum()).backward()
+    rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()  # noqa: E731
+    # x in bf16 on the one side, x's gradient on the other: half a step of 2^-8 at most each
+    assert rel(grads["router"], rd.grad) < 2.0 ** -8
+    assert rel(grads["h"], hd.grad) < 2.0 ** -7
+    block.layer.close()
