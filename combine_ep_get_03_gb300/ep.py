@@ -806,6 +806,7 @@ class Handle:
         self.T_ll = None   # tokens of the last low-latency dispatch
         self.T_em = None   # tokens of the last expert-major layout
         self.em_layouts = 0  # expert-major layouts so far: tells whether the last one is still a caller's own
+        self.em_captured = False  # ... unless a graph that makes one was replayed, which nothing here sees
         self.ptr = ep_handle_create(num_ranks, num_experts, num_topk, hidden, max_tokens_per_rank)
 
     @property
@@ -976,6 +977,7 @@ class Handle:
                                   recv_src_idx, recv_weights, num_sms, stream)
         self.T_em = T
         self.em_layouts += 1
+        self.em_captured = self.em_captured or torch.cuda.is_current_stream_capturing()
 
     def em_dispatch(self, x, topk_weights, dtype, recv_x, recv_scales=None, recv_src_idx=None, recv_weights=None,
                     num_sms=0, stream=None):

@@ -99,9 +99,9 @@ class ExpertWeights4:
 class MoELayer:
     """hidden and ffn are multiples of 128.  Every output is a tensor of its
     own, and what forward saves is all that its backward needs: other forwards
-    and decodes may come between, and backward calls in any order.  The handle
-    and the gate's workspace are the layer's, so its calls go to one stream at a
-    time."""
+    and decodes may come between, replayed from a graph too, and backward calls in
+    any order.  The handle and the gate's workspace are the layer's, so its calls
+    go to one stream at a time."""
 
     def __init__(self, num_ranks, num_experts, num_topk, hidden, ffn, max_tokens_per_rank, score=ep.EP_GATE_SOFTMAX,
                  num_groups=1, topk_groups=1, loss_coef=1e-2, expert_alignment=128, device="cuda",
@@ -192,7 +192,8 @@ class MoELayer:
         T = grad_out.shape[0]
         gy, gy_s = self._fp8(self.H)
         grad_w = self._f32(T, self.k)
-        if self.h.em_layouts != layout:  # another forward came between: the same ids give the same rows again
+        # another forward came, or may have been replayed, between: the same ids give the same rows again
+        if self.h.em_captured or self.h.em_layouts != layout:
             self.h.em_layout_and_dispatch(idx, grad_out, None, ep.EP_FP8_E4M3, self.align, gy, gy_s)
         elif not weighed:
             self.h.em_dispatch(grad_out, None, ep.EP_FP8_E4M3, gy, gy_s)

@@ -1,5 +1,5 @@
 """The layer of experts and the block around it: what a call's result has to be bit
-for bit, and how the block routes."""
+for bit, how the block routes, and backward passes around replayed graphs."""
 import math
 
 import pytest
@@ -99,3 +99,46 @@ def test_gradients_of_an_fp32_router():
     assert rel(grads["router"], rd.grad) < 2.0 ** -8
     assert rel(grads["h"], hd.grad) < 2.0 ** -7
     block.layer.close()
+
+
+@pytest.mark.parametrize("weigh", [False, True])
+def test_backward_around_a_replayed_forward(weigh):
+    """A captured forward makes the handle's layout anew whenever it is replayed,
+    which the host does not see: a backward behind it has the bits of one that
+    directly follows its forward."""
+    T, E, H = 64, 8, 256
+    block, w1, w2 = block_and_weights(None, weigh, T, k=2)
+    layer = block.layer
+    batch = lambda s: (torch.randn((T, H), generator=gen(s), device=DEV).bfloat16(),  # noqa: E731
+                       torch.randn((T, E), generator=gen(s + 50), device=DEV))
+    (x, logits), (x2, logits2), (go, _) = batch(1), batch(2), batch(3)
+    gl = torch.ones(1, device=DEV)
+    out, _, saved = layer.forward(x, logits, w1, w2)
+    want = layer.backward(go, gl, saved, w1, w2)
+    out2, _, saved2 = layer.forward(x2, logits2, w1, w2)
+    want2 = layer.backward(go, gl, saved2, w1, w2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured, _, kept = layer.forward(x2, logits2, w1, w2)
+    out, _, saved = layer.forward(x, logits, w1, w2)
+    graph.replay()
+    got = layer.backward(go, gl, saved, w1, w2)
+    graph.replay()
+    got2 = layer.backward(go, gl, kept, w1, w2)
+    layer.check()
+    assert torch.equal(captured, out2)
+    for a, b in zip(got + got2, want + want2):
+        assert torch.equal(a, b)
+    # a captured step of both passes, an eager forward before each replay
+    step = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(step):
+        _, _, kept = layer.forward(x2, logits2, w1, w2)
+        both = layer.backward(go, gl, kept, w1, w2)
+    for _ in range(2):
+        _, _, saved = layer.forward(x, logits, w1, w2)
+        step.replay()
+        for a, b in zip(both + layer.backward(go, gl, saved, w1, w2), want2 + want):
+            assert torch.equal(a, b)
+    layer.check()
+    layer.close()
