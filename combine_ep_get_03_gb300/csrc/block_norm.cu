@@ -11,13 +11,17 @@
 // shared memory, in a fixed order.
 //
 // Forward: two sums a row, of y^2 and of h^2.  16 384 tokens of 7168 channels: fp32
-// residual 224 us (6.3 TB/s), bf16 150; 4 096 channels fp32 123; one token 3.6 us in
-// a graph.  (Rows loaded to registers, a block of 8 warps a row: 226 us with the next
-// rows fetched to L2, 158, 132 and 4.9; 240, 191 without.  The second sum exchanged
-// with the next row's first, one barrier a row: 245, 150, 145 and 3.9.)
+// residual 221 us (6.4 TB/s), bf16 146; 4 096 channels fp32 124; one token 3.7 us in
+// a graph.  Rows in registers beyond 8192 channels: 4 096 tokens of 12 288 bf16 85 us, fp32
+// 104; of 16 384 90 and 141 (5.7 TB/s).  (Up to 8192, rows loaded to registers, a block of
+// 8 warps a row: 226 us with the next rows fetched to L2, 158, 132 and 4.9; 240, 191
+// without.  The second sum exchanged with the next row's first, one barrier a row: 245,
+// 150, 145 and 3.9.)
 //
 // Backward.  8 192 tokens of 7168, gate a vector: bf16 115 us (6.1 TB/s), fp32 165; 4 099
-// of 2048, fp32, gate per token: 39 us, some 8 of them two launches' start and end.
+// of 2048, fp32, gate per token: 39 us, some 8 of them two launches' start and end.  Beyond
+// 8192 channels rows are read twice: 4 096 of 12 288 bf16 270 us, fp32 277; of 16 384 369
+// and 415.
 // With hn = h rstd2, yn = y rstd1, a = grad_x pre, q = scale gate post:
 //   gh = grad_h + rstd2 (a - hn m1),        m1 = mean(a hn)
 //   grad_residual = gh,  grad_gate = scale gh yn post,  grad_post = scale gate gh yn,

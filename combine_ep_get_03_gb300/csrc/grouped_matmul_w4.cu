@@ -26,9 +26,11 @@
 // are start and end; with experts enough to fill the SMs four times 90 % of the copy
 // rate.  The loads alone take 45 of the 50 us (39 at the copy rate): TMA's spreading costs
 // some.  Many rows: the accumulators' round from the MMAs to the warps that add and back,
-// some 1 150 cycles a stage; 16 384 rows, 7 168 -> 2 x 2 048: 560 us, 1.7 PFLOP/s, at 1.3 of
-// 1.4 kW.  Of a stage's cycles shared memory is busy for 850 (weights and tokens are
-// written once and read once, the tokens twice): without the sums 375 us.
+// some 1 150 cycles a stage; 16 384 rows, 7 168 -> 2 x 2 048: 560 to 587 us over several runs,
+// 1.7 PFLOP/s, at 1.3 of 1.4 kW; plain, 2 048 -> 7 168: 349 us, 1.4 PFLOP/s (8-bit weights 278:
+// they are the faster ones there).  Of a stage's cycles shared memory is busy for 850
+// (weights and tokens are written once and read once, the tokens twice): without the
+// sums SwiGLU's takes 375 us.
 #include <cuda.h>
 
 #include <atomic>

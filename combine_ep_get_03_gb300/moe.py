@@ -258,7 +258,12 @@ class MoEBlock:
     pre and post [H] (post may be None: no norm behind), gate [H], [T, H] bf16 or
     None, router [E, H] bf16 or fp32.  The logits are fp32 for both: of two experts
     close together a bf16 logit, of 8 bits, would make a tie.  What forward saves is
-    complete, as the layer's."""
+    complete, as the layer's.
+
+    The norm in front and what is behind are two calls, so that a block stands
+    alone: h is written and read between two blocks, and the next norm takes it as it
+    was rounded.  ``ep_block_norm_forward`` does both at once, with the next block's
+    pre."""
 
     def __init__(self, layer: MoELayer, pre, router, post=None, gate=None, residual_scale=1.0, eps=1e-6):
         self.layer, self.pre, self.post, self.gate, self.router = layer, pre, post, gate, router
