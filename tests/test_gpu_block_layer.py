@@ -142,3 +142,24 @@ def test_backward_around_a_replayed_forward(weigh):
             assert torch.equal(a, b)
     layer.check()
     layer.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_token(dtype):
+    """A block of one token, trained and decoded: its row is the row of a batch that
+    holds it (the router's product may sum in another order)."""
+    router = (torch.randn((8, 256), generator=gen(31), device=DEV) / 16).to(dtype)
+    block, w1, w2 = block_and_weights(router, T=64, R=1, k=2)
+    h = torch.randn((64, 256), generator=gen(32), device=DEV)
+    many, _, saved = block.forward(h, w1, w2)
+    one, _, single = block.forward(h[5:6].clone(), w1, w2)
+    dec = block.decode(h[5:6].clone(), w1, w2)
+    assert torch.equal(saved[5][2][5], single[5][2][0])
+    # the routing weights differ by fp32 roundings, which may move an e4m3 code by a step
+    rel = lambda a, b: ((a - b).norm() / (b - h[5]).norm()).item()  # noqa: E731
+    assert rel(one[0], many[5]) < 2.0 ** -4 and rel(dec[0], many[5]) < 3 * math.sqrt(4) * 0.026
+    grads = block.backward(torch.ones((1, 256), device=DEV), torch.ones(1, device=DEV), single, w1, w2)
+    assert all(t is None or t.isfinite().all() for t in grads.values())
+    assert grads["router"].dtype is dtype and grads["h"].shape == (1, 256)
+    block.layer.check()
+    block.layer.close()
